@@ -17,9 +17,13 @@ Entry points (same names as the C ABI):
     sdpa_decode(q, k_cache, v_cache, kv_len, ...)   two-phase split-KV decode
     sdpa_decode_paged(q, k_pool, v_pool, page_table, kv_len, ...)   the same over a paged cache
     sdpa_decode_noalloc(q, k_cache, v_cache, kv_len, ...)   the same with library-owned scratch
+    sdpa_cache_write_fp8(k, v, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens)
+                                                quantise new tokens into a paged e4m3 cache
+    sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens, total, ...)   read it back
+    sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, ...)   decode over it
     sdpa_fwd_workspace_size, sdpa_fwd_varlen_workspace_size, sdpa_fwd_int8_workspace_size,
     sdpa_fwd_host_workspace_size,
-    sdpa_decode_workspace_size,
+    sdpa_decode_workspace_size, sdpa_decode_paged_fp8_workspace_size,
     sdpa_check_device_status,
     sdpa_status_string, sdpa_version
 """
@@ -86,6 +90,14 @@ def _load():
         lib.sdpa_decode_workspace_size.restype = sz
         lib.sdpa_decode.argtypes = [p, p, p, p, p, p, i, i, i, i, i, i, p, f, p, sz, i, p]
         lib.sdpa_decode.restype = i
+        lib.sdpa_cache_write_fp8.argtypes = [p] * 9 + [i] * 8 + [p, i, p]
+        lib.sdpa_cache_write_fp8.restype = i
+        lib.sdpa_cache_read_fp8.argtypes = [p] * 8 + [i] * 8 + [p, i, p]
+        lib.sdpa_cache_read_fp8.restype = i
+        lib.sdpa_decode_paged_fp8_workspace_size.argtypes = [i, i, i, i, i]
+        lib.sdpa_decode_paged_fp8_workspace_size.restype = sz
+        lib.sdpa_decode_paged_fp8.argtypes = [p] * 9 + [i] * 8 + [p, f, p, sz, i, p]
+        lib.sdpa_decode_paged_fp8.restype = i
         lib.sdpa_check_device_status.argtypes = [p]
         lib.sdpa_check_device_status.restype = i
         lib.sdpa_status_string.argtypes = [i]
@@ -483,4 +495,126 @@ def sdpa_decode_noalloc(q, k_cache, v_cache, kv_len, *, scale: float | None = No
     rc = fn(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(kv_len), _ptr(out), _ptr(lse), B, Hq, Hkv, max_kv, D, Dv,
             strides, scale, _DT[q.dtype], _stream_ptr(stream))
     _check("sdpa_decode_noalloc", rc)
+    return out, lse
+
+
+def _check_pages(q_rows, page_table):
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (q_rows is not None and
+                                                                      page_table.shape[0] != q_rows):
+        raise ValueError("page_table must be an int32 [B, max_pages] tensor")
+
+
+def _check_fp8_pools(k_pool, v_pool, k_scale, v_scale):
+    """e4m3 pools [n_pages, page_size, Hkv, D | Dv] and their scales [n_pages, Hkv, page_size]."""
+    if k_pool.dim() != 4 or v_pool.dim() != 4 or k_pool.shape[:3] != v_pool.shape[:3]:
+        raise ValueError("the pools must be [n_pages, page_size, Hkv, D | Dv]")
+    if k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn:
+        raise ValueError("the pools must hold float8_e4m3fn codes")
+    n_pages, page_size, Hkv, _ = k_pool.shape
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (n_pages, Hkv, page_size) or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n_pages, Hkv, page_size)}")
+    _on_device(k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale)
+
+
+def sdpa_cache_write_fp8(k, v, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens, *, stream=None):
+    """Quantise new tokens into a paged cache: k [total,Hkv,D], v [total,Hkv,Dv] (fp16/bf16, packed
+    sequences, offsets cu_seqlens int32 [B+1]) become e4m3 codes in the pools [n_pages,page_size,Hkv,D|Dv]
+    and scales [n_pages,Hkv,page_size] fp32 (one power of two per token and head).  kv_len int32 [B] counts
+    each sequence's rows after the call; its new tokens are the last of them.  Writes in place."""
+    if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2]:
+        raise ValueError("k and v must be packed [total, Hkv, D | Dv]")
+    if k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype:
+        raise ValueError("sdpa_cache_write_fp8 takes fp16 or bf16 rows of one type")
+    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    total, Hkv, D = k.shape
+    n_pages, page_size, pool_heads, pool_d = k_pool.shape
+    Dv = v.shape[2]
+    if pool_heads != Hkv or pool_d != D or v_pool.shape[3] != Dv:
+        raise ValueError("the pools' heads and head dims must be those of k and v")
+    _on_device(k=k, v=v, page_table=page_table, kv_len=kv_len, cu_seqlens=cu_seqlens)
+    _int32_vector("kv_len", kv_len)
+    B = kv_len.shape[0]
+    _int32_vector("cu_seqlens", cu_seqlens, B + 1)
+    _check_pages(B, page_table)
+    strides = _i64((*k.stride()[:2], *v.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3],
+                    page_table.stride(0)))
+    rc = _load().sdpa_cache_write_fp8(
+        k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), kv_len.data_ptr(), cu_seqlens.data_ptr(), B, Hkv, total, page_size,
+        page_table.shape[1], n_pages, D, Dv, strides, _DT[k.dtype], _stream_ptr(stream))
+    _check("sdpa_cache_write_fp8", rc)
+
+
+def sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens, total: int, *,
+                        dtype=torch.bfloat16, k_out=None, v_out=None, stream=None):
+    """Read a quantised paged cache back: the first cu_seqlens[b+1] - cu_seqlens[b] rows of each sequence as
+    packed rows, (k [total,Hkv,D], v [total,Hkv,Dv]) in ``dtype`` (fp16 or bf16) or the type of the outputs
+    that are passed."""
+    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    n_pages, page_size, Hkv, D = k_pool.shape
+    Dv = v_pool.shape[3]
+    if k_out is None:
+        k_out = torch.empty((total, Hkv, D), dtype=dtype if v_out is None else v_out.dtype, device=k_pool.device)
+    if v_out is None:
+        v_out = torch.empty((total, Hkv, Dv), dtype=k_out.dtype, device=k_pool.device)
+    if tuple(k_out.shape) != (total, Hkv, D) or tuple(v_out.shape) != (total, Hkv, Dv) or k_out.dtype != v_out.dtype:
+        raise ValueError(f"outputs must be tensors of one type of shapes {(total, Hkv, D)} and {(total, Hkv, Dv)}")
+    if k_out.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("sdpa_cache_read_fp8 writes fp16 or bf16")
+    _on_device(k_out=k_out, v_out=v_out, page_table=page_table, cu_seqlens=cu_seqlens)
+    _int32_vector("cu_seqlens", cu_seqlens)
+    B = cu_seqlens.shape[0] - 1
+    _check_pages(B, page_table)
+    strides = _i64((*k_out.stride()[:2], *v_out.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3],
+                    page_table.stride(0)))
+    rc = _load().sdpa_cache_read_fp8(
+        k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
+        cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, total, page_size, page_table.shape[1],
+        n_pages, D, Dv, strides, _DT[k_out.dtype], _stream_ptr(stream))
+    _check("sdpa_cache_read_fp8", rc)
+    return k_out, v_out
+
+
+def sdpa_decode_paged_fp8_workspace_size(B: int, Hq: int, Hkv: int, max_kv: int, Dv: int) -> int:
+    """Bytes of workspace for sdpa_decode_paged_fp8 (max_kv = max_pages * page_size)."""
+    return int(_load().sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_kv, Dv))
+
+
+def sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, *, scale: float | None = None,
+                          out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """sdpa_decode_paged over a quantised cache: q [B,Hq,D] fp16/bf16, e4m3 pools [n_pages,page_size,Hkv,D|Dv],
+    scales [n_pages,Hkv,page_size] fp32.  Returns (o [B,Hq,Dv] in q's type, lse [B,Hq] fp32 or None)."""
+    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be an fp16 or bf16 [B, Hq, D] tensor")
+    B, Hq, D = q.shape
+    n_pages, page_size, Hkv, pool_d = k_pool.shape
+    Dv = v_pool.shape[3]
+    if pool_d != D:
+        raise ValueError("q and the K pool must share one head dim")
+    _check_pages(B, page_table)
+    max_pages = page_table.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((B, Hq, Dv), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (B, Hq, Dv) or out.dtype != q.dtype:
+        raise ValueError(f"out must be a {q.dtype} tensor of shape {(B, Hq, Dv)}")
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+    elif tuple(lse.shape) != (B, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq)}")
+    if workspace is None:
+        workspace = torch.empty(sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_pages * page_size, Dv),
+                                dtype=torch.uint8, device=q.device)
+    _on_device(q=q, page_table=page_table, kv_len=kv_len, out=out, lse=lse, workspace=workspace)
+    _int32_vector("kv_len", kv_len, B)
+    strides = _i64((*q.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3], *out.stride()[:2],
+                    page_table.stride(0)))
+    rc = _load().sdpa_decode_paged_fp8(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), kv_len.data_ptr(), out.data_ptr(), _ptr(lse), B, Hq, Hkv, page_size, max_pages,
+        n_pages, D, Dv, strides, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _DT[q.dtype], _stream_ptr(stream))
+    _check("sdpa_decode_paged_fp8", rc)
     return out, lse

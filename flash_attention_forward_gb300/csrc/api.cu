@@ -87,13 +87,19 @@ bool encode_bshd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_scales(CUtensorMap* map, const float* base, int n_pages, int Hkv, int page_size, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)n_pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)page_size * 4, (cuuint64_t)page_size * Hkv * 4};
+  const cuuint32_t box[3] = {(cuuint32_t)box_rows, 1u, 1u};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Strides usable by a tensor map / 16-byte vector access: positive multiples of `mult` (a
-// stride of a size-1 dimension only needs the multiple).
-bool stride_ok(int64_t s, int64_t mult) { return s >= 0 && s % mult == 0 && s < (int64_t(1) << 36); }
 
 size_t round16(size_t x) { return (x + 15) & ~size_t(15); }
 
@@ -365,6 +371,7 @@ int decode_check(const void* q, const void* k, const void* v, const int32_t* pag
   p.v_b = st[5], p.v_s = st[6], p.v_h = st[7], p.o_b = st[8], p.o_h = st[9];
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.max_kv = max_kv, p.group = group;
   p.n_splits_max = (max_kv + kDecodeSplit - 1) / kDecodeSplit;
+  p.log2_split = kDecodeLog2Split;
   p.scale2 = (float)((double)scale * 1.4426950408889634);
   if (paged) {
     p.page_table = page_table;

@@ -400,7 +400,7 @@ template <int ELEM>
 __global__ void __launch_bounds__(kDecodeDv) decode_combine_kernel(const DecodeParams p) {
   const int h = blockIdx.x, b = blockIdx.y, dv = threadIdx.x;
   const int L = min(max(__ldg(p.kv_len + b), 0), p.max_kv);
-  const int ns = (L + kDecodeSplit - 1) / kDecodeSplit;
+  const int ns = (L + (1 << p.log2_split) - 1) >> p.log2_split;
   constexpr int kPart = kDecodeDv + 2;  // floats per partial: O, then max, then sum
   constexpr int kGroup = 8;             // partials whose loads are in flight together
   const float* base = p.ws + (int64_t)(b * p.Hq + h) * p.n_splits_max * kPart;
@@ -578,7 +578,10 @@ cudaError_t launch_decode(int elem, int D, const DecodeParams& p, const CUtensor
     e = D == 192 ? launch_split<kBF16, 192>(g1, tk, tv, p, st) : launch_split<kBF16, 128>(g1, tk, tv, p, st);
   else
     e = D == 192 ? launch_split<kF16, 192>(g1, tk, tv, p, st) : launch_split<kF16, 128>(g1, tk, tv, p, st);
-  if (e != cudaSuccess) return e;
+  return e == cudaSuccess ? launch_decode_combine(elem, p, st) : e;
+}
+
+cudaError_t launch_decode_combine(int elem, const DecodeParams& p, cudaStream_t st) {
   // programmatic dependent launch: the combine's CTAs are scheduled while the split grid drains
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -589,8 +592,8 @@ cudaError_t launch_decode(int elem, int D, const DecodeParams& p, const CUtensor
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  e = elem == kBF16 ? cudaLaunchKernelEx(&cfg, decode_combine_kernel<kBF16>, p)
-                    : cudaLaunchKernelEx(&cfg, decode_combine_kernel<kF16>, p);
+  const cudaError_t e = elem == kBF16 ? cudaLaunchKernelEx(&cfg, decode_combine_kernel<kBF16>, p)
+                                      : cudaLaunchKernelEx(&cfg, decode_combine_kernel<kF16>, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }

@@ -155,6 +155,7 @@ struct DecodeParams {
   uint32_t* status;        // device status word
   int64_t q_b, q_h, k_b, k_s, k_h, v_b, v_s, v_h, o_b, o_h;
   int B, Hq, Hkv, max_kv, group, n_splits_max;
+  int log2_split;          // log2 of the keys per split
   float scale2;            // scale * log2(e)
   // paged caches (page_table != null): key row t of sequence b is row t % page_size of physical
   // page page_table[b * pt_b + t / page_size]; k/v then point at pools [n_pages, page_size, Hkv, .]
@@ -165,8 +166,27 @@ struct DecodeParams {
 };
 
 constexpr int kDecodeSplit = 2048;      // keys per phase-1 CTA (1024 measured 7-8% slower)
+constexpr int kDecodeLog2Split = 11;
+static_assert(kDecodeSplit == 1 << kDecodeLog2Split, "split sizes agree");
 constexpr int kDecodeWarps = 4;         // consumer warps: 16 keys of every 64-key chunk each
 constexpr int kDecodeDv = 128;
+
+// Quantised paged cache (e4m3 codes, fp32 scales [n_pages, Hkv, page_size]); see cache.cu.
+constexpr int kCacheMinExp = -80;       // smallest exponent of a written scale
+struct CacheParams {
+  const void *k, *v;       // writer: packed rows [total, Hkv, D | Dv]
+  void *k_out, *v_out;     // reader: the same, written
+  uint8_t *k_pool, *v_pool;
+  float *k_scale, *v_scale;
+  const int32_t* page_table;
+  const int32_t* kv_len;   // writer: rows of each sequence, the packed ones last; reader: null
+  const int32_t* cu;       // [B + 1] packed row offsets
+  uint32_t* status;        // device status word
+  int64_t k_s, k_h, v_s, v_h, kp_p, kp_r, kp_h, vp_p, vp_r, vp_h, pt_b;  // element strides
+  int B, Hkv, rows;        // rows: total * Hkv
+  int log2_page, max_pages, n_pages;
+  FastDiv div_h;           // by Hkv
+};
 
 struct MaskConvertParams {
   const uint16_t* mask;
@@ -213,6 +233,9 @@ cudaError_t launch_prefill_e4m3(int D, int Dv, bool causal, bool has_mask, const
 cudaError_t launch_decode(int elem, int D, const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                           cudaStream_t st);
 
+// Phase 2 of the decode alone (partials in p.ws, 2^p.log2_split keys each).
+cudaError_t launch_decode_combine(int elem, const DecodeParams& p, cudaStream_t st);
+
 // The decode entry points share one validated call description, built without any CUDA call,
 // and one launch path; they differ only in where the per-split partials go.
 struct DecodeCall {
@@ -256,6 +279,18 @@ cudaError_t smem_opt_in(Kernel kern, int bytes, int dev, std::atomic<uint64_t>& 
 // box of box0 x 1 x box_rows x 1 elements; false if the driver rejects it.
 bool encode_bshd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, int B, int S, int H, int Dh,
                  int64_t sb, int64_t ss, int64_t sh, int box0, int box_rows, CUtensorMapSwizzle sw);
+// Tensor map of a quantised cache's scales [n_pages, Hkv, page_size] fp32, contiguous, with a box
+// of box_rows scales of one head and page.
+bool encode_scales(CUtensorMap* map, const float* base, int n_pages, int Hkv, int page_size, int box_rows);
+
+// Argument rules shared by the entry points.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Strides usable by a tensor map / 16-byte vector access: positive multiples of `mult` (a
+// stride of a size-1 dimension only needs the multiple).
+inline bool stride_ok(int64_t s, int64_t mult) { return s >= 0 && s % mult == 0 && s < (int64_t(1) << 36); }
+// Page sizes and counts of a paged cache: 0 or the public status code.
+int page_check(int page_size, int max_pages, int n_pages);
+
 cudaError_t launch_mask_convert(const MaskConvertParams& p, cudaStream_t st);
 cudaError_t launch_varlen_prep(const VarlenPrepParams& p, cudaStream_t st);
 cudaError_t launch_widen(const WidenParams& p, cudaStream_t st);

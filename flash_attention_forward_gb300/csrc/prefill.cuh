@@ -106,21 +106,6 @@ __device__ __forceinline__ uint32_t pack_out(float lo, float hi) {
     return pack_bf16x2(lo, hi);
 }
 
-// Eight e4m3 codes (two 32-bit words) -> eight f16 values (four f16x2 words); exact.
-__device__ __forceinline__ uint4 e4m3x8_to_f16x8(uint2 in) {
-  uint4 out;
-  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
-      "mov.b32 {a, b}, %4;\n\t"
-      "mov.b32 {c, d}, %5;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
-      : "=r"(out.x), "=r"(out.y), "=r"(out.z), "=r"(out.w)
-      : "r"(in.x), "r"(in.y));
-  return out;
-}
-
 // One work unit: two consecutive 128-row query tiles of one (batch, query head) against the
 // key blocks [jb0, jb0 + n_blocks), which is every block the tiles need unless the work tile is
 // split (split >= 0: part `part` of p.split_parts key ranges of split work tile `split`).

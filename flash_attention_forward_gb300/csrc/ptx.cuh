@@ -131,6 +131,14 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
 // 4-D tiled store of one box from shared memory (bulk-group completion; rows outside the tensor
 // are not written).  The source must have been written before a fence.proxy.async.
 __device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, const void* src, int c0, int c1, int c2, int c3) {
@@ -333,6 +341,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// log2(x) on the special-function unit (lg2.approx.ftz.f32): log2(0) = -inf.
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // max(a, b, c) in one instruction.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float d;
@@ -391,5 +406,50 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 // fp32 values of the two halves of a packed bf16x2 word (exact).
 __device__ __forceinline__ float bf16lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi_f32(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Eight e4m3 codes (two 32-bit words) -> eight f16 values (four f16x2 words); exact.
+__device__ __forceinline__ uint4 e4m3x8_to_f16x8(uint2 in) {
+  uint4 out;
+  asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+      "mov.b32 {a, b}, %4;\n\t"
+      "mov.b32 {c, d}, %5;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %3, d;\n\t}"
+      : "=r"(out.x), "=r"(out.y), "=r"(out.z), "=r"(out.w)
+      : "r"(in.x), "r"(in.y));
+  return out;
+}
+
+// Four e4m3 codes -> two f16x2 words, in order; exact.
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t in, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(in));
+}
+
+// Four fp32 values -> e4m3 codes (nearest even, saturating at 448), `a` in the lowest byte.
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+// Powers of two that bring a bf16 row with largest magnitude amax into fp16's range (amax to
+// [2^14, 2^15), so that entries down to 2^-28 of it stay normal) and back.
+__device__ __forceinline__ void q_f16_scale(float amax, float& mul, float& back) {
+  const uint32_t e = min(max(__float_as_uint(amax) >> 23, 15u), 254u);
+  mul = __uint_as_float((268u - e) << 23);
+  back = __uint_as_float((e - 14u) << 23);
+}
 
 }  // namespace sdpa

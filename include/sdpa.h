@@ -30,8 +30,8 @@
  *  - Validation happens before any CUDA call; an invalid call launches nothing.
  *  - The library allocates no device memory in these entry points.  Decode and masked
  *    prefill take a caller workspace sized by the *_workspace_size functions.
- *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_int8, sdpa_decode and
- *    sdpa_decode_paged may be recorded into a CUDA graph (stream capture) once a first call on
+ *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_int8, sdpa_decode, sdpa_decode_paged*
+ *    and sdpa_cache_* may be recorded into a CUDA graph (stream capture) once a first call on
  *    the device has run outside the capture; sdpa_fwd_host may not.
  */
 #ifndef SDPA_GB300_H
@@ -309,6 +309,93 @@ int sdpa_decode_paged(const void* q, const void* k_pool, const void* v_pool, con
                       int n_pages, int D, int Dv, const int64_t* strides, float scale, void* workspace,
                       size_t workspace_bytes, sdpa_dtype dtype, void* stream);
 
+/* Number of int64 entries in the stride array of sdpa_cache_write_fp8 / sdpa_cache_read_fp8. */
+#define SDPA_CACHE_NSTRIDES 11
+
+/*
+ * Quantised paged caches.  A cache is two page pools of FP8 e4m3 codes with one fp32 scale per row
+ * (token and KV head) of each,
+ *
+ *   k_pool [n_pages, page_size, Hkv, D], v_pool [n_pages, page_size, Hkv, Dv]   e4m3 codes
+ *   k_scale, v_scale [n_pages, Hkv, page_size] fp32, contiguous                 value = code * scale
+ *
+ * and a page table as in sdpa_decode_paged: row t of sequence b is row t % page_size of page
+ * page_table[b][t / page_size].  A head's scales of a page lie together, so that an attention
+ * kernel reads those of a block of keys as one run.  The readers take any scales that are positive
+ * and finite.  page_size: a power of two >= 16.  Pool strides: multiples of 16 elements; pools and
+ * scales 16-byte aligned.  Head dims: (D, Dv) in {(64, 64), (128, 128), (192, 128)} unless said otherwise.
+ */
+
+/*
+ * sdpa_cache_write_fp8 -- quantises new tokens' K and V and stores them into their pages.
+ *
+ *   k [total, Hkv, D], v [total, Hkv, Dv]   in_dtype (SDPA_F16 or SDPA_BF16), packed sequences
+ *   cu_seqlens DEVICE int32 [B + 1], non-decreasing: sequence b's new tokens are rows
+ *           cu_seqlens[b] .. cu_seqlens[b+1]-1; rows no sequence owns are skipped
+ *   kv_len  DEVICE int32 [B]: rows of each sequence's cache AFTER the call; its n_b new tokens are
+ *           rows kv_len[b] - n_b .. kv_len[b] - 1.  The attention that follows takes the same array.
+ *   strides: NULL for the contiguous layouts, else 11 element strides {k_s, k_h,  v_s, v_h,
+ *           k_pool page, row, head,  v_pool page, row, head,  page_table row}; those of k and v
+ *           multiples of 8
+ *
+ * The scale of a row is the least power of two 2^k, k >= -80, with amax <= 448 * 2^k, and a code is
+ * x * 2^-k rounded to nearest even: the scaling is exact, so a value is off by at most 2^-4 of
+ * itself (or 2^-10 * scale, where the code is subnormal).  A row of zeros takes 2^-80.  NaN stays NaN and does
+ * not move the scale; a row that holds an infinity takes 2^120, reads back as that infinity there
+ * and as zeros elsewhere.
+ *
+ * A row whose slot lies outside the page table or the pool (a negative position, a page index not in
+ * [0, n_pages)) is not written, and the call raises a status that sdpa_check_device_status()
+ * reports as SDPA_ERR_INVALID.  No two rows of a call may share a slot (a page that several sequences
+ * share is only read).  total * Hkv < 2^30; no workspace; one kernel.
+ */
+int sdpa_cache_write_fp8(const void* k, const void* v, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
+                         const int32_t* page_table, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int Hkv,
+                         int total, int page_size, int max_pages, int n_pages, int D, int Dv, const int64_t* strides,
+                         sdpa_dtype in_dtype, void* stream);
+
+/*
+ * sdpa_cache_read_fp8 -- reads cached rows back as packed 16-bit tensors: rows 0 .. n_b - 1 of each
+ * sequence's cache, n_b = cu_seqlens[b+1] - cu_seqlens[b], become rows cu_seqlens[b] .. of
+ *
+ *   k [total, Hkv, D], v [total, Hkv, Dv]   out_dtype (SDPA_F16 or SDPA_BF16), written
+ *
+ * each code * scale rounded once (exact in bf16 for the scales sdpa_cache_write_fp8 writes).  The
+ * result is what sdpa_fwd_varlen takes.  Rows no sequence owns are left as they are; a row whose slot
+ * lies outside the page table or the pool is written as zeros and reported as in
+ * sdpa_cache_write_fp8.  strides as there.
+ */
+int sdpa_cache_read_fp8(const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
+                        const int32_t* page_table, const int32_t* cu_seqlens, void* k, void* v, int B, int Hkv,
+                        int total, int page_size, int max_pages, int n_pages, int D, int Dv, const int64_t* strides,
+                        sdpa_dtype out_dtype, void* stream);
+
+/*
+ * sdpa_decode_paged_fp8_workspace_size -- bytes of device scratch sdpa_decode_paged_fp8 needs
+ * (per-split partial results; max_kv = max_pages * page_size).  Splits hold 2048 keys, or fewer
+ * (down to 256) where B * Hkv * splits would leave SMs idle.  0 for bad sizes.
+ */
+size_t sdpa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int max_kv, int Dv);
+
+/*
+ * sdpa_decode_paged_fp8 -- sdpa_decode_paged over a quantised cache: one query token per sequence,
+ * K = k_code * k_scale, V = v_code * v_scale.  Both products run on fp16 tensor cores with fp32
+ * accumulation: the codes are exact in fp16, a bf16 query is scaled into fp16 by a power of two per
+ * row, K's scale multiplies the fp32 score and V's scale joins the exponent of the probability, which
+ * is rounded to fp16; the row sum is taken in fp32 of the unrounded probabilities.
+ *
+ *   q [B, Hq, D], o [B, Hq, Dv] in dtype (SDPA_F16 or SDPA_BF16); the pools, scales and page table as above
+ *   strides: NULL or the 11 element strides of sdpa_decode_paged (pool strides multiples of 16)
+ *   workspace: at least sdpa_decode_paged_fp8_workspace_size(...) bytes, 16-byte aligned
+ * (D, Dv) in {(128, 128), (192, 128)}, Hq / Hkv <= 16; kv_len, table entries past a sequence's pages,
+ * lse and the other arguments and limits as in sdpa_decode_paged.
+ */
+int sdpa_decode_paged_fp8(const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                          const float* v_scale, const int32_t* page_table, const int32_t* kv_len, void* o, float* lse,
+                          int B, int Hq, int Hkv, int page_size, int max_pages, int n_pages, int D, int Dv,
+                          const int64_t* strides, float scale, void* workspace, size_t workspace_bytes,
+                          sdpa_dtype dtype, void* stream);
+
 /*
  * sdpa_decode_noalloc -- sdpa_decode for callers that cannot allocate device memory: runtimes
  * without a device allocator of their own, hosts that hand out device memory only through
@@ -335,7 +422,7 @@ int sdpa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
  * sdpa_check_device_status -- synchronizes `stream`, then reports and clears the device
  * status word the kernels raise when a bounded wait inside them gives up (a pipeline
  * stage that never arrived): SDPA_ERR_TIMEOUT in that case, SDPA_ERR_INVALID when a varlen
- * call found bad sequence offsets, SDPA_ERR_CUDA if the synchronization itself failed, else
+ * call found bad sequence offsets or a cache call a row without a slot, SDPA_ERR_CUDA if the synchronization itself failed, else
  * SDPA_OK.  The status word is per device and per
  * process, shared by all streams.
  */

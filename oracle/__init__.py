@@ -240,3 +240,69 @@ def sdpa_decode_paged(q, k_pool, v_pool, page_table, kv_len, *, scale: float, ba
     k = gather_pages(k_pool, page_table, kv_len)
     v = gather_pages(v_pool, page_table, kv_len)
     return sdpa_decode(q, k, v, kv_len, scale=scale, batches=batches, nthreads=nthreads)
+
+
+E4M3_MAX = 448.0
+CACHE_MIN_EXP = -80
+
+
+def quantise_e4m3_rows(x):
+    """e4m3 codes and scales of the rows (last axis) of x, in fp64: scale = 2^k with k the least integer
+    >= CACHE_MIN_EXP for which amax <= 448 * 2^k (NaN entries do not count), code = x / scale rounded to
+    the nearest of e4m3's values, ties to even.  Returns (codes float8_e4m3fn, scales fp32)."""
+    a = as_f64(x)
+    amax = np.where(np.isnan(a), 0.0, np.abs(a)).max(-1)
+    m, e = np.frexp(amax / E4M3_MAX)  # m in [0.5, 1): the least power of two not below is 2^e, or 2^(e - 1) if m = 0.5
+    k = np.where(amax > 0, np.where(m == 0.5, e - 1, e), CACHE_MIN_EXP)
+    k = np.where(np.isinf(amax), 120, np.maximum(k, CACHE_MIN_EXP))
+    with np.errstate(invalid="ignore", over="ignore"):
+        y = np.clip(np.ldexp(a, -k[..., None]), -E4M3_MAX, E4M3_MAX)
+    # e4m3 has 3 bits behind the leading one down to 2^-6, and steps of 2^-9 below
+    exp = np.frexp(np.maximum(np.where(np.isnan(y), 1.0, np.abs(y)), 2.0 ** -6))[1] - 1
+    step = np.ldexp(1.0, exp - 3)
+    codes = np.rint(y / step) * step
+    return (torch.from_numpy(codes).to(torch.float32).to(torch.float8_e4m3fn),
+            torch.from_numpy(np.ldexp(1.0, k)).to(torch.float32))
+
+
+def quantise_pool(pool):
+    """A pool [n_pages, page_size, H, D] as (codes of the same shape, scales [n_pages, H, page_size])."""
+    codes, scales = quantise_e4m3_rows(pool)
+    return codes, scales.transpose(1, 2).contiguous()
+
+
+def dequantise_pool(codes, scales):
+    """fp64 values [n_pages, page_size, H, D] of e4m3 codes and their scales [n_pages, H, page_size]."""
+    return torch.as_tensor(codes).cpu().to(torch.float64) * \
+        torch.as_tensor(scales).cpu().to(torch.float64).transpose(1, 2)[..., None]
+
+
+def sdpa_fwd_paged(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, *, scale: float, causal: bool):
+    """A chunk of new tokens per sequence over a paged cache, in fp64: query i of sequence b (packed row
+    cu_seqlens_q[b] + i of n_b) is position kv_len[b] - n_b + i and sees the keys j < kv_len[b], causal
+    ones only up to its position.  Returns O [total_q, Hq, Dv] and LSE [Hq, total_q], NaN on rows no
+    sequence owns; a query without keys gets O = 0, LSE = -inf."""
+    cq = _offsets(cu_seqlens_q)
+    kvl = [int(x) for x in (kv_len.tolist() if hasattr(kv_len, "tolist") else kv_len)]
+    k, v = as_f64(gather_pages(k_pool, page_table, kvl)), as_f64(gather_pages(v_pool, page_table, kvl))
+    qd = as_f64(q)
+    total, Hq, _ = qd.shape
+    group = Hq // k.shape[2]
+    o = np.full((total, Hq, v.shape[-1]), np.nan)
+    lse = np.full((Hq, total), np.nan)
+    for b in range(len(kvl)):
+        q0, q1 = cq[b], cq[b + 1]
+        n, L = q1 - q0, max(0, min(kvl[b], k.shape[1]))
+        for h in range(Hq):
+            kh, vh = k[b, :L, h // group], v[b, :L, h // group]
+            s = scale * (qd[q0:q1, h] @ kh.T)
+            if causal:
+                pos = kvl[b] - n + np.arange(n)
+                s = np.where(np.arange(L)[None] <= pos[:, None], s, -np.inf)
+            m = np.where(L > 0, s.max(-1, initial=-np.inf), -np.inf)
+            p = np.exp(s - np.where(np.isinf(m), 0.0, m)[:, None])
+            t = p.sum(-1)
+            with np.errstate(divide="ignore", invalid="ignore"):
+                o[q0:q1, h] = np.where(t[:, None] > 0, (p @ vh) / t[:, None], 0.0)
+                lse[h, q0:q1] = np.where(t > 0, m + np.log(t), -np.inf)
+    return o, lse
