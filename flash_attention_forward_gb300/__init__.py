@@ -21,9 +21,13 @@ Entry points (same names as the C ABI):
                                                 quantise new tokens into a paged e4m3 cache
     sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens, total, ...)   read it back
     sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, ...)   decode over it
+    sdpa_fwd_paged(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q, ...)
+                                                a chunk of new tokens per sequence over a paged cache
+    sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens_q,
+                       max_seqlen_q, ...)       the same over a quantised cache
     sdpa_fwd_workspace_size, sdpa_fwd_varlen_workspace_size, sdpa_fwd_int8_workspace_size,
     sdpa_fwd_host_workspace_size,
-    sdpa_decode_workspace_size, sdpa_decode_paged_fp8_workspace_size,
+    sdpa_decode_workspace_size, sdpa_decode_paged_fp8_workspace_size, sdpa_fwd_paged_workspace_size,
     sdpa_check_device_status,
     sdpa_status_string, sdpa_version
 """
@@ -98,6 +102,12 @@ def _load():
         lib.sdpa_decode_paged_fp8_workspace_size.restype = sz
         lib.sdpa_decode_paged_fp8.argtypes = [p] * 9 + [i] * 8 + [p, f, p, sz, i, p]
         lib.sdpa_decode_paged_fp8.restype = i
+        lib.sdpa_fwd_paged_workspace_size.argtypes = [i, i, i, i, i, i, i]
+        lib.sdpa_fwd_paged_workspace_size.restype = sz
+        lib.sdpa_fwd_paged.argtypes = [p] * 8 + [i] * 10 + [p, f, i, p, sz, i, p]
+        lib.sdpa_fwd_paged.restype = i
+        lib.sdpa_fwd_paged_fp8.argtypes = [p] * 10 + [i] * 10 + [p, f, i, p, sz, i, p]
+        lib.sdpa_fwd_paged_fp8.restype = i
         lib.sdpa_check_device_status.argtypes = [p]
         lib.sdpa_check_device_status.restype = i
         lib.sdpa_status_string.argtypes = [i]
@@ -617,4 +627,86 @@ def sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_le
         n_pages, D, Dv, strides, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         _DT[q.dtype], _stream_ptr(stream))
     _check("sdpa_decode_paged_fp8", rc)
+    return out, lse
+
+
+def sdpa_fwd_paged_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_q: int, max_kv: int,
+                                  Dv: int) -> int:
+    """Bytes of workspace for sdpa_fwd_paged and sdpa_fwd_paged_fp8: the work plan (required), then
+    partial results of cut key ranges (optional)."""
+    return int(_load().sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_kv, Dv))
+
+
+def _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q, scale, out, lse, return_lse,
+                    workspace):
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be a packed fp16 or bf16 [total_q, Hq, D] tensor")
+    total_q, Hq, D = q.shape
+    n_pages, page_size, Hkv, pool_d = k_pool.shape
+    Dv = v_pool.shape[3]
+    if pool_d != D:
+        raise ValueError("q and the K pool must share one head dim")
+    _int32_vector("kv_len", kv_len)
+    B = kv_len.shape[0]
+    _int32_vector("cu_seqlens_q", cu_seqlens_q, B + 1)
+    _check_pages(B, page_table)
+    max_pages = page_table.shape[1]
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    if out is None:
+        out = torch.empty((total_q, Hq, Dv), dtype=q.dtype, device=q.device)
+    elif tuple(out.shape) != (total_q, Hq, Dv) or out.dtype != q.dtype:
+        raise ValueError(f"out must be a {q.dtype} tensor of shape {(total_q, Hq, Dv)}")
+    if lse is None:
+        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if return_lse else None
+    elif tuple(lse.shape) != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(Hq, total_q)}")
+    max_seqlen_q = int(max_seqlen_q)
+    if workspace is None:
+        need = sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_pages * page_size, Dv)
+        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+    _on_device(q=q, page_table=page_table, kv_len=kv_len, cu_seqlens_q=cu_seqlens_q, out=out, lse=lse,
+               workspace=workspace)
+    strides = _i64((*q.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3], *out.stride()[:2],
+                    page_table.stride(0)))
+    sizes = (B, Hq, Hkv, total_q, max_seqlen_q, page_size, max_pages, n_pages, D, Dv, strides, scale)
+    return out, lse, workspace, sizes
+
+
+def sdpa_fwd_paged(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q: int, *,
+                   scale: float | None = None, causal: bool = False, out=None, lse=None, return_lse: bool = True,
+                   workspace=None, stream=None):
+    """A chunk of new tokens per sequence over a paged cache that holds them: q [total_q,Hq,D] (fp16/bf16,
+    packed, offsets cu_seqlens_q int32 [B+1], at most max_seqlen_q tokens each), pools
+    [n_pages,page_size,Hkv,D|Dv], page_table int32 [B,max_pages], kv_len int32 [B] counting the new tokens.
+    Causal masking is bottom-right: token i of n is position kv_len - n + i.  Returns (o [total_q,Hq,Dv],
+    lse [Hq,total_q] fp32 or None)."""
+    if k_pool.dim() != 4 or v_pool.dim() != 4 or k_pool.shape[:3] != v_pool.shape[:3]:
+        raise ValueError("the pools must be [n_pages, page_size, Hkv, D | Dv]")
+    if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
+        raise ValueError("q and the pools must share one dtype (use sdpa_fwd_paged_fp8 for e4m3 pools)")
+    out, lse, workspace, sizes = _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q,
+                                                 scale, out, lse, return_lse, workspace)
+    _on_device(k_pool=k_pool, v_pool=v_pool)
+    rc = _load().sdpa_fwd_paged(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
+        cu_seqlens_q.data_ptr(), out.data_ptr(), _ptr(lse), *sizes, int(bool(causal)), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _DT[q.dtype], _stream_ptr(stream))
+    _check("sdpa_fwd_paged", rc)
+    return out, lse
+
+
+def sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens_q, max_seqlen_q: int, *,
+                       scale: float | None = None, causal: bool = False, out=None, lse=None, return_lse: bool = True,
+                       workspace=None, stream=None):
+    """sdpa_fwd_paged over a quantised cache: e4m3 pools and scales [n_pages,Hkv,page_size] fp32; q and o in
+    fp16 or bf16."""
+    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    out, lse, workspace, sizes = _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q,
+                                                 scale, out, lse, return_lse, workspace)
+    rc = _load().sdpa_fwd_paged_fp8(
+        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        page_table.data_ptr(), kv_len.data_ptr(), cu_seqlens_q.data_ptr(), out.data_ptr(), _ptr(lse), *sizes,
+        int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _DT[q.dtype],
+        _stream_ptr(stream))
+    _check("sdpa_fwd_paged_fp8", rc)
     return out, lse

@@ -87,17 +87,24 @@ bool encode_bshd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool encode_scales(CUtensorMap* map, const float* base, int n_pages, int Hkv, int page_size, int box_rows) {
+bool encode_tiled3(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, int d0, int d1, int d2,
+                   int64_t s1, int64_t s2, int box0, int box1, int box2, CUtensorMapSwizzle sw) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
-  const cuuint64_t dims[3] = {(cuuint64_t)page_size, (cuuint64_t)Hkv, (cuuint64_t)n_pages};
-  const cuuint64_t strides[2] = {(cuuint64_t)page_size * 4, (cuuint64_t)page_size * Hkv * 4};
-  const cuuint32_t box[3] = {(cuuint32_t)box_rows, 1u, 1u};
+  const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
+  const cuuint64_t strides[2] = {(cuuint64_t)(s1 * esize), (cuuint64_t)(s2 * esize)};
+  const cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, (cuuint32_t)box2};
   const cuuint32_t estr[3] = {1u, 1u, 1u};
-  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+bool encode_scales(CUtensorMap* map, const float* base, int n_pages, int Hkv, int page_size, int box_rows) {
+  return encode_tiled3(map, base, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, page_size, Hkv, n_pages, page_size,
+                       (int64_t)page_size * Hkv, box_rows, 1, 1, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+int take_stall_flag() { return g_stall_next.exchange(0); }
 
 namespace {
 
@@ -267,7 +274,7 @@ int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse,
   p.inv_scale = (float)(1.0 / s_eff);
   p.out_scale = descale_v;
   p.status = status;
-  p.stall_first_stage = g_stall_next.exchange(0);
+  p.stall_first_stage = take_stall_flag();
   p.n_full = (int)(n_items - sp.tail);
   p.split_tail = sp.tail;
   p.split_parts = sp.parts;

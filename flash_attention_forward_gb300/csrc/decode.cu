@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kDecodeDv) decode_combine_kernel(const DecodeP
   for (int s0 = 0; s0 < ns; s0 += kGroup) {
     float m[kGroup];
 #pragma unroll
-    for (int i = 0; i < kGroup; ++i) m[i] = (s0 + i < ns) ? __ldg(base + (s0 + i) * kPart + kDecodeDv) : -INFINITY;
+    for (int i = 0; i < kGroup; ++i) m[i] = (s0 + i < ns) ? ld_dep(base + (s0 + i) * kPart + kDecodeDv) : -INFINITY;
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) M = fmaxf(M, m[i]);
   }
@@ -420,9 +420,9 @@ __global__ void __launch_bounds__(kDecodeDv) decode_combine_kernel(const DecodeP
     for (int i = 0; i < kGroup; ++i) {
       const bool in = s0 + i < ns;
       const float* part = base + (s0 + i) * kPart;
-      m[i] = in ? __ldg(part + kDecodeDv) : -INFINITY;
-      x[i] = in ? __ldg(part + dv) : 0.f;
-      l[i] = in ? __ldg(part + kDecodeDv + 1) : 0.f;
+      m[i] = in ? ld_dep(part + kDecodeDv) : -INFINITY;
+      x[i] = in ? ld_dep(part + dv) : 0.f;
+      l[i] = in ? ld_dep(part + kDecodeDv + 1) : 0.f;
     }
 #pragma unroll
     for (int i = 0; i < kGroup; ++i) {  // splits in order, as a sequential loop would take them

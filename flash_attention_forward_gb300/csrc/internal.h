@@ -279,6 +279,11 @@ cudaError_t smem_opt_in(Kernel kern, int bytes, int dev, std::atomic<uint64_t>& 
 // box of box0 x 1 x box_rows x 1 elements; false if the driver rejects it.
 bool encode_bshd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, int B, int S, int H, int Dh,
                  int64_t sb, int64_t ss, int64_t sh, int box0, int box_rows, CUtensorMapSwizzle sw);
+// Tensor map of a 3-D tensor [d2, d1, d0] (element strides s2, s1, innermost 1).
+bool encode_tiled3(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int esize, int d0, int d1, int d2,
+                   int64_t s1, int64_t s2, int box0, int box1, int box2, CUtensorMapSwizzle sw);
+// Takes the one-shot flag of sdpa_debug_stall_next_call.
+int take_stall_flag();
 // Tensor map of a quantised cache's scales [n_pages, Hkv, page_size] fp32, contiguous, with a box
 // of box_rows scales of one head and page.
 bool encode_scales(CUtensorMap* map, const float* base, int n_pages, int Hkv, int page_size, int box_rows);

@@ -1,0 +1,798 @@
+// Attention of a chunk of new tokens per sequence over a paged cache (16-bit pages, or e4m3 pages
+// with one scale per row), for sm_103a: TMA by page table -> shared-memory ring -> tcgen05 MMAs with
+// accumulators in tensor memory -> blocked online softmax -> P.V, warp-specialised.
+//
+// The mathematics is that of the prefill kernels (running row max, lazily rescaled O, fp32 row sums).
+// What the paged cache and the chunk change:
+//   * a query tile's 128 rows are (token, head) pairs: the G query heads of a KV head ride in one
+//     tile, tok_tile = 128 / G tokens high, so a short chunk still fills the rows and every K/V byte
+//     serves all heads of its group.  One TMA box [tok_tile tokens, G heads, 64 columns] loads a chunk of columns;
+//   * the keys of a 128-key block come in boxes of min(128, page_size) rows, one page each, issued
+//     by the lanes of the producer warp side by side; pages past the cache read as zeros;
+//   * rows of the last page past kv_len may hold anything: their scores are masked, and their V rows
+//     are zeroed in shared memory before the P.V product (0 * NaN would poison it);
+//   * the key range of long sequences is cut into segments so that few query rows still occupy every
+//     SM; segments write partials (unnormalised O, max, sum) that a second kernel merges.  The cut
+//     is planned on the device, where the lengths are (paged_plan_kernel).
+// K and V take turns in one ring of equal slots: item 2 j is K(j), item 2 j + 1 is V(j).
+//
+// Quantised pages.  Every e4m3 value is exact in fp16, so four converter warps turn a block's codes
+// into fp16 operands (one thread per row) and both products are fp16, whatever the query's type:
+//   * K' = code * (k_scale / 2^ek), 2^(ek + 6) the power of two of the block's largest scale: the
+//     largest row lies just below fp16's largest value, rows of power-of-two scales stay exact down
+//     to 2^-21 of the largest scale and lose a bit for each one below (K' is read as 0 under
+//     2^-30).  The block's scores are multiplied by 2^ek;
+//   * V' likewise with ev, and 2^ev joins the exponent: with y = s + ev the running maximum is taken
+//     over y, P = 2^(y - m) meets V', and the row sum takes 2^-ev of the block's sum.  P stays in
+//     fp16's best range whatever the scales are;
+//   * a bf16 query is brought into fp16's range by a power of two per row.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace sdpa {
+
+constexpr float kPagedRescaleLog2 = 8.0f;
+constexpr float kPagedLn2 = 0.6931471805599453f;
+constexpr int kMinBlockExp = -100;  // exponent floor of a block's scales: 2^100 * sums stays finite
+constexpr int kBlockExpRoom = 6;    // codes reach 448 < 2^9, fp16 65504: six powers of two to spare
+constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn masked scores into NaN
+constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
+constexpr int kExpRing = 16;        // blocks whose exponents are kept: more than the ring can run ahead
+
+template <bool QUANT, int D, int DV>
+struct PagedCfg {
+  static constexpr int NCH_D = D / 64, NCH_V = DV / 64;
+  static constexpr int Q_BYTES = kBlockQ * D * 2;
+  static constexpr int K_BYTES = kBlockK * D * 2;
+  static constexpr int V_BYTES = kBlockK * DV * 2;
+  static constexpr int SLOT = K_BYTES > V_BYTES ? K_BYTES : V_BYTES;
+  static constexpr int SLOTS = D == 64 ? (QUANT ? 6 : 8) : D == 128 ? (QUANT ? 3 : 5) : 2;
+  // raw codes: boxes of 128 (or 64) codes a row
+  static constexpr int KW = D % 128 == 0 ? 128 : 64, VW = DV % 128 == 0 ? 128 : 64;
+  static constexpr int RAW = QUANT ? kBlockK * D : 0;
+  static constexpr int RAWS = !QUANT ? 0 : D == 64 ? 8 : D == 128 ? 4 : 1;
+  static constexpr int QK_STEPS = D / 16, PV_STEPS = kBlockK / 16;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_SLOT = OFF_Q + kTilesPerCta * Q_BYTES;
+  static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
+  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+  static constexpr int OFF_EXP = OFF_BAR + 512;                     // int2 [kExpRing]
+  static constexpr int OFF_QEXP = OFF_EXP + kExpRing * 8;           // int8 [2 tiles][2][128]
+  static constexpr int SMEM = OFF_QEXP + (QUANT ? 512 : 0) + 1024;  // 1 KB of slack for the alignment
+  // warpgroups: control (producer, MMA, helpers), converters (quantised), two softmax
+  static constexpr int THREADS = QUANT ? 512 : 384;
+  static constexpr int SOFTMAX_WARP = QUANT ? 8 : 4;
+  // registers per thread; the sums must stay within what the block is launched with
+  static constexpr uint32_t REGS_CONTROL = QUANT ? 64 : 96;
+  static constexpr uint32_t REGS_CONVERT = 64;
+  static constexpr uint32_t REGS_SOFTMAX = QUANT ? 192 : 200;
+  static constexpr uint32_t REGS_LAUNCH = QUANT ? 128 : 168;
+  static_assert(128 * REGS_CONTROL + (QUANT ? 128 * REGS_CONVERT : 0) + 256 * REGS_SOFTMAX <= THREADS * REGS_LAUNCH,
+                "register split exceeds the launch");
+  static_assert(SMEM <= 227 * 1024, "more shared memory than a CTA may opt in to");
+  static_assert(Q_BYTES % 1024 == 0 && SLOT % 1024 == 0 && RAW % 1024 == 0, "1 KB tile alignment");
+};
+
+// One work unit: two query tiles (2 * tok_tile tokens of one sequence, the G heads of one KV head)
+// against the key blocks [jb0, jb0 + n_blocks) of segment `seg`.
+struct PagedUnit {
+  int b, kvh, tok0;
+  int n_t[kTilesPerCta];
+  int n_blocks, jb0;
+  int slot;                // partial slot, or -1: the unit stores O itself
+  int q_off, n, len, sk;
+};
+
+__device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, int unit) {
+  PagedUnit w;
+  const int32_t* prefix = p.plan + kPlanHeader;
+  const int seg_blocks = ld_dep(p.plan + kPlanSeg);
+  int lo = 0, hi = p.B;  // prefix[lo] <= unit < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (ld_dep(prefix + mid) <= unit) lo = mid; else hi = mid;
+  }
+  w.b = lo;
+  w.q_off = __ldg(p.cu_q + lo);
+  w.n = __ldg(p.cu_q + lo + 1) - w.q_off;
+  w.len = __ldg(p.kv_len + lo);
+  w.sk = min(max(w.len, 0), p.max_kv);
+  // local order: segment, work tile (longest first), KV head.  The SMs that run at one time then
+  // stream the same keys for different tiles, which L2 serves.
+  const int local = unit - ld_dep(prefix + lo);
+  const int rest = static_cast<int>(fast_div(static_cast<uint32_t>(local), p.div_hkv));
+  w.kvh = local - rest * p.Hkv;
+  const int tok_unit = kTilesPerCta * p.tok_tile;
+  const int tiles = (w.n + tok_unit - 1) / tok_unit;
+  const int seg = rest / tiles;
+  const int rank = rest - seg * tiles;
+  const int tile = tiles - 1 - rank;
+  w.tok0 = tile * tok_unit;
+  w.jb0 = seg * seg_blocks;
+  w.n_blocks = 0;
+#pragma unroll
+  for (int t = 0; t < kTilesPerCta; ++t) {
+    const int blocks = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, tile * kTilesPerCta + t);
+    w.n_t[t] = min(max(blocks - w.jb0, 0), seg_blocks);
+    w.n_blocks = max(w.n_blocks, w.n_t[t]);
+  }
+  const int32_t* slots = prefix + p.B + 1;
+  const int s0 = ld_dep(slots + lo);
+  w.slot = ld_dep(slots + lo + 1) > s0 ? s0 + local : -1;
+  return w;
+}
+
+// The k-th unit of this CTA: snake order over the longest-first list.
+__device__ __forceinline__ int paged_nth(int k) {
+  const int G = gridDim.x;
+  return (k & 1) ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Converts row r of a raw tile (boxes of W codes a row, swizzled) into the 128-byte-swizzled fp16
+// chunks of 64 columns that the MMAs read, times the pair factor f.
+template <int COLS, int W>
+__device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int r, uint32_t f) {
+  const int x = r & 7;
+#pragma unroll
+  for (int u = 0; u < COLS / 16; ++u) {  // 16 codes
+    const int box = u / (W / 16), uu = u % (W / 16);
+    const int sw = W == 128 ? (uu ^ x) : (uu ^ ((r >> 1) & 3));
+    const uint4 c = *reinterpret_cast<const uint4*>(raw + box * kBlockK * W + r * W + (sw << 4));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e4m3x4_to_f16x4(w[i], h[2 * i], h[2 * i + 1]);
+      h[2 * i] = mul_f16x2(h[2 * i], f);
+      h[2 * i + 1] = mul_f16x2(h[2 * i + 1], f);
+    }
+    uint8_t* d = dst + (u / 4) * kBlockK * 128 + r * 128;
+    const int v = 2 * (u % 4);
+    *reinterpret_cast<uint4*>(d + ((v ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(d + (((v + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+  }
+}
+
+// Barriers (phases continue from unit to unit):
+//   q_full[t] / q_empty[t]: Q tile t landed / its last QK MMA finished
+//   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
+//   full[s] / empty[s]    : ring slot s holds its item / the MMAs that read it finished
+//   raw_full / raw_empty  : quantised pages: codes landed / read by the converters
+//   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
+//                           then zeroes those rows and completes full[s] in the copy's place
+//   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels
+template <bool BF16, bool QUANT, int D, int DV>
+__global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
+    paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+  using C = PagedCfg<QUANT, D, DV>;
+  constexpr int NS = C::SLOTS;
+  constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
+  constexpr bool CONVERT_Q = QUANT && BF16;
+  constexpr bool F16_MATH = QUANT || !BF16;
+  extern __shared__ uint8_t paged_smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sKV = smem + C::OFF_SLOT;
+  uint8_t* sRaw = smem + C::OFF_RAW;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* q_full = bars;              // [2]
+  uint64_t* q_empty = q_full + 2;       // [2]
+  uint64_t* q_ready = q_empty + 2;      // [2]
+  uint64_t* s_full = q_ready + 2;       // [2]
+  uint64_t* p_half = s_full + 2;        // [2]
+  uint64_t* p_full = p_half + 2;        // [2]
+  uint64_t* o_full = p_full + 2;        // [2]
+  uint64_t* o_empty = o_full + 2;       // [2]
+  uint64_t* mma_done = o_empty + 2;     // [1]
+  uint64_t* v_ragged = mma_done + 1;     // [kFixRing]
+  uint64_t* full = v_ragged + kFixRing;  // [NS]
+  uint64_t* empty = full + NS;          // [NS]
+  uint64_t* raw_full = empty + NS;      // [NR]
+  uint64_t* raw_empty = raw_full + NR;  // [NR]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + NR);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int2* blk_exp = reinterpret_cast<int2*>(smem + C::OFF_EXP);
+  int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
+  static_assert((17 + kFixRing + 2 * NS + 2 * NR) * 8 + 8 <= 512, "barriers fit their area");
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5;
+  const int lane = tid & 31;
+  pdl_launch_dependents();  // the combine may be scheduled early; it waits for this grid
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&q_full[t], 1);
+      mbar_init(&q_empty[t], 1);
+      mbar_init(&q_ready[t], 128);
+      mbar_init(&s_full[t], 1);
+      mbar_init(&p_half[t], 128);
+      mbar_init(&p_full[t], 128);
+      mbar_init(&o_full[t], 1);
+      mbar_init(&o_empty[t], 128);
+    }
+    mbar_init(mma_done, 1);
+    for (int s = 0; s < kFixRing; ++s) mbar_init(&v_ragged[s], 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(&full[s], QUANT ? 128 : 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < NR; ++s) {
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_empty[s], 128);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  pdl_wait();  // the plan comes from the kernel launched before
+  const int n_units = ld_dep(p.plan + kPlanUnits);
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ TMA producer (one warp)
+    regs_dec<C::REGS_CONTROL>();
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const int rows = min(kBlockK, p.page_size);  // rows per box
+    const int nsub = kBlockK / rows;             // boxes per column chunk: 1 .. 8
+    constexpr int KPARTS = QUANT ? D / C::KW : C::NCH_D, VPARTS = QUANT ? DV / C::VW : C::NCH_V;
+    constexpr int KCOLS = QUANT ? C::KW : 64, VCOLS = QUANT ? C::VW : 64;    // columns per box
+    constexpr int KROW = QUANT ? C::KW : 128, VROW = QUANT ? C::VW : 128;    // bytes of a box row
+    constexpr int KTX = QUANT ? kBlockK * D : C::K_BYTES, VTX = QUANT ? kBlockK * DV : C::V_BYTES;
+    constexpr int NL = QUANT ? NR : NS;          // ring that TMA fills
+    uint64_t* ld_full = QUANT ? raw_full : full;
+    uint64_t* ld_empty = QUANT ? raw_empty : empty;
+    const int q_tx = p.tok_tile * p.group * D * 2;
+    int qn[2] = {0, 0};
+    int g = 0, nr = 0;  // items, and ragged V blocks, issued
+    bool ok = true;
+    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
+      const PagedUnit w = paged_unit(p, item);
+      if (w.n_blocks == 0) continue;  // a segment past its tile's keys: skipped by every role
+      for (int t = 0; t < kTilesPerCta && ok; ++t) {
+        if (w.n_t[t] == 0) continue;
+        if (qn[t] > 0 && !mbar_wait_warp(&q_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&q_full[t], q_tx);
+          for (int c = 0; c < C::NCH_D; ++c)
+            tma_load_3d(sQ + t * C::Q_BYTES + c * kBlockQ * 128, &tm_q, &q_full[t], c * 64, w.kvh * p.group,
+                        w.q_off + w.tok0 + t * p.tok_tile);
+        }
+        ++qn[t];
+      }
+      const int32_t* table = p.page_table + w.b * p.pt_b;
+      const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
+      const int sub = lane & 7;                                  // page of the block: lane % 8 < nsub
+      for (int j = 0; ok && j < w.n_blocks; ++j) {
+        const int key = (w.jb0 + j) * kBlockK + sub * rows;
+        const int lp = key >> p.log2_page, prow = key & (p.page_size - 1);
+        int phys = p.n_pages;  // outside the pool: zeros
+        if (sub < nsub && lp < used) phys = __ldg(table + lp);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+          const int s = g % NL, r = g / NL;
+          if (r > 0 && !mbar_wait_warp(&ld_empty[s], (r - 1) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (p.stall_first_stage && g == 0) continue;  // test hook: slot 0 never fills
+          uint64_t* bar = &ld_full[s];
+          if (!QUANT && kv == 1 && (w.jb0 + j + 1) * kBlockK > w.sk) {
+            bar = &v_ragged[nr % kFixRing];
+            ++nr;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(bar, kv == 0 ? KTX : VTX);
+          __syncwarp();
+          uint8_t* dst = QUANT ? sRaw + s * C::RAW : sKV + s * C::SLOT;
+          const int parts = kv == 0 ? KPARTS : VPARTS, row_b = kv == 0 ? KROW : VROW;
+          const int part = lane >> 3;  // column chunk
+          if (sub < nsub && part < parts)
+            tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, kv == 0 ? &tm_k : &tm_v, bar,
+                        part * (kv == 0 ? KCOLS : VCOLS), w.kvh, prow, phys);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      // let every copy already in flight land before the CTA's shared memory goes away
+      for (int t = 0; t < kTilesPerCta; ++t)
+        if (qn[t] > 0) mbar_drain(&q_full[t], (qn[t] - 1) & 1);
+      for (int j = max(0, nr - kFixRing); j < nr; ++j) mbar_drain(&v_ragged[j % kFixRing], (j / kFixRing) & 1);
+      for (int j = max(0, g - NL); j < g; ++j) mbar_drain(&ld_full[j % NL], (j / NL) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (one thread)
+    regs_dec<C::REGS_CONTROL>();
+    if (lane == 0) {
+      constexpr uint32_t fmt = F16_MATH ? 0 : 1;
+      constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, 0, 0, kBlockQ, kBlockK);
+      constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, 0, 1, kBlockQ, DV);
+      const uint64_t dq0 = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+      const uint64_t dk0 = make_smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
+      const uint64_t dv0 = make_smem_desc(smem_u32(sKV), kBlockK * 128, 1024, kSwizzle128B);
+      const uint32_t q_lo = static_cast<uint32_t>(dq0), q_hi = static_cast<uint32_t>(dq0 >> 32);
+      const uint32_t k_lo = static_cast<uint32_t>(dk0), k_hi = static_cast<uint32_t>(dk0 >> 32);
+      const uint32_t v_lo = static_cast<uint32_t>(dv0), v_hi = static_cast<uint32_t>(dv0 >> 32);
+      int qn[2] = {0, 0}, pn[2] = {0, 0};
+      int g = 0;       // items consumed before this unit
+      bool ok = true;
+      for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
+        const PagedUnit w = paged_unit(p, item);
+        if (w.n_blocks == 0) continue;
+        for (int t = 0; t < kTilesPerCta && ok; ++t)
+          if (w.n_t[t] > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[t] : &q_full[t], qn[t] & 1, abort_flag, p.status);
+        for (int j = 0; ok && j <= w.n_blocks; ++j) {
+          const int gk = g + 2 * j, gv = gk - 1;
+          const int sk = gk % NS, sv = (gv + NS) % NS;
+          bool v_in = false, k_in = false;  // waited for in this step
+          for (int t = 0; t < kTilesPerCta && ok; ++t) {
+            const uint32_t tS = tmem_base + t * 128;
+            const uint32_t tO = tmem_base + 256 + t * 128;
+            if (j >= 1 && j - 1 < w.n_t[t]) {
+              // O_t += P_t(j-1) V(j-1)
+              if (!v_in) {
+                if (!mbar_wait(&full[sv], (gv / NS) & 1, abort_flag, p.status)) {
+                  ok = false;
+                  break;
+                }
+                v_in = true;
+              }
+              if (j == 1 && qn[t] > 0 && !mbar_wait(&o_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+              }
+              const uint32_t dv = v_lo + static_cast<uint32_t>((sv * C::SLOT) >> 4);
+              const uint32_t acc0 = (j - 1 > 0) ? 1u : 0u;
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                if (!mbar_wait(h == 0 ? &p_half[t] : &p_full[t], pn[t] & 1, abort_flag, p.status)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int kk = h * C::PV_STEPS / 2; kk < (h + 1) * C::PV_STEPS / 2; ++kk)
+                  mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv,
+                             kk > 0 ? 1u : acc0);
+              }
+              if (!ok) break;
+              if (j == w.n_t[t]) mma_commit(&o_full[t]);
+              ++pn[t];
+            }
+            if (t == kTilesPerCta - 1 && j >= 1) mma_commit(&empty[sv]);
+            if (j < w.n_t[t]) {
+              // S_t = Q_t K(j)^T
+              if (!k_in) {
+                if (!mbar_wait(&full[sk], (gk / NS) & 1, abort_flag, p.status)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                k_in = true;
+              }
+              const uint32_t dq = q_lo + static_cast<uint32_t>((t * C::Q_BYTES) >> 4);
+              const uint32_t dk = k_lo + static_cast<uint32_t>((sk * C::SLOT) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+                const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
+                mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&s_full[t]);
+              if (j == w.n_t[t] - 1) mma_commit(&q_empty[t]);
+            }
+          }
+          if (ok && j < w.n_blocks) mma_commit(&empty[sk]);
+        }
+        g += 2 * w.n_blocks;
+        for (int t = 0; t < kTilesPerCta; ++t)
+          if (w.n_t[t] > 0) ++qn[t];
+      }
+      // every MMA issued so far has finished before tensor memory is released
+      mma_commit(mma_done);
+      mbar_drain(mma_done, 0);
+    }
+  } else if (warp < 4) {
+    regs_dec<C::REGS_CONTROL>();
+    if constexpr (!QUANT) {
+      // ---------------------------------------------------------- V rows past kv_len -> 0 (one warp)
+      if (warp == 2) {
+        int g = 0, nr = 0;
+        for (int k = 0, item = paged_nth(0); item < n_units; item = paged_nth(++k)) {
+          const PagedUnit w = paged_unit(p, item);
+          if (w.n_blocks == 0) continue;
+          const int last = w.n_blocks - 1;  // only a unit's last block can end past kv_len
+          const int live = w.sk - (w.jb0 + last) * kBlockK;
+          if (live < kBlockK) {
+            const int s = (g + 2 * last + 1) % NS;
+            if (!mbar_wait_warp(&v_ragged[nr % kFixRing], (nr / kFixRing) & 1, abort_flag, p.status)) break;
+            ++nr;
+            uint8_t* v = sKV + s * C::SLOT;
+            // whole 128-byte rows of every column chunk: the swizzle stays inside a row
+            for (int u = lane + max(live, 0) * 8; u < kBlockK * 8; u += 32)
+#pragma unroll
+              for (int c = 0; c < C::NCH_V; ++c)
+                *reinterpret_cast<uint4*>(v + c * kBlockK * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+          }
+          g += 2 * w.n_blocks;
+        }
+      }
+    }
+  } else if (QUANT && warp < 8) {
+    // ------------------------------------------------------------ converters: codes -> fp16 operands
+    regs_dec<C::REGS_CONVERT>();
+    const int row = tid - 128;  // tile row of this thread
+    int qn[2] = {0, 0};
+    int g = 0, blk = 0;
+    bool ok = true;
+    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
+      const PagedUnit w = paged_unit(p, item);
+      if (w.n_blocks == 0) continue;
+      if constexpr (CONVERT_Q) {
+        for (int t = 0; t < kTilesPerCta && ok; ++t) {
+          if (w.n_t[t] == 0) continue;
+          if (!mbar_wait_warp(&q_full[t], qn[t] & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* q = sQ + t * C::Q_BYTES + row * 128;
+          float amax = 0.f;
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            const uint4 v = *reinterpret_cast<const uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_f32(x[i])), fabsf(bf16hi_f32(x[i]))));
+          }
+          float mul, back;
+          q_f16_scale(amax, mul, back);
+#pragma unroll 4
+          for (int u = 0; u < D / 8; ++u) {
+            uint4* ptr = reinterpret_cast<uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
+            const uint4 v = *ptr;
+            *ptr = make_uint4(pack_f16x2(bf16lo_f32(v.x) * mul, bf16hi_f32(v.x) * mul),
+                              pack_f16x2(bf16lo_f32(v.y) * mul, bf16hi_f32(v.y) * mul),
+                              pack_f16x2(bf16lo_f32(v.z) * mul, bf16hi_f32(v.z) * mul),
+                              pack_f16x2(bf16lo_f32(v.w) * mul, bf16hi_f32(v.w) * mul));
+          }
+          // exponent of `back`, in [-126, 113]; two buffers, as the next unit's tile may be converted
+          // before this one's softmax has begun
+          q_exp[(t * 2 + (qn[t] & 1)) * 128 + row] =
+              static_cast<int8_t>(static_cast<int>(__float_as_uint(back) >> 23) - 127);
+          fence_proxy_async_smem();
+          mbar_arrive(&q_ready[t]);
+          ++qn[t];
+        }
+        if (!ok) break;
+      }
+      const int32_t* table = p.page_table + w.b * p.pt_b;
+      for (int j = 0; ok && j < w.n_blocks; ++j, ++blk) {
+        const int k0 = (w.jb0 + j) * kBlockK;
+        // exponents of the block's largest scales: every warp looks at all 128 rows, four a lane
+        float s4[2][4], own[2];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          own[kv] = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s4[kv][i] = 0.f;
+        }
+        {
+          const int key = k0 + 4 * lane;  // four keys share a page
+          const int phys = key < w.sk ? __ldg(table + (key >> p.log2_page)) : -1;
+          if (phys >= 0 && phys < p.n_pages) {
+            const int64_t at = ((static_cast<int64_t>(phys) * p.Hkv + w.kvh) << p.log2_page) + (key & (p.page_size - 1));
+            const float4 a = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
+            const float4 b = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
+            const float ks[4] = {a.x, a.y, a.z, a.w}, vs[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (key + i < w.sk) s4[0][i] = ks[i], s4[1][i] = vs[i];
+          }
+        }
+        int e[2];
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const float m = fmaxf(fmaxf(s4[kv][0], s4[kv][1]), fmaxf(s4[kv][2], s4[kv][3]));
+          const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // scales are not negative
+          e[kv] = max(static_cast<int>(top >> 23) - 127 - kBlockExpRoom, kMinBlockExp);
+          // the scale of this thread's row: lane row / 4 of the warp holds it
+          const int src = row >> 2;
+          const float a0 = __shfl_sync(0xffffffffu, s4[kv][0], src), a1 = __shfl_sync(0xffffffffu, s4[kv][1], src);
+          const float a2 = __shfl_sync(0xffffffffu, s4[kv][2], src), a3 = __shfl_sync(0xffffffffu, s4[kv][3], src);
+          own[kv] = (row & 2) ? ((row & 1) ? a3 : a2) : ((row & 1) ? a1 : a0);
+        }
+        if (tid == 128) blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
+        const bool live = k0 + row < w.sk;  // rows past kv_len may hold anything
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++g) {
+          const int rs = g % NR, s = g % NS;
+          // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+          const float f32 = own[kv] * __uint_as_float(static_cast<uint32_t>(127 - e[kv]) << 23);
+          const uint32_t f = pack_f16x2(f32, f32);
+          if (!mbar_wait_warp(&raw_full[rs], (g / NR) & 1, abort_flag, p.status) ||
+              (g >= NS && !mbar_wait_warp(&empty[s], (g / NS - 1) & 1, abort_flag, p.status))) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = sKV + s * C::SLOT;
+          if (live) {
+            if (kv == 0)
+              convert_row<D, C::KW>(sRaw + rs * C::RAW, dst, row, f);
+            else
+              convert_row<DV, C::VW>(sRaw + rs * C::RAW, dst, row, f);
+          } else {
+#pragma unroll
+            for (int c = 0; c < (kv == 0 ? C::NCH_D : C::NCH_V); ++c)
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                *reinterpret_cast<uint4*>(dst + c * kBlockK * 128 + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&full[s]);
+          mbar_arrive(&raw_empty[rs]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax warpgroups
+    regs_inc<C::REGS_SOFTMAX>();
+    const int t = (warp - C::SOFTMAX_WARP) >> 2;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem_base + lane_off + t * 128;
+    const uint32_t tO = tmem_base + lane_off + 256 + t * 128;
+    // (token, head) of this thread's row
+    const int row_tok = static_cast<int>(fast_div(static_cast<uint32_t>(row), p.div_group));
+    const int row_head = row - row_tok * p.group;
+    int sn = 0, on = 0;
+    int g = 0, blk = 0;
+    bool ok = true;
+    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
+      const PagedUnit w = paged_unit(p, item);
+      const int g0 = g, blk0 = blk;
+      g += 2 * w.n_blocks;
+      blk += w.n_blocks;
+      const int n = w.n_t[t];
+      if (n == 0) continue;
+      const int tok = w.tok0 + t * p.tok_tile + row_tok;
+      const bool row_valid = row_tok < p.tok_tile && tok < w.n;
+      // keys this row sees, and those every row of the tile sees
+      const int lim_row = p.causal ? min(w.sk, w.len - w.n + tok + 1) : w.sk;
+      const int lim_all = p.causal ? min(w.sk, w.len - w.n + w.tok0 + t * p.tok_tile + 1) : w.sk;
+      float row_scale2 = p.scale2;
+      float m_used = -INFINITY;
+      float l = 0.f;
+      for (int j = 0; j < n; ++j, ++sn) {
+        if (!mbar_wait_warp(&s_full[t], sn & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        // the query's exponent was stored before q_ready, which the MMAs behind s_full waited for
+        if (CONVERT_Q && j == 0)
+          row_scale2 *= __uint_as_float(
+              static_cast<uint32_t>(127 + static_cast<int>(q_exp[(t * 2 + (on & 1)) * 128 + row])) << 23);
+        float blk_scale2 = row_scale2, shift = 0.f, unshift = 1.f;
+        if constexpr (QUANT) {
+          const int gv = g0 + 2 * j + 1;  // V(j) converted: both exponents of the block are there
+          if (!mbar_wait_warp(&full[gv % NS], (gv / NS) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const int2 e = blk_exp[(blk0 + j) % kExpRing];
+          blk_scale2 = fmaxf(blk_scale2 * __uint_as_float(static_cast<uint32_t>(127 + e.x) << 23), kMinBlkScale2);
+          shift = static_cast<float>(e.y);
+          unshift = __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
+        }
+        tc_fence_after();
+        float s[kBlockK];
+        {
+          uint32_t r0[32], r1[32], r2[32], r3[32];
+          tmem_ld32(tS + 0, r0);
+          tmem_ld32(tS + 32, r1);
+          tmem_ld32(tS + 64, r2);
+          tmem_ld32(tS + 96, r3);
+          tmem_ld_wait();
+          reg_fence(r0);
+          reg_fence(r1);
+          reg_fence(r2);
+          reg_fence(r3);
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            s[c] = __uint_as_float(r0[c]);
+            s[32 + c] = __uint_as_float(r1[c]);
+            s[64 + c] = __uint_as_float(r2[c]);
+            s[96 + c] = __uint_as_float(r3[c]);
+          }
+        }
+        const int k0 = (w.jb0 + j) * kBlockK;
+        if (k0 + kBlockK > lim_all) {  // the diagonal and the ragged last block
+          const int lim = lim_row - k0;
+#pragma unroll
+          for (int c = 0; c < kBlockK; ++c)
+            if (c >= lim) s[c] = -INFINITY;
+        }
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mx[i] = fmaxf(s[i], s[8 + i]);
+#pragma unroll
+        for (int gi = 1; gi < kBlockK / 16; ++gi)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) mx[i] = fmax3(mx[i], s[16 * gi + i], s[16 * gi + 8 + i]);
+        const float mb = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+        const float m_cand = fmaxf(m_used, QUANT ? fmaf(mb, blk_scale2, shift) : mb * blk_scale2);
+        const bool need = m_cand > m_used + kPagedRescaleLog2;
+        const bool rescale = __any_sync(0xffffffffu, need);
+        float alpha = 1.f;
+        if (rescale) {
+          alpha = (m_cand == -INFINITY) ? 1.f : ex2(m_used - m_cand);
+          l *= alpha;
+          m_used = m_cand;
+        }
+        // P = 2^(y - m), rounded to 16 bits for the P.V product; the row sum takes the fp32 values.  P
+        // goes to tensor memory in two halves, so that P.V starts on the first.
+        const float neg_m = (m_used == -INFINITY) ? 0.f : (QUANT ? shift - m_used : -m_used);
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int w2 = 0; w2 < 32; ++w2) {
+            const int c = half * 64 + 2 * w2;
+            float x0, x1;
+            ffma2_scalar(x0, x1, s[c], s[c + 1], blk_scale2, neg_m);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            pk[w2] = F16_MATH ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            if (w2 & 1)
+              fadd2(ls[2], ls[3], p0, p1);
+            else
+              fadd2(ls[0], ls[1], p0, p1);
+          }
+          tmem_st32(tS + half * 32, pk);
+          if (half == 1) break;
+          if (rescale && j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < DV / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO + c * 32, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                float a = __uint_as_float(o[i]), b = __uint_as_float(o[i + 1]);
+                fmul2_scalar(a, b, alpha);
+                o[i] = __float_as_uint(a);
+                o[i + 1] = __float_as_uint(b);
+              }
+              tmem_st32(tO + c * 32, o);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(&p_half[t]);
+        }
+        const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l = QUANT ? fmaf(sum, unshift, l) : l + sum;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&p_full[t]);
+      }
+      if (!ok) break;
+
+      // ---------------------------------------------------------- epilogue: O / l and LSE, or a partial
+      if (!mbar_wait_warp(&o_full[t], on & 1, abort_flag, p.status)) {
+        ok = false;
+        break;
+      }
+      ++on;
+      tc_fence_after();
+      if (w.slot >= 0) {
+        const int64_t prow = static_cast<int64_t>(w.slot) * p.slot_rows + t * kBlockQ + row;
+#pragma unroll 1
+        for (int c = 0; c < DV / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO + c * 32, o);
+          tmem_ld_wait();
+          reg_fence(o);
+          if (row_valid) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * DV + c * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+        mbar_arrive(&o_empty[t]);
+        if (row_valid) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m_used, l);
+        continue;
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int head = w.kvh * p.group + row_head;
+      uint16_t* orow = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(w.q_off + tok) * p.o_s + static_cast<int64_t>(head) * p.o_h;
+#pragma unroll 1
+      for (int c = 0; c < DV / 32; ++c) {
+        uint32_t o[32];
+        tmem_ld32(tO + c * 32, o);
+        tmem_ld_wait();
+        reg_fence(o);
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
+          pk[i] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+        }
+        if (row_valid) {
+          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        }
+        __syncwarp();
+      }
+      tc_fence_before();
+      mbar_arrive(&o_empty[t]);
+      if (p.lse != nullptr && row_valid)
+        p.lse[static_cast<int64_t>(head) * p.total_q + w.q_off + tok] =
+            l > 0.f ? (m_used + lg2(l)) * kPagedLn2 : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// Launches the kernel as a programmatic dependent of the plan kernel, one CTA per SM.
+template <bool BF16, bool QUANT, int D, int DV>
+cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, cudaStream_t st) {
+  using C = PagedCfg<QUANT, D, DV>;
+  auto kern = paged_kernel<BF16, QUANT, D, DV>;
+  int dev = 0, sms = 0;
+  cudaError_t e = current_device_sms(&dev, &sms);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> opted{0};
+  if ((e = smem_opt_in(kern, C::SMEM, dev, opted)) != cudaSuccess) return e;
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.sms));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
+}
+
+}  // namespace sdpa

@@ -1,0 +1,13 @@
+// Chunk attention over 16-bit pages, f16.
+#include "paged.cuh"
+
+namespace sdpa {
+
+cudaError_t launch_paged_f16(int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                             const PagedParams& p, cudaStream_t st) {
+  if (D == 64) return launch_paged_instance<false, false, 64, 64>(tq, tk, tv, p, st);
+  if (D == 128) return launch_paged_instance<false, false, 128, 128>(tq, tk, tv, p, st);
+  return launch_paged_instance<false, false, 192, 128>(tq, tk, tv, p, st);
+}
+
+}  // namespace sdpa

@@ -30,7 +30,7 @@
  *  - Validation happens before any CUDA call; an invalid call launches nothing.
  *  - The library allocates no device memory in these entry points.  Decode and masked
  *    prefill take a caller workspace sized by the *_workspace_size functions.
- *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_int8, sdpa_decode, sdpa_decode_paged*
+ *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_paged*, sdpa_fwd_int8, sdpa_decode, sdpa_decode_paged*
  *    and sdpa_cache_* may be recorded into a CUDA graph (stream capture) once a first call on
  *    the device has run outside the capture; sdpa_fwd_host may not.
  */
@@ -396,6 +396,67 @@ int sdpa_decode_paged_fp8(const void* q, const void* k_pool, const void* v_pool,
                           const int64_t* strides, float scale, void* workspace, size_t workspace_bytes,
                           sdpa_dtype dtype, void* stream);
 
+/* Number of int64 entries in the stride array of sdpa_fwd_paged / sdpa_fwd_paged_fp8. */
+#define SDPA_FWD_PAGED_NSTRIDES 11
+
+/*
+ * sdpa_fwd_paged_workspace_size -- bytes of device scratch for sdpa_fwd_paged and
+ * sdpa_fwd_paged_fp8 (max_kv = max_pages * page_size): the work plan, which the call needs, and
+ * partial results of key ranges that run on otherwise idle SMs.  With less than the full size
+ * (but at least 32 + 12 * (B + 1) bytes, rounded up to 16) the call cuts fewer ranges; results agree
+ * within rounding.  0 for bad sizes.
+ */
+size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_kv, int Dv);
+
+/*
+ * sdpa_fwd_paged -- attention of a chunk of new tokens per sequence over a paged cache that already
+ * holds them (a prompt's chunk, drafted tokens, a mixed batch).  Sequence b's n_b new tokens are
+ * packed rows cu_seqlens_q[b] .. cu_seqlens_q[b+1]-1; token i of them is position
+ * kv_len[b] - n_b + i of the sequence and sees the keys j < kv_len[b], with causal != 0 only those up to its
+ * position (bottom-right aligned).  A token without visible keys (kv_len[b] = 0, a negative
+ * position) gets O = 0, LSE = -inf.
+ *
+ *   q [total_q, Hq, D], o [total_q, Hq, Dv]  dtype (SDPA_F16 or SDPA_BF16; o written for the rows
+ *           some sequence owns, the others are left as they are)
+ *   lse [Hq, total_q] fp32 contiguous, natural log; may be NULL
+ *   k_pool [n_pages, page_size, Hkv, D], v_pool [n_pages, page_size, Hkv, Dv]  dtype
+ *   page_table [B, max_pages] DEVICE int32, entries past ceil(kv_len[b] / page_size) never used; an
+ *           entry outside [0, n_pages) reads as zero rows
+ *   kv_len [B] DEVICE int32, clamped into [0, max_pages * page_size] as the number of keys
+ *   cu_seqlens_q [B + 1] DEVICE int32, non-decreasing within [0, total_q]; max_seqlen_q >= every
+ *           n_b and <= total_q.  Offsets that break this make the call store nothing and raise a status
+ *           that sdpa_check_device_status() reports as SDPA_ERR_INVALID.
+ *   strides: NULL for the contiguous layouts, else 11 element strides {q_s, q_h,  k_pool page, row,
+ *           head,  v_pool page, row, head,  o_s, o_h,  page_table row}, multiples of 8
+ *   workspace: see sdpa_fwd_paged_workspace_size; 16-byte aligned, contents on entry irrelevant.
+ *           Calls that overlap on the GPU need separate workspaces.
+ *
+ * Rows of a page at or past kv_len never contribute and may hold anything; the visible rows must be
+ * finite.  (D, Dv) in {(64, 64), (128, 128), (192, 128)}; Hq / Hkv <= 128; page_size a power of
+ * two >= 16; pointers 16-byte aligned.  Two kernels run in `stream` (the plan, the attention), three where
+ * the workspace allows cuts.
+ */
+int sdpa_fwd_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
+                   const int32_t* kv_len, const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
+                   int total_q, int max_seqlen_q, int page_size, int max_pages, int n_pages, int D, int Dv,
+                   const int64_t* strides, float scale, int causal, void* workspace, size_t workspace_bytes,
+                   sdpa_dtype dtype, void* stream);
+
+/*
+ * sdpa_fwd_paged_fp8 -- sdpa_fwd_paged over a quantised cache (K = k_code * k_scale, V = v_code *
+ * v_scale; pool strides multiples of 16).  The codes are brought to fp16 on chip and both products
+ * run in fp16 with fp32 accumulation, a bf16 query scaled into fp16 by a power of two per row; P is
+ * rounded to fp16.  Scales enter relative to the largest of their 128-key block: rows of power-of-two
+ * scales are exact down to 2^-21 of it, then lose a bit for each power of two and vanish under 2^-30;
+ * other scales are rounded to fp16 (2^-11).
+ */
+int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
+                       const float* v_scale, const int32_t* page_table, const int32_t* kv_len,
+                       const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv, int total_q,
+                       int max_seqlen_q, int page_size, int max_pages, int n_pages, int D, int Dv,
+                       const int64_t* strides, float scale, int causal, void* workspace, size_t workspace_bytes,
+                       sdpa_dtype dtype, void* stream);
+
 /*
  * sdpa_decode_noalloc -- sdpa_decode for callers that cannot allocate device memory: runtimes
  * without a device allocator of their own, hosts that hand out device memory only through
@@ -422,7 +483,7 @@ int sdpa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
  * sdpa_check_device_status -- synchronizes `stream`, then reports and clears the device
  * status word the kernels raise when a bounded wait inside them gives up (a pipeline
  * stage that never arrived): SDPA_ERR_TIMEOUT in that case, SDPA_ERR_INVALID when a varlen
- * call found bad sequence offsets or a cache call a row without a slot, SDPA_ERR_CUDA if the synchronization itself failed, else
+ * or paged call found bad sequence offsets or a cache call a row without a slot, SDPA_ERR_CUDA if the synchronization itself failed, else
  * SDPA_OK.  The status word is per device and per
  * process, shared by all streams.
  */

@@ -153,3 +153,62 @@ def test_oracle_paged_chunk_is_plain_attention():
     s = s + torch.full_like(s, float("-inf")).triu(46)
     assert np.allclose(o[:, 0], (torch.softmax(s, -1) @ v[0, :50, 0]).numpy(), atol=1e-12)
     assert np.allclose(lse[0], torch.logsumexp(s, -1).numpy(), atol=1e-12)
+
+
+def _fwd(lib, quant, **over):
+    a = dict(q=FAKE, kp=FAKE, vp=FAKE, ks=FAKE, vs=FAKE, pt=FAKE, kv=FAKE, cu=FAKE, o=FAKE, lse=None, B=2, Hq=8, Hkv=2,
+             total=20, maxq=12, page=16, maxp=4, np=8, D=128, Dv=128, strides=None, scale=0.1, causal=1, ws=FAKE,
+             wsb=1 << 26, dt=fa.SDPA_BF16, stream=None)
+    a.update(over)
+    if not quant:
+        del a["ks"], a["vs"]
+    return (lib.sdpa_fwd_paged_fp8 if quant else lib.sdpa_fwd_paged)(*a.values())
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_chunk_codes(lib, quant):
+    for name in ("q", "kp", "vp", "pt", "kv", "cu", "o", "ws") + (("ks", "vs") if quant else ()):
+        assert _fwd(lib, quant, **{name: None}) == fa.SDPA_ERR_INVALID, name
+    for name in ("q", "kp", "vp", "o") + (("ks", "vs") if quant else ()):
+        assert _fwd(lib, quant, **{name: OFF8}) == fa.SDPA_ERR_UNSUPPORTED, name
+    for name in ("pt", "kv", "cu", "lse"):
+        assert _fwd(lib, quant, **{name: ODD}) == fa.SDPA_ERR_INVALID, name
+    for name in ("B", "Hq", "Hkv", "total", "maxq", "np", "maxp", "D"):
+        assert _fwd(lib, quant, **{name: 0}) == fa.SDPA_ERR_INVALID, name
+    assert _fwd(lib, quant, maxq=21) == fa.SDPA_ERR_INVALID       # longer than all the packed rows
+    assert _fwd(lib, quant, Hkv=3) == fa.SDPA_ERR_INVALID
+    assert _fwd(lib, quant, Hq=258) == fa.SDPA_ERR_UNSUPPORTED    # 129 heads per KV head
+    assert _fwd(lib, quant, scale=0.0) == fa.SDPA_ERR_INVALID
+    assert _fwd(lib, quant, page=48) == fa.SDPA_ERR_INVALID
+    assert _fwd(lib, quant, page=8) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, D=96, Dv=96) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, D=64) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, dt=fa.SDPA_E4M3) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, wsb=32) == fa.SDPA_ERR_INVALID        # below the plan
+    assert _fwd(lib, quant, ws=OFF8) == fa.SDPA_ERR_INVALID
+    good = [1024, 128, 4096, 256, 128, 4096, 256, 128, 1024, 128, 4]
+
+    def strides(i, x):
+        s = list(good)
+        s[i] = x
+        return (ctypes.c_int64 * 11)(*s)
+
+    assert _fwd(lib, quant, strides=strides(0, 1028)) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, strides=strides(9, 130)) == fa.SDPA_ERR_UNSUPPORTED
+    assert _fwd(lib, quant, strides=strides(10, 3)) == fa.SDPA_ERR_INVALID
+    if quant:
+        assert _fwd(lib, quant, strides=strides(3, 264)) == fa.SDPA_ERR_UNSUPPORTED
+
+
+def test_chunk_workspace(lib):
+    size = fa.sdpa_fwd_paged_workspace_size
+    plan = lambda B: ((4 + 3 * (B + 1)) * 4 + 15) // 16 * 16  # noqa: E731
+    # one block of keys: nothing to cut
+    assert size(3, 8, 2, 30, 12, 128, 128) == plan(3)
+    # 5 tokens x 4 heads = 20 rows a slot; one tile per sequence and head, at most 64 segments
+    assert size(2, 8, 2, 10, 5, 1 << 20, 128) == plan(2) + 2 * 2 * 64 * 20 * 130 * 4
+    # long chunks take slots of 256 rows, 64 MB of them
+    one = 256 * 130 * 4
+    assert size(4, 32, 8, 8192, 2048, 16384, 128) == plan(4) + ((64 << 20) // one) * one
+    for bad in ((0, 8, 2, 10, 5, 64, 128), (2, 8, 3, 10, 5, 64, 128), (2, 8, 2, 10, 11, 64, 128), (2, 8, 2, 10, 5, 0, 128)):
+        assert size(*bad) == 0

@@ -1,0 +1,320 @@
+"""GPU parity of the chunk attention over paged caches (16-bit and quantised) against the fp64 oracle.
+
+Tolerance.  The probabilities are rounded to the 16-bit type of the P.V product (half a step u_p: bf16
+2^-8, fp16 2^-11; quantised caches use fp16 whatever the query's type), the row sums are fp32 of the
+unrounded ones, exp2 and the fp32 score carry 2^-21 |s| (scores below 2^6 here: 2^-15, twice: numerator and
+sum), and the output is rounded once (half a step u).  With |V| <= vmax over the visible keys
+    |dO| <= u |O| + (u_p + 2^-14 + 2^-16) vmax,   |dLSE| <= 2^-15 + 2^-16.
+A quantised V row adds at most 2^-25 of its block's largest magnitude (fp16's smallest step below the
+scaled codes), inside the 2^-16.
+"""
+import numpy as np
+import pytest
+import torch
+
+import flash_attention_forward_gb300 as fa
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+TOL_LSE = 2.0 ** -15 + 2.0 ** -16
+
+
+def make(new, lens, Hq, Hkv, D, Dv, page, dtype, quant, seed=0, spare=2, gain=None):
+    """Packed queries and a paged cache: rows past a length and spare pages are NaN (codes and scales), table
+    entries past a sequence's pages are wild."""
+    g = torch.Generator().manual_seed(seed)
+    pages = [(L + page - 1) // page for L in lens]
+    n_pages, max_pages = sum(pages) + spare, max(max(pages), 1) + 1
+    perm = torch.randperm(n_pages, generator=g).to(torch.int32)
+    wild = torch.tensor([-7, 1 << 30, n_pages, 3], dtype=torch.int32)
+    table = wild[torch.arange(len(lens) * max_pages) % 4].view(len(lens), max_pages).clone()
+    k = torch.full((n_pages, page, Hkv, D), float("nan"))
+    v = torch.full((n_pages, page, Hkv, Dv), float("nan"))
+    at = 0
+    for b, L in enumerate(lens):
+        ids = perm[at:at + pages[b]].long()
+        table[b, :pages[b]] = ids.to(torch.int32)
+        at += pages[b]
+        for pool, d in ((k, D), (v, Dv)):
+            rows = torch.full((pages[b] * page, Hkv, d), float("nan"))
+            rows[:L] = torch.randn((L, Hkv, d), generator=g)
+            if gain is not None:
+                rows = rows * gain(g, rows)
+            pool[ids] = rows.view(pages[b], page, Hkv, d)
+    q = torch.randn((sum(new), Hq, D), generator=g).to(DT[dtype])
+    if quant:
+        pools = []
+        for pool in (k, v):
+            codes, scales = oracle.quantise_pool(pool)
+            nan = torch.isnan(pool).all(-1).transpose(1, 2)
+            pools += [codes, torch.where(nan, torch.full_like(scales, float("nan")), scales).contiguous()]
+    else:
+        pools = [k.to(DT[dtype]), v.to(DT[dtype])]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32)
+    return q, pools, table, torch.tensor(lens, dtype=torch.int32), cu
+
+
+def run(q, pools, table, kv, cu, maxq, **kw):
+    d = [t.to(DEV) for t in pools]
+    if len(pools) == 4:
+        o, lse = fa.sdpa_fwd_paged_fp8(q.to(DEV), d[0], d[2], d[1], d[3], table.to(DEV), kv.to(DEV), cu.to(DEV), maxq, **kw)
+    else:
+        o, lse = fa.sdpa_fwd_paged(q.to(DEV), d[0], d[1], table.to(DEV), kv.to(DEV), cu.to(DEV), maxq, **kw)
+    torch.cuda.synchronize()
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    return o, lse
+
+
+def values(pools):
+    if len(pools) == 4:
+        return oracle.dequantise_pool(*pools[:2]), oracle.dequantise_pool(*pools[2:])
+    return pools
+
+
+def check(q, pools, table, kv, cu, o, lse, scale, causal):
+    k, v = values(pools)
+    kvl = kv.tolist()
+    ref, ref_lse = oracle.sdpa_fwd_paged(q, k, v, table, kvl, cu, scale=scale, causal=causal)
+    got, got_lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    u = torch.finfo(o.dtype).eps / 2
+    u_p = 2.0 ** -11 if len(pools) == 4 or o.dtype == torch.float16 else 2.0 ** -8
+    vg = oracle.gather_pages(v, table, kvl)
+    for b in range(len(kvl)):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        if rows.stop == rows.start:
+            continue
+        L = max(0, min(kvl[b], vg.shape[1]))
+        vmax = float(vg[b, :L].abs().max()) if L else 0.0
+        assert np.isfinite(got[rows]).all(), f"sequence {b}: NaN or Inf"
+        err = np.abs(got[rows] - ref[rows])
+        assert (err <= u * np.abs(ref[rows]) + (u_p + 2.0 ** -14 + 2.0 ** -16) * vmax).all(), (b, err.max(), vmax)
+        dead = np.isneginf(ref_lse[:, rows])
+        assert np.array_equal(np.isneginf(got_lse[:, rows]), dead)
+        assert (got[rows][dead.T] == 0).all()
+        if (~dead).any():
+            e = np.abs(got_lse[:, rows] - ref_lse[:, rows])[~dead].max()
+            assert e <= TOL_LSE, (b, e)
+
+
+NEW = [1, 3, 0, 33, 64, 130, 5, 20, 1, 2]
+LENS = [1, 3, 5, 33, 700, 131, 127, 128, 129, 1500]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("Hq,Hkv,D,Dv,page", [(8, 2, 128, 128, 64), (14, 2, 128, 128, 16), (3, 3, 64, 64, 32),
+                                              (16, 1, 192, 128, 128), (4, 4, 192, 128, 16), (24, 2, 64, 64, 256)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_ragged_chunks(quant, dtype, Hq, Hkv, D, Dv, page, causal):
+    x = make(NEW, LENS, Hq, Hkv, D, Dv, page, dtype, quant)
+    o, lse = run(*x, max(NEW), scale=D ** -0.5, causal=causal)
+    check(*x, o, lse, D ** -0.5, causal)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_tokens_without_keys(quant):
+    # an empty cache, and more new tokens than rows: the first ones sit at negative positions
+    x = make([4, 10, 2], [0, 6, 2], 8, 2, 128, 128, 16, "bf16", quant)
+    o, lse = run(*x, 10, scale=0.1, causal=True)
+    check(*x, o, lse, 0.1, True)
+    assert torch.isneginf(lse[:, :8]).all() and (o[:8] == 0).all()
+    o, lse = run(*x, 10, scale=0.1, causal=False)
+    check(*x, o, lse, 0.1, False)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens", [([5], [20000]), ([1, 8, 3], [9000, 300, 6000]), ([300], [8000]), ([2000], [2000])])
+def test_cut_key_ranges(quant, new, lens):
+    # few rows over long caches: the plan cuts the keys; a workspace for the plan alone must give the same
+    x = make(new, lens, 8, 2, 128, 128, 64, "bf16", quant, seed=4)
+    o, lse = run(*x, max(new), scale=0.09, causal=True)
+    check(*x, o, lse, 0.09, True)
+    small = torch.empty((4 + 3 * (len(new) + 1)) * 4 + 16, dtype=torch.uint8, device=DEV)
+    o2, lse2 = run(*x, max(new), scale=0.09, causal=True, workspace=small)
+    check(*x, o2, lse2, 0.09, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("B,new", [(40, 1), (300, 2)])
+def test_many_sequences_on_each_sm(quant, B, new):
+    # every CTA walks several units, most of one ragged block
+    g = torch.Generator().manual_seed(6)
+    lens = torch.randint(new, 400, (B,), generator=g).tolist()
+    x = make([new] * B, lens, 4, 2, 128, 128, 16, "bf16", quant, seed=7)
+    o, lse = run(*x, new, scale=0.09, causal=True)
+    check(*x, o, lse, 0.09, True)
+
+
+def test_rows_of_very_different_scales():
+    # scales up to 2^12 apart inside a block, bf16 queries far outside fp16's range
+    gain = lambda g, rows: torch.exp2(torch.randint(-12, 1, rows.shape[:-1], generator=g).float())[..., None]  # noqa: E731
+    for qg in (2.0 ** -20, 2.0 ** 20):
+        q, pools, table, kv, cu = make([9, 40], [500, 140], 8, 2, 128, 128, 32, "bf16", True, gain=gain)
+        q = (q.float() * qg).to(q.dtype)
+        o, lse = run(q, pools, table, kv, cu, 40, scale=0.09 / qg, causal=True)
+        check(q, pools, table, kv, cu, o, lse, 0.09 / qg, True)
+
+
+def test_small_values_keep_their_precision_beside_large_ones():
+    # all the weight on a key whose V row is 2^-18 of its block's others: the output is that row.  Its codes
+    # reach fp16 times 2^-18 * 2^6 of the block's factor, exact down to codes of 2^-12 * 2^-24
+    q, pools, table, kv, cu = make([3], [200], 4, 1, 128, 128, 16, "bf16", False)
+    k, v = torch.zeros(pools[0].shape), pools[1].float()
+    p, r = int(table[0, 77 // 16]), 77 % 16
+    k[p, r, 0] = 20.0  # score 2560 against 0
+    v[p, r] *= 2.0 ** -18
+    pools = [*oracle.quantise_pool(k), *oracle.quantise_pool(torch.nan_to_num(v))]
+    o, _ = run(torch.ones_like(q), pools, table, kv, cu, 3, scale=1.0, causal=True)
+    want = oracle.dequantise_pool(*pools[2:])[p, r, 0]
+    err = (o[0, 0].double().cpu() - want).abs()
+    assert (err <= 2.0 ** -8 * want.abs() + 2.0 ** -25 * 2.0 ** -6 * float(pools[3].max()) * 2).all()
+
+
+def test_zero_queries_and_zero_keys():
+    # a zero query row against a zero K block: every score is 0 and the mask must stay a mask
+    q, pools, table, kv, cu = make([4], [130], 4, 1, 128, 128, 16, "bf16", False)
+    k, v = torch.nan_to_num(pools[0].float()) * 0, torch.nan_to_num(pools[1].float())
+    pools = [*oracle.quantise_pool(k), *oracle.quantise_pool(v)]
+    q[:2] = 0
+    o, lse = run(q, pools, table, kv, cu, 4, scale=0.09, causal=True)
+    check(q, pools, table, kv, cu, o, lse, 0.09, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_strides_interleaved_pools_and_untouched_rows(quant):
+    new, lens, page = [7, 20], [50, 40], 16
+    q, pools, table, kv, cu = make(new, lens, 8, 2, 128, 128, page, "f16", quant)
+    k, v = pools[0], pools[-2] if quant else pools[1]
+    # K and V pages alternate in one pool; q and o are slices of wider rows; two rows belong to nobody
+    both = torch.stack([k.view(torch.uint8 if quant else torch.int16), v.view(torch.uint8 if quant else torch.int16)], 1).to(DEV)
+    both = both.view(torch.float8_e4m3fn if quant else torch.float16)
+    wide = torch.zeros((29, 10, 256), dtype=q.dtype, device=DEV)
+    wide[:27, 1:9, 128:] = q.to(DEV)
+    out = torch.full((29, 9, 192), 5.0, dtype=q.dtype, device=DEV)
+    tab = torch.full((2, table.shape[1] + 5), -1, dtype=torch.int32, device=DEV)
+    tab[:, : table.shape[1]] = table.to(DEV)
+    args = (table.shape[1],)
+    qs, os_ = wide[:, 1:9, 128:], out[:, :8, 64:]
+    common = (tab[:, : args[0]], kv.to(DEV), cu.to(DEV), 20)
+    if quant:
+        _, lse = fa.sdpa_fwd_paged_fp8(qs, both[:, 0], both[:, 1], pools[1].to(DEV), pools[3].to(DEV), *common, scale=0.1,
+                                       causal=True, out=os_)
+    else:
+        _, lse = fa.sdpa_fwd_paged(qs, both[:, 0], both[:, 1], *common, scale=0.1, causal=True, out=os_)
+    torch.cuda.synchronize()
+    assert (out[27:] == 5).all() and (out[..., :64] == 5).all() and (out[:, 8] == 5).all()
+    check(q, pools, table, kv, cu, os_[:27].contiguous(), lse[:, :27].contiguous(), 0.1, True)
+
+
+def test_bad_offsets_store_nothing_and_are_reported():
+    q, pools, table, kv, cu = make([5, 6], [50, 40], 4, 2, 128, 128, 16, "bf16", False)
+    d = [t.to(DEV) for t in pools]
+    for bad, maxq in (([0, 12, 11], 11), ([0, 5, 12], 11), ([-1, 5, 11], 11), ([0, 5, 11], 5)):
+        out = torch.full((11, 4, 128), 3.0, dtype=q.dtype, device=DEV)
+        fa.sdpa_fwd_paged(q.to(DEV), d[0], d[1], table.to(DEV), kv.to(DEV), torch.tensor(bad, dtype=torch.int32, device=DEV),
+                          maxq, out=out)
+        torch.cuda.synchronize()
+        assert fa.sdpa_check_device_status() == fa.SDPA_ERR_INVALID
+        assert (out == 3).all()
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_pages_outside_the_pool_read_as_zeros(quant):
+    x = make([3], [64], 4, 1, 128, 128, 16, "bf16", quant)
+    q, pools, table, kv, cu = x
+    table[0, 1], table[0, 3] = -1, pools[0].shape[0]
+    o, lse = run(*x, 3, scale=0.1, causal=False)
+    k, v = (t.clone().double() for t in values(pools))
+    zk = torch.cat([k, torch.zeros_like(k[:1])])
+    zv = torch.cat([v, torch.zeros_like(v[:1])])
+    table[0, 1] = table[0, 3] = k.shape[0]
+    ref, ref_lse = oracle.sdpa_fwd_paged(q, zk, zv, table, [64], cu, scale=0.1, causal=False)
+    vmax = float(torch.nan_to_num(v).abs().max())
+    u_p = 2.0 ** -11 if quant else 2.0 ** -8
+    assert (np.abs(o.double().cpu().numpy() - ref) <= 2.0 ** -8 * np.abs(ref) + (u_p + 2.0 ** -13) * vmax).all()
+    assert np.abs(lse.cpu().numpy() - ref_lse).max() <= TOL_LSE
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_streams_graph_and_repeatability(quant):
+    q, pools, table, kv, cu = make([3, 70, 1], [9000, 900, 77], 8, 2, 128, 128, 64, "bf16", quant, seed=2)
+    d = [t.to(DEV) for t in pools]
+    args = (q.to(DEV), d[0], d[2], d[1], d[3]) if quant else (q.to(DEV), d[0], d[1])
+    args += (table.to(DEV), kv.to(DEV), cu.to(DEV), 70)
+    fn = fa.sdpa_fwd_paged_fp8 if quant else fa.sdpa_fwd_paged
+    want, want_lse = fn(*args, causal=True)
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(2):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            outs += [fn(*args, causal=True) for _ in range(3)]
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = fn(*args, causal=True)
+    o.zero_()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_a_wait_that_gives_up_is_reported(quant):
+    x = make([3, 200], [300, 900], 8, 2, 128, 128, 64, "bf16", quant)
+    fa.library().sdpa_debug_stall_next_call()
+    q, pools, table, kv, cu = x
+    d = [t.to(DEV) for t in pools]
+    args = (q.to(DEV), d[0], d[2], d[1], d[3]) if quant else (q.to(DEV), d[0], d[1])
+    fn = fa.sdpa_fwd_paged_fp8 if quant else fa.sdpa_fwd_paged
+    fn(*args, table.to(DEV), kv.to(DEV), cu.to(DEV), 200, causal=True)
+    torch.cuda.synchronize()
+    assert fa.sdpa_check_device_status() == fa.SDPA_ERR_TIMEOUT
+    o, lse = run(*x, 200, scale=128 ** -0.5, causal=True)
+    check(*x, o, lse, 128 ** -0.5, True)
+
+
+def test_a_quantised_cache_in_use():
+    # prompts written in chunks, then single tokens: write, attend, decode and read back agree with the
+    # oracle on the values the cache holds
+    g = torch.Generator().manual_seed(9)
+    B, Hq, Hkv, D, page, dt = 3, 8, 2, 128, 16, torch.bfloat16
+    n_pages = 40
+    kp, vp = (torch.zeros((n_pages, page, Hkv, D), device=DEV).to(torch.float8_e4m3fn) for _ in range(2))
+    ks, vs = (torch.zeros((n_pages, Hkv, page), device=DEV) for _ in range(2))
+    table = torch.randperm(n_pages, generator=g)[:36].view(B, 12).to(torch.int32)
+    lens = [0, 0, 0]
+    for step in ([70, 5, 33], [30, 60, 0], [1, 1, 1]):
+        lens = [a + b for a, b in zip(lens, step)]
+        total = sum(step)
+        k, v = (torch.randn((total, Hkv, D), generator=g).to(dt) for _ in range(2))
+        q = torch.randn((total, Hq, D), generator=g).to(dt)
+        kv = torch.tensor(lens, dtype=torch.int32)
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(step)]), dtype=torch.int32)
+        t, kvd, cud = table.to(DEV), kv.to(DEV), cu.to(DEV)
+        fa.sdpa_cache_write_fp8(k.to(DEV), v.to(DEV), kp, vp, ks, vs, t, kvd, cud)
+        o, lse = fa.sdpa_fwd_paged_fp8(q.to(DEV), kp, vp, ks, vs, t, kvd, cud, max(step), causal=True)
+        torch.cuda.synchronize()
+        pools = [x.cpu() for x in (kp, ks, vp, vs)]
+        check(q, pools, table, kv, cu, o, lse, D ** -0.5, True)
+        if step == [1, 1, 1]:
+            od, lsed = fa.sdpa_decode_paged_fp8(q.to(DEV), kp, vp, ks, vs, t, kvd)
+            torch.cuda.synchronize()
+            check(q, pools, table, kv, cu, od, lsed.t().contiguous(), D ** -0.5, True)
+    cuk = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32)
+    rk, rv = fa.sdpa_cache_read_fp8(kp, vp, ks, vs, table.to(DEV), cuk.to(DEV), sum(lens))
+    torch.cuda.synchronize()
+    for got, i in ((rk, 0), (rv, 2)):
+        val = oracle.gather_pages(oracle.dequantise_pool(*pools[i:i + 2]), table, lens)
+        assert torch.equal(got.double().cpu(), torch.cat([val[b, :L] for b, L in enumerate(lens)]))
+    # the packed rows feed the packed prefill: the last token of each sequence sees the same keys
+    o2, _ = fa.sdpa_fwd_varlen(q.to(DEV), rk, rv, torch.arange(B + 1, dtype=torch.int32, device=DEV), cuk.to(DEV), 1)
+    torch.cuda.synchronize()
+    assert (o2.float() - od.float()).abs().max().item() <= 2 * 2.0 ** -8 * 4.5
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
