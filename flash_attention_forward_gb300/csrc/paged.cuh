@@ -61,7 +61,7 @@ struct PagedCfg {
   static constexpr int OFF_SLOT = OFF_Q + kTilesPerCta * Q_BYTES;
   static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
-  static constexpr int OFF_EXP = OFF_BAR + 512;                     // int2 [kExpRing]
+  static constexpr int OFF_EXP = OFF_BAR + 640;                     // int2 [kExpRing]
   static constexpr int OFF_QEXP = OFF_EXP + kExpRing * 8;           // int8 [2 tiles][2][128]
   static constexpr int SMEM = OFF_QEXP + (QUANT ? 512 : 0) + 1024;  // 1 KB of slack for the alignment
   // warpgroups: control (producer, MMA, helpers), converters (quantised), two softmax
@@ -167,8 +167,10 @@ __device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, in
 // Barriers (phases continue from unit to unit):
 //   q_full[t] / q_empty[t]: Q tile t landed / its last QK MMA finished
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
-//   full[s] / empty[s]    : ring slot s holds its item / the MMAs that read it finished
+//   full[s] / empty[s]    : ring slot s holds its item / both issuers' MMAs that read it finished
 //   raw_full / raw_empty  : quantised pages: codes landed / read by the converters
+//   e_full[i % 16]        : quantised pages: the exponents of block i are there
+//   turn[t]               : issuer t may issue (both tiles active)
 //   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
 //                           then zeroes those rows and completes full[s] in the copy's place
 //   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels
@@ -195,17 +197,19 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
   uint64_t* p_full = p_half + 2;        // [2]
   uint64_t* o_full = p_full + 2;        // [2]
   uint64_t* o_empty = o_full + 2;       // [2]
-  uint64_t* mma_done = o_empty + 2;     // [1]
-  uint64_t* v_ragged = mma_done + 1;     // [kFixRing]
+  uint64_t* mma_done = o_empty + 2;     // [2]
+  uint64_t* turn = mma_done + 2;        // [2]
+  uint64_t* v_ragged = turn + 2;        // [kFixRing]
   uint64_t* full = v_ragged + kFixRing;  // [NS]
   uint64_t* empty = full + NS;          // [NS]
   uint64_t* raw_full = empty + NS;      // [NR]
   uint64_t* raw_empty = raw_full + NR;  // [NR]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(raw_empty + NR);
+  uint64_t* e_full = raw_empty + NR;    // [kExpRing]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(e_full + kExpRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int2* blk_exp = reinterpret_cast<int2*>(smem + C::OFF_EXP);
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
-  static_assert((17 + kFixRing + 2 * NS + 2 * NR) * 8 + 8 <= 512, "barriers fit their area");
+  static_assert((20 + kFixRing + kExpRing + 2 * NS + 2 * NR) * 8 + 8 <= 640, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -222,13 +226,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       mbar_init(&p_full[t], 128);
       mbar_init(&o_full[t], 1);
       mbar_init(&o_empty[t], 128);
+      mbar_init(&mma_done[t], 1);
+      mbar_init(&turn[t], 1);
     }
-    mbar_init(mma_done, 1);
     for (int s = 0; s < kFixRing; ++s) mbar_init(&v_ragged[s], 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], QUANT ? 128 : 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);
     }
+    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 1);
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 128);
@@ -324,96 +330,131 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       for (int j = max(0, nr - kFixRing); j < nr; ++j) mbar_drain(&v_ragged[j % kFixRing], (j / kFixRing) & 1);
       for (int j = max(0, g - NL); j < g; ++j) mbar_drain(&ld_full[j % NL], (j / NL) & 1);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer (one thread)
+  } else if (warp == 1 || warp == 3) {
+    // ------------------------------------------------------------ MMA issuers: one thread per query tile
+    // An issuing thread blocks while the tensor core is busy, and whatever it does between two MMAs
+    // (a wait that succeeds at once costs some 75 cycles) leaves the tensor core idle if nobody else
+    // feeds it: with one issuer for both tiles that was 1800 of 4000 cycles a block.  So each tile
+    // has its own, and the two take turns: an issuer waits for everything its step reads, then for
+    // its turn, issues P.V and Q K^T, hands the turn over and does its commits while the other's MMAs
+    // run.  Without turns the tiles drift into step and both softmaxes leave the tensor core alone.
     regs_dec<C::REGS_CONTROL>();
     if (lane == 0) {
       constexpr uint32_t fmt = F16_MATH ? 0 : 1;
       constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, 0, 0, kBlockQ, kBlockK);
       constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, 0, 1, kBlockQ, DV);
-      const uint64_t dq0 = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
+      const int t = warp >> 1;
+      const uint64_t dq0 = make_smem_desc(smem_u32(sQ + t * C::Q_BYTES), 16, 1024, kSwizzle128B);
       const uint64_t dk0 = make_smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
       const uint64_t dv0 = make_smem_desc(smem_u32(sKV), kBlockK * 128, 1024, kSwizzle128B);
       const uint32_t q_lo = static_cast<uint32_t>(dq0), q_hi = static_cast<uint32_t>(dq0 >> 32);
       const uint32_t k_lo = static_cast<uint32_t>(dk0), k_hi = static_cast<uint32_t>(dk0 >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv0), v_hi = static_cast<uint32_t>(dv0 >> 32);
-      int qn[2] = {0, 0}, pn[2] = {0, 0};
-      int g = 0;       // items consumed before this unit
+      const uint32_t tS = tmem_base + t * 128;
+      const uint32_t tO = tmem_base + 256 + t * 128;
+      int qn = 0, pn = 0;         // units and blocks of this tile so far
+      uint32_t turns = 1 - t;     // parity of the turn barrier's next phase; tile 0 begins
+      int s = 0;                  // ring slot of the next item and the parity of its phase
+      uint32_t ph = 0;
       bool ok = true;
+      auto next = [&]() {
+        if (++s == NS) s = 0, ph ^= 1u;
+      };
       for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
         const PagedUnit w = paged_unit(p, item);
         if (w.n_blocks == 0) continue;
-        for (int t = 0; t < kTilesPerCta && ok; ++t)
-          if (w.n_t[t] > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[t] : &q_full[t], qn[t] & 1, abort_flag, p.status);
+        const int n = w.n_t[t];
+        const bool both = w.n_t[0] > 0 && w.n_t[1] > 0;
+        if (n > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[t] : &q_full[t], qn & 1, abort_flag, p.status);
+        // step j: O += P(j-1) V(j-1), then S = Q K(j)^T: the items in ring order.  Items that this
+        // tile does not read are seen and passed on.
         for (int j = 0; ok && j <= w.n_blocks; ++j) {
-          const int gk = g + 2 * j, gv = gk - 1;
-          const int sk = gk % NS, sv = (gv + NS) % NS;
-          bool v_in = false, k_in = false;  // waited for in this step
-          for (int t = 0; t < kTilesPerCta && ok; ++t) {
-            const uint32_t tS = tmem_base + t * 128;
-            const uint32_t tO = tmem_base + 256 + t * 128;
-            if (j >= 1 && j - 1 < w.n_t[t]) {
-              // O_t += P_t(j-1) V(j-1)
-              if (!v_in) {
-                if (!mbar_wait(&full[sv], (gv / NS) & 1, abort_flag, p.status)) {
-                  ok = false;
-                  break;
-                }
-                v_in = true;
-              }
-              if (j == 1 && qn[t] > 0 && !mbar_wait(&o_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) {
+          const bool pv = j >= 1 && j <= n, qk = j < n;
+          const int vs = s;  // slot of V(j-1)
+          if (j >= 1) {
+            if (!mbar_wait(&full[s], ph, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            next();
+            if (!pv) mbar_arrive(&empty[vs]);
+          }
+          const int ks = s;  // slot of K(j)
+          if (both && j < w.n_blocks && !mbar_wait(&full[ks], ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (pv) {
+            if (j == 1 && qn > 0 && !mbar_wait(&o_empty[t], (qn - 1) & 1, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            if (!mbar_wait(&p_half[t], pn & 1, abort_flag, p.status) ||
+                (both && !mbar_wait(&p_full[t], pn & 1, abort_flag, p.status))) {
+              ok = false;
+              break;
+            }
+          }
+          if (both) {
+            if (!mbar_wait(&turn[t], turns, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            turns ^= 1u;
+          }
+          if (pv) {
+            const uint32_t dv = v_lo + static_cast<uint32_t>((vs * C::SLOT) >> 4);
+            const uint32_t acc0 = (j > 1) ? 1u : 0u;
+            tc_fence_after();
+#pragma unroll
+            for (int kk = 0; kk < C::PV_STEPS / 2; ++kk)
+              mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv,
+                         kk > 0 ? 1u : acc0);
+            // a tile alone starts on the first half of P while the second is computed
+            if (!both) {
+              if (!mbar_wait(&p_full[t], pn & 1, abort_flag, p.status)) {
                 ok = false;
                 break;
               }
-              const uint32_t dv = v_lo + static_cast<uint32_t>((sv * C::SLOT) >> 4);
-              const uint32_t acc0 = (j - 1 > 0) ? 1u : 0u;
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                if (!mbar_wait(h == 0 ? &p_half[t] : &p_full[t], pn[t] & 1, abort_flag, p.status)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-#pragma unroll
-                for (int kk = h * C::PV_STEPS / 2; kk < (h + 1) * C::PV_STEPS / 2; ++kk)
-                  mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv,
-                             kk > 0 ? 1u : acc0);
-              }
-              if (!ok) break;
-              if (j == w.n_t[t]) mma_commit(&o_full[t]);
-              ++pn[t];
+              tc_fence_after();
             }
-            if (t == kTilesPerCta - 1 && j >= 1) mma_commit(&empty[sv]);
-            if (j < w.n_t[t]) {
-              // S_t = Q_t K(j)^T
-              if (!k_in) {
-                if (!mbar_wait(&full[sk], (gk / NS) & 1, abort_flag, p.status)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                k_in = true;
-              }
-              const uint32_t dq = q_lo + static_cast<uint32_t>((t * C::Q_BYTES) >> 4);
-              const uint32_t dk = k_lo + static_cast<uint32_t>((sk * C::SLOT) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < C::QK_STEPS; ++kk) {
-                const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
-                mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
-              }
-              mma_commit(&s_full[t]);
-              if (j == w.n_t[t] - 1) mma_commit(&q_empty[t]);
+            for (int kk = C::PV_STEPS / 2; kk < C::PV_STEPS; ++kk)
+              mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv, 1u);
+            ++pn;
+          }
+          if (!both && j < w.n_blocks && !mbar_wait(&full[ks], ph, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          if (qk) {
+            tc_fence_after();
+            const uint32_t dk = k_lo + static_cast<uint32_t>((ks * C::SLOT) >> 4);
+            if (!both && pv) mma_commit(&empty[vs]);
+#pragma unroll
+            for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+              const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
+              mma_f16_ss(tS, q_lo + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
             }
           }
-          if (ok && j < w.n_blocks) mma_commit(&empty[sk]);
+          if (both) mbar_arrive(&turn[1 - t]);
+          if (qk) mma_commit(&s_full[t]);
+          if (pv && (both || !qk)) mma_commit(&empty[vs]);
+          if (j < w.n_blocks) {
+            if (qk)
+              mma_commit(&empty[ks]);
+            else
+              mbar_arrive(&empty[ks]);
+            next();
+          }
+          if (pv && j == n) mma_commit(&o_full[t]);
+          if (qk && j == n - 1) mma_commit(&q_empty[t]);
         }
-        g += 2 * w.n_blocks;
-        for (int t = 0; t < kTilesPerCta; ++t)
-          if (w.n_t[t] > 0) ++qn[t];
+        if (n > 0) ++qn;
       }
       // every MMA issued so far has finished before tensor memory is released
-      mma_commit(mma_done);
-      mbar_drain(mma_done, 0);
+      mma_commit(&mma_done[t]);
+      mbar_drain(&mma_done[t], 0);
     }
   } else if (warp < 4) {
     regs_dec<C::REGS_CONTROL>();
@@ -492,42 +533,45 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
         if (!ok) break;
       }
       const int32_t* table = p.page_table + w.b * p.pt_b;
-      for (int j = 0; ok && j < w.n_blocks; ++j, ++blk) {
-        const int k0 = (w.jb0 + j) * kBlockK;
-        // exponents of the block's largest scales: every warp looks at all 128 rows, four a lane
-        float s4[2][4], own[2];
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          own[kv] = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s4[kv][i] = 0.f;
-        }
-        {
-          const int key = k0 + 4 * lane;  // four keys share a page
-          const int phys = key < w.sk ? __ldg(table + (key >> p.log2_page)) : -1;
+      // a block's scales: every warp looks at all 128 rows of K and V, four a lane, one block ahead
+      float4 nk, nv;
+      auto fetch = [&](int j) {
+        const int key = (w.jb0 + j) * kBlockK + 4 * lane;  // four keys share a page
+        nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (j < w.n_blocks && key < w.sk) {
+          const int phys = __ldg(table + (key >> p.log2_page));
           if (phys >= 0 && phys < p.n_pages) {
             const int64_t at = ((static_cast<int64_t>(phys) * p.Hkv + w.kvh) << p.log2_page) + (key & (p.page_size - 1));
-            const float4 a = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
-            const float4 b = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
-            const float ks[4] = {a.x, a.y, a.z, a.w}, vs[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (key + i < w.sk) s4[0][i] = ks[i], s4[1][i] = vs[i];
+            nk = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
+            nv = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
           }
         }
+      };
+      fetch(0);
+      for (int j = 0; ok && j < w.n_blocks; ++j, ++blk) {
+        const int k0 = (w.jb0 + j) * kBlockK;
+        const int below = w.sk - (k0 + 4 * lane);  // rows past kv_len may hold any scale
         int e[2];
+        float own[2];
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const float m = fmaxf(fmaxf(s4[kv][0], s4[kv][1]), fmaxf(s4[kv][2], s4[kv][3]));
-          const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));  // scales are not negative
+          const float4 n = kv == 0 ? nk : nv;
+          const float s0 = below > 0 ? n.x : 0.f, s1 = below > 1 ? n.y : 0.f, s2 = below > 2 ? n.z : 0.f,
+                      s3 = below > 3 ? n.w : 0.f;
+          const unsigned top = __reduce_max_sync(
+              0xffffffffu, __float_as_uint(fmaxf(fmaxf(s0, s1), fmaxf(s2, s3))));  // scales are not negative
           e[kv] = max(static_cast<int>(top >> 23) - 127 - kBlockExpRoom, kMinBlockExp);
           // the scale of this thread's row: lane row / 4 of the warp holds it
           const int src = row >> 2;
-          const float a0 = __shfl_sync(0xffffffffu, s4[kv][0], src), a1 = __shfl_sync(0xffffffffu, s4[kv][1], src);
-          const float a2 = __shfl_sync(0xffffffffu, s4[kv][2], src), a3 = __shfl_sync(0xffffffffu, s4[kv][3], src);
+          const float a0 = __shfl_sync(0xffffffffu, s0, src), a1 = __shfl_sync(0xffffffffu, s1, src);
+          const float a2 = __shfl_sync(0xffffffffu, s2, src), a3 = __shfl_sync(0xffffffffu, s3, src);
           own[kv] = (row & 2) ? ((row & 1) ? a3 : a2) : ((row & 1) ? a1 : a0);
         }
-        if (tid == 128) blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
+        if (tid == 128) {
+          blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
+          mbar_arrive(&e_full[blk % kExpRing]);
+        }
+        fetch(j + 1);
         const bool live = k0 + row < w.sk;  // rows past kv_len may hold anything
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++g) {
@@ -572,12 +616,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
     const int row_tok = static_cast<int>(fast_div(static_cast<uint32_t>(row), p.div_group));
     const int row_head = row - row_tok * p.group;
     int sn = 0, on = 0;
-    int g = 0, blk = 0;
+    int blk = 0;
     bool ok = true;
     for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
       const PagedUnit w = paged_unit(p, item);
-      const int g0 = g, blk0 = blk;
-      g += 2 * w.n_blocks;
+      const int blk0 = blk;
       blk += w.n_blocks;
       const int n = w.n_t[t];
       if (n == 0) continue;
@@ -600,12 +643,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
               static_cast<uint32_t>(127 + static_cast<int>(q_exp[(t * 2 + (on & 1)) * 128 + row])) << 23);
         float blk_scale2 = row_scale2, shift = 0.f, unshift = 1.f;
         if constexpr (QUANT) {
-          const int gv = g0 + 2 * j + 1;  // V(j) converted: both exponents of the block are there
-          if (!mbar_wait_warp(&full[gv % NS], (gv / NS) & 1, abort_flag, p.status)) {
+          const int be = blk0 + j;
+          if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          const int2 e = blk_exp[(blk0 + j) % kExpRing];
+          const int2 e = blk_exp[be % kExpRing];
           blk_scale2 = fmaxf(blk_scale2 * __uint_as_float(static_cast<uint32_t>(127 + e.x) << 23), kMinBlkScale2);
           shift = static_cast<float>(e.y);
           unshift = __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
