@@ -11,10 +11,13 @@
 //     by the lanes of the producer warp side by side; pages past the cache read as zeros;
 //   * rows of the last page past kv_len may hold anything: their scores are masked, and their V rows
 //     are zeroed in shared memory before the P.V product (0 * NaN would poison it);
-//   * the key range of long sequences is cut into segments so that few query rows still occupy every
-//     SM; segments write partials (unnormalised O, max, sum) that a second kernel merges.  The cut
-//     is planned on the device, where the lengths are (paged_plan_kernel).
-// K and V take turns in one ring of equal slots: item 2 j is K(j), item 2 j + 1 is V(j).
+//   * all the work, every (query tile, KV head, key block), is one line that the SMs divide equally, so
+//     that few query rows over long caches, ragged batches and long chunks alike keep every SM busy to the end.
+//     A unit whose keys a cut divides writes partials (unnormalised O, max, sum) that a second
+//     kernel merges.  The cuts are planned on the device, where the lengths are (paged_plan_kernel).
+// K and V blocks take turns in one ring of equal slots, in the order of their use: K(0), then K(j) and
+// V(j-1) for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the
+// rest of the ring is loads in flight.
 //
 // Quantised pages.  Every e4m3 value is exact in fp16, so four converter warps turn a block's codes
 // into fp16 operands (one thread per row) and both products are fp16, whatever the query's type:
@@ -44,26 +47,36 @@ constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn mas
 constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
 constexpr int kExpRing = 16;        // blocks whose exponents are kept: more than the ring can run ahead
 
-template <bool QUANT, int D, int DV>
+// ONE: no sequence has more tokens than one query tile holds, so shared memory keeps one and the ring
+// takes the other's place (such calls are bound by reading the cache).
+template <bool QUANT, int D, int DV, bool ONE>
 struct PagedCfg {
   static constexpr int NCH_D = D / 64, NCH_V = DV / 64;
   static constexpr int Q_BYTES = kBlockQ * D * 2;
   static constexpr int K_BYTES = kBlockK * D * 2;
   static constexpr int V_BYTES = kBlockK * DV * 2;
   static constexpr int SLOT = K_BYTES > V_BYTES ? K_BYTES : V_BYTES;
-  static constexpr int SLOTS = D == 64 ? (QUANT ? 6 : 8) : D == 128 ? (QUANT ? 3 : 5) : 2;
+  static constexpr int Q_TILES = ONE ? 1 : 2;
+  static constexpr int SLOTS = D == 64 ? 8 : D == 128 ? (QUANT ? 4 : ONE ? 6 : 5) : (ONE && !QUANT ? 3 : 2);
   // raw codes: boxes of 128 (or 64) codes a row
   static constexpr int KW = D % 128 == 0 ? 128 : 64, VW = DV % 128 == 0 ? 128 : 64;
   static constexpr int RAW = QUANT ? kBlockK * D : 0;
-  static constexpr int RAWS = !QUANT ? 0 : D == 64 ? 8 : D == 128 ? 4 : 1;
+  static constexpr int RAWS = !QUANT ? 0 : D == 64 ? 6 : D == 128 ? (ONE ? 4 : 2) : (ONE ? 3 : 1);
   static constexpr int QK_STEPS = D / 16, PV_STEPS = kBlockK / 16;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_SLOT = OFF_Q + kTilesPerCta * Q_BYTES;
+  static constexpr int OFF_SLOT = OFF_Q + Q_TILES * Q_BYTES;
   static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
-  static constexpr int OFF_EXP = OFF_BAR + 640;                     // int2 [kExpRing]
-  static constexpr int OFF_QEXP = OFF_EXP + kExpRing * 8;           // int8 [2 tiles][2][128]
-  static constexpr int SMEM = OFF_QEXP + (QUANT ? 512 : 0) + 1024;  // 1 KB of slack for the alignment
+  static constexpr int BARS = D == 64 ? 768 : 640;
+  static constexpr int OFF_EXP = OFF_BAR + BARS;                    // int2 [kExpRing]
+  static constexpr int OFF_QEXP = OFF_EXP + (QUANT ? kExpRing * 8 : 0);  // int8 [2 tiles][2][128]
+  // pieces announced by the producer: more than it can run ahead of the slowest role.  With m pieces behind
+  // the one whose V is used up, 2 m - 1 items lie in the rings (each piece's V waits for its softmax).
+  static constexpr int PIECES = D == 64 ? 16 : 8;
+  static constexpr int OFF_PIECE = OFF_QEXP + (QUANT ? 512 : 0);
+  static constexpr int OFF_ML = OFF_PIECE + PIECES * 64;            // float2 [128]: max and sum of slot 1
+  static constexpr int SMEM = OFF_ML + 1024;
+  static_assert((SLOTS + RAWS) / 2 + 2 <= PIECES, "the piece ring holds what the producer announces");
   // warpgroups: control (producer, MMA, helpers), converters (quantised), two softmax
   static constexpr int THREADS = QUANT ? 512 : 384;
   static constexpr int SOFTMAX_WARP = QUANT ? 8 : 4;
@@ -78,60 +91,68 @@ struct PagedCfg {
   static_assert(Q_BYTES % 1024 == 0 && SLOT % 1024 == 0 && RAW % 1024 == 0, "1 KB tile alignment");
 };
 
-// One work unit: two query tiles (2 * tok_tile tokens of one sequence, the G heads of one KV head)
-// against the key blocks [jb0, jb0 + n_blocks) of segment `seg`.
-struct PagedUnit {
-  int b, kvh, tok0;
-  int n_t[kTilesPerCta];
-  int n_blocks, jb0;
-  int slot;                // partial slot, or -1: the unit stores O itself
+// One piece of a work unit: two query tiles (2 * tok_tile tokens of one sequence, the G heads of one KV
+// head) against the key blocks [jb0, jb0 + n_blocks).  There are two S / O accumulators ("slots").
+// Normally slot t serves query tile t, and both read every block.  A unit whose tokens all lie in tile
+// 0 ("alternating") gives the even blocks to slot 0 and the odd ones to slot 1, so that one slot's
+// softmax runs beside the other's MMAs there too; slot 0's warps merge the two at the end.
+struct PagedPiece {
+  int b, kvh, tok0, jb0;
+  int n_blocks;            // 0: no more pieces
+  int n_s[2];              // blocks of each slot
+  int slot;                // partial slot, or -1: the whole unit, which stores O itself
   int q_off, n, len, sk;
+  int alt;                 // alternating
+  int pad[3];
 };
+static_assert(sizeof(PagedPiece) == 64, "the producer announces a piece in 64 bytes");
 
-__device__ __forceinline__ PagedUnit paged_unit(const PagedParams& p, int unit) {
-  PagedUnit w;
-  const int32_t* prefix = p.plan + kPlanHeader;
-  const int seg_blocks = ld_dep(p.plan + kPlanSeg);
-  int lo = 0, hi = p.B;  // prefix[lo] <= unit < prefix[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (ld_dep(prefix + mid) <= unit) lo = mid; else hi = mid;
+// The pieces of this CTA's stretch of the line, in order (the producer's walk; the other roles read
+// what it announces).
+struct PagedWalk {
+  int tile, kvh, off, first;
+  int4 end;
+
+  __device__ __forceinline__ explicit PagedWalk(const PagedParams& p) : first(1) {
+    const int n = ld_dep(&p.plan.head->n_ctas);
+    int4 c = make_int4(0, 0, 0, 0);
+    end = c;
+    if (static_cast<int>(blockIdx.x) < n) {
+      c = ld_dep(p.plan.cuts + blockIdx.x);
+      end = ld_dep(p.plan.cuts + blockIdx.x + 1);
+    }
+    tile = c.x, kvh = c.y, off = c.z;
   }
-  w.b = lo;
-  w.q_off = __ldg(p.cu_q + lo);
-  w.n = __ldg(p.cu_q + lo + 1) - w.q_off;
-  w.len = __ldg(p.kv_len + lo);
-  w.sk = min(max(w.len, 0), p.max_kv);
-  // local order: segment, work tile (longest first), KV head.  The SMs that run at one time then
-  // stream the same keys for different tiles, which L2 serves.
-  const int local = unit - ld_dep(prefix + lo);
-  const int rest = static_cast<int>(fast_div(static_cast<uint32_t>(local), p.div_hkv));
-  w.kvh = local - rest * p.Hkv;
-  const int tok_unit = kTilesPerCta * p.tok_tile;
-  const int tiles = (w.n + tok_unit - 1) / tok_unit;
-  const int seg = rest / tiles;
-  const int rank = rest - seg * tiles;
-  const int tile = tiles - 1 - rank;
-  w.tok0 = tile * tok_unit;
-  w.jb0 = seg * seg_blocks;
-  w.n_blocks = 0;
+  __device__ __forceinline__ PagedPiece next(const PagedParams& p) {
+    PagedPiece w{};
+    if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
+    const int2 at = ld_dep(p.plan.tiles + tile);
+    w.b = at.x;
+    w.kvh = kvh;
+    w.q_off = __ldg(p.cu_q + w.b);
+    w.n = __ldg(p.cu_q + w.b + 1) - w.q_off;
+    w.len = __ldg(p.kv_len + w.b);
+    w.sk = min(max(w.len, 0), p.max_kv);
+    w.tok0 = at.y * kTilesPerCta * p.tok_tile;
+    w.jb0 = off;
+    int blocks[kTilesPerCta];
 #pragma unroll
-  for (int t = 0; t < kTilesPerCta; ++t) {
-    const int blocks = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, tile * kTilesPerCta + t);
-    w.n_t[t] = min(max(blocks - w.jb0, 0), seg_blocks);
-    w.n_blocks = max(w.n_blocks, w.n_t[t]);
+    for (int t = 0; t < kTilesPerCta; ++t)
+      blocks[t] = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, at.y * kTilesPerCta + t);
+    const int all = max(blocks[0], blocks[1]);
+    const int stop = (tile == end.x && kvh == end.y) ? end.z : all;
+    w.n_blocks = stop - off;
+    w.alt = blocks[1] == 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      w.n_s[t] = w.alt ? (w.n_blocks + 1 - t) / 2 : min(max(blocks[t] - off, 0), w.n_blocks);
+    w.slot = (off > 0 || stop < all) ? 2 * static_cast<int>(blockIdx.x) + 1 - first : -1;
+    first = 0;
+    off = 0;
+    if (++kvh == p.Hkv) kvh = 0, ++tile;
+    return w;
   }
-  const int32_t* slots = prefix + p.B + 1;
-  const int s0 = ld_dep(slots + lo);
-  w.slot = ld_dep(slots + lo + 1) > s0 ? s0 + local : -1;
-  return w;
-}
-
-// The k-th unit of this CTA: snake order over the longest-first list.
-__device__ __forceinline__ int paged_nth(int k) {
-  const int G = gridDim.x;
-  return (k & 1) ? (k + 1) * G - 1 - (int)blockIdx.x : k * G + (int)blockIdx.x;
-}
+};
 
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -140,58 +161,83 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 }
 
 // Converts row r of a raw tile (boxes of W codes a row, swizzled) into the 128-byte-swizzled fp16
-// chunks of 64 columns that the MMAs read, times the pair factor f.
+// chunks of 64 columns that the MMAs read, times the pair factor f.  One thread per row: both the reads
+// and the writes of eight neighbouring rows fall on all banks.  The reads of a half row are issued
+// together, as one converting warp per scheduler has nobody to hide their latency.
 template <int COLS, int W>
 __device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int r, uint32_t f) {
   const int x = r & 7;
+  constexpr int UNITS = COLS / 16, BATCH = 4;
 #pragma unroll
-  for (int u = 0; u < COLS / 16; ++u) {  // 16 codes
-    const int box = u / (W / 16), uu = u % (W / 16);
-    const int sw = W == 128 ? (uu ^ x) : (uu ^ ((r >> 1) & 3));
-    const uint4 c = *reinterpret_cast<const uint4*>(raw + box * kBlockK * W + r * W + (sw << 4));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-    uint32_t h[8];
+  for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
+    uint4 c[BATCH];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e4m3x4_to_f16x4(w[i], h[2 * i], h[2 * i + 1]);
-      h[2 * i] = mul_f16x2(h[2 * i], f);
-      h[2 * i + 1] = mul_f16x2(h[2 * i + 1], f);
+    for (int i = 0; i < BATCH; ++i) {
+      const int u = u0 + i, box = u / (W / 16), uu = u % (W / 16);
+      const int sw = W == 128 ? (uu ^ x) : (uu ^ ((r >> 1) & 3));
+      c[i] = *reinterpret_cast<const uint4*>(raw + box * kBlockK * W + r * W + (sw << 4));
     }
-    uint8_t* d = dst + (u / 4) * kBlockK * 128 + r * 128;
-    const int v = 2 * (u % 4);
-    *reinterpret_cast<uint4*>(d + ((v ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<uint4*>(d + (((v + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int u = u0 + i;
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      uint32_t h[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        e4m3x4_to_f16x4(w[q], h[2 * q], h[2 * q + 1]);
+        h[2 * q] = mul_f16x2(h[2 * q], f);
+        h[2 * q + 1] = mul_f16x2(h[2 * q + 1], f);
+      }
+      uint8_t* d = dst + (u / 4) * kBlockK * 128 + r * 128;
+      const int v = 2 * (u % 4);
+      *reinterpret_cast<uint4*>(d + ((v ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(d + (((v + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
   }
 }
 
-// Barriers (phases continue from unit to unit):
-//   q_full[t] / q_empty[t]: Q tile t landed / its last QK MMA finished
+// One arrival for a warp whose lanes have all done their part (their fences included).
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Barriers (phases continue from piece to piece; the arrivals of warps are one each):
+//   piece[i % PIECES]     : the producer announced piece i
+//   q_full[t] / q_empty[t]: Q tile t landed / its last QK MMA finished (q_empty[2]: slot 1's last one
+//                           on tile 0 in an alternating piece)
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
-//   full[s] / empty[s]    : ring slot s holds its item / both issuers' MMAs that read it finished
+//   full[s] / empty[s]    : ring slot s holds its item / both issuers are done with it
 //   raw_full / raw_empty  : quantised pages: codes landed / read by the converters
 //   e_full[i % 16]        : quantised pages: the exponents of block i are there
 //   turn[t]               : issuer t may issue (both tiles active)
 //   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
 //                           then zeroes those rows and completes full[s] in the copy's place
-//   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels
-template <bool BF16, bool QUANT, int D, int DV>
-__global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
+//   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels, per slot
+//   ml_full               : alternating pieces: slot 1's max and sum are there
+template <bool BF16, bool QUANT, int D, int DV, bool ONE>
+__global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
-  using C = PagedCfg<QUANT, D, DV>;
+  using C = PagedCfg<QUANT, D, DV, ONE>;
   constexpr int NS = C::SLOTS;
   constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
   constexpr bool CONVERT_Q = QUANT && BF16;
   constexpr bool F16_MATH = QUANT || !BF16;
-  extern __shared__ uint8_t paged_smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(paged_smem_raw) + 1023) & ~uintptr_t(1023));
+  // D = 128 fills the shared memory, without room to align the window by hand
+  extern __shared__ __align__(1024) uint8_t paged_smem[];
+  uint8_t* smem = paged_smem;
+  if (smem_u32(smem) & 1023u) {  // never: nothing static lies in front of it
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusTimeout);
+    return;
+  }
   uint8_t* sQ = smem + C::OFF_Q;
   uint8_t* sKV = smem + C::OFF_SLOT;
   uint8_t* sRaw = smem + C::OFF_RAW;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;              // [2]
-  uint64_t* q_empty = q_full + 2;       // [2]
-  uint64_t* q_ready = q_empty + 2;      // [2]
+  uint64_t* q_empty = q_full + 2;       // [3]
+  uint64_t* q_ready = q_empty + 3;      // [2]
   uint64_t* s_full = q_ready + 2;       // [2]
   uint64_t* p_half = s_full + 2;        // [2]
   uint64_t* p_full = p_half + 2;        // [2]
@@ -205,11 +251,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
   uint64_t* raw_full = empty + NS;      // [NR]
   uint64_t* raw_empty = raw_full + NR;  // [NR]
   uint64_t* e_full = raw_empty + NR;    // [kExpRing]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(e_full + kExpRing);
+  uint64_t* piece = e_full + kExpRing;  // [PIECES]
+  uint64_t* ml_full = piece + C::PIECES;  // [1]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ml_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int2* blk_exp = reinterpret_cast<int2*>(smem + C::OFF_EXP);
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
-  static_assert((20 + kFixRing + kExpRing + 2 * NS + 2 * NR) * 8 + 8 <= 640, "barriers fit their area");
+  PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::OFF_PIECE);
+  float2* ml_x = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [128]
+  static_assert((22 + kFixRing + kExpRing + 2 * NS + 2 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -219,26 +269,28 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
   if (tid == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1);
-      mbar_init(&q_empty[t], 1);
-      mbar_init(&q_ready[t], 128);
+      mbar_init(&q_ready[t], 4);
       mbar_init(&s_full[t], 1);
-      mbar_init(&p_half[t], 128);
-      mbar_init(&p_full[t], 128);
+      mbar_init(&p_half[t], 4);
+      mbar_init(&p_full[t], 4);
       mbar_init(&o_full[t], 1);
-      mbar_init(&o_empty[t], 128);
+      mbar_init(&o_empty[t], 4);
       mbar_init(&mma_done[t], 1);
       mbar_init(&turn[t], 1);
     }
+    mbar_init(ml_full, 4);
+    for (int t = 0; t < 3; ++t) mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kFixRing; ++s) mbar_init(&v_ragged[s], 1);
     for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], QUANT ? 128 : 1);
+      mbar_init(&full[s], QUANT ? 4 : 1);
       mbar_init(&empty[s], 2);
     }
     for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 1);
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);
-      mbar_init(&raw_empty[s], 128);
+      mbar_init(&raw_empty[s], 4);
     }
+    for (int s = 0; s < C::PIECES; ++s) mbar_init(&piece[s], 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -251,7 +303,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   pdl_wait();  // the plan comes from the kernel launched before
-  const int n_units = ld_dep(p.plan + kPlanUnits);
+  // the next announced piece, for the other roles
+  int n_piece = 0;
+  auto next_piece = [&](bool& ok) -> const PagedPiece& {
+    const PagedPiece& w = pieces[n_piece % C::PIECES];
+    ok = mbar_wait(&piece[n_piece % C::PIECES], (n_piece / C::PIECES) & 1, abort_flag, p.status);
+    ++n_piece;
+    return w;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer (one warp)
@@ -271,15 +330,23 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
     uint64_t* ld_full = QUANT ? raw_full : full;
     uint64_t* ld_empty = QUANT ? raw_empty : empty;
     const int q_tx = p.tok_tile * p.group * D * 2;
-    int qn[2] = {0, 0};
-    int g = 0, nr = 0;  // items, and ragged V blocks, issued
+    PagedWalk walk(p);
+    int qn[2] = {0, 0}, alts = 0;
+    bool last_alt = false;  // tile 0's last piece was alternating, with blocks for slot 1
+    int g = 0, nr = 0;      // items, and ragged V blocks, issued
     bool ok = true;
-    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
-      const PagedUnit w = paged_unit(p, item);
-      if (w.n_blocks == 0) continue;  // a segment past its tile's keys: skipped by every role
+    while (ok) {
+      const PagedPiece w = walk.next(p);
+      if (lane == 0) {
+        pieces[n_piece % C::PIECES] = w;
+        mbar_arrive(&piece[n_piece % C::PIECES]);
+      }
+      ++n_piece;
+      if (w.n_blocks == 0) break;
       for (int t = 0; t < kTilesPerCta && ok; ++t) {
-        if (w.n_t[t] == 0) continue;
-        if (qn[t] > 0 && !mbar_wait_warp(&q_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) {
+        if (t == 0 ? w.n_s[0] == 0 : (w.alt || w.n_s[1] == 0)) continue;
+        if ((qn[t] > 0 && !mbar_wait_warp(&q_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) ||
+            (t == 0 && last_alt && !mbar_wait_warp(&q_empty[2], (alts - 1) & 1, abort_flag, p.status))) {
           ok = false;
           break;
         }
@@ -290,25 +357,38 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
                         w.q_off + w.tok0 + t * p.tok_tile);
         }
         ++qn[t];
+        if (t == 0) {
+          last_alt = w.alt && w.n_s[1] > 0;
+          alts += last_alt;
+        }
       }
       const int32_t* table = p.page_table + w.b * p.pt_b;
       const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
       const int sub = lane & 7;                                  // page of the block: lane % 8 < nsub
-      for (int j = 0; ok && j < w.n_blocks; ++j) {
-        const int key = (w.jb0 + j) * kBlockK + sub * rows;
-        const int lp = key >> p.log2_page, prow = key & (p.page_size - 1);
-        int phys = p.n_pages;  // outside the pool: zeros
-        if (sub < nsub && lp < used) phys = __ldg(table + lp);
+      int phys_k = p.n_pages, row_k = 0;  // page and row of this lane's box; outside the pool: zeros
+      for (int j = 0; ok && j <= w.n_blocks; ++j) {
+        const int phys_v = phys_k, row_v = row_k;
+        if (j < w.n_blocks) {
+          const int key = (w.jb0 + j) * kBlockK + sub * rows;
+          const int lp = key >> p.log2_page;
+          row_k = key & (p.page_size - 1);
+          phys_k = p.n_pages;
+          if (sub < nsub && lp < used) phys_k = __ldg(table + lp);
+        }
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++g) {
+        for (int kv = 0; kv < 2; ++kv) {
+          if (kv == 0 ? j == w.n_blocks : j == 0) continue;  // K(j), then V(j-1)
           const int s = g % NL, r = g / NL;
           if (r > 0 && !mbar_wait_warp(&ld_empty[s], (r - 1) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          if (p.stall_first_stage && g == 0) continue;  // test hook: slot 0 never fills
+          if (p.stall_first_stage && g == 0) {  // test hook: slot 0 never fills
+            ++g;
+            continue;
+          }
           uint64_t* bar = &ld_full[s];
-          if (!QUANT && kv == 1 && (w.jb0 + j + 1) * kBlockK > w.sk) {
+          if (!QUANT && kv == 1 && (w.jb0 + j) * kBlockK > w.sk) {
             bar = &v_ragged[nr % kFixRing];
             ++nr;
           }
@@ -319,7 +399,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
           const int part = lane >> 3;  // column chunk
           if (sub < nsub && part < parts)
             tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, kv == 0 ? &tm_k : &tm_v, bar,
-                        part * (kv == 0 ? KCOLS : VCOLS), w.kvh, prow, phys);
+                        part * (kv == 0 ? KCOLS : VCOLS), w.kvh, kv == 0 ? row_k : row_v, kv == 0 ? phys_k : phys_v);
+          ++g;
         }
       }
     }
@@ -344,7 +425,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       constexpr uint32_t idesc_qk = make_idesc(fmt, fmt, 0, 0, kBlockQ, kBlockK);
       constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, 0, 1, kBlockQ, DV);
       const int t = warp >> 1;
-      const uint64_t dq0 = make_smem_desc(smem_u32(sQ + t * C::Q_BYTES), 16, 1024, kSwizzle128B);
+      const uint64_t dq0 = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
       const uint64_t dk0 = make_smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
       const uint64_t dv0 = make_smem_desc(smem_u32(sKV), kBlockK * 128, 1024, kSwizzle128B);
       const uint32_t q_lo = static_cast<uint32_t>(dq0), q_hi = static_cast<uint32_t>(dq0 >> 32);
@@ -352,7 +433,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       const uint32_t v_lo = static_cast<uint32_t>(dv0), v_hi = static_cast<uint32_t>(dv0 >> 32);
       const uint32_t tS = tmem_base + t * 128;
       const uint32_t tO = tmem_base + 256 + t * 128;
-      int qn = 0, pn = 0;         // units and blocks of this tile so far
+      int qn[2] = {0, 0};         // Q tiles loaded so far
+      int on = 0, pn = 0;         // pieces and blocks of this slot so far
       uint32_t turns = 1 - t;     // parity of the turn barrier's next phase; tile 0 begins
       int s = 0;                  // ring slot of the next item and the parity of its phase
       uint32_t ph = 0;
@@ -360,32 +442,45 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       auto next = [&]() {
         if (++s == NS) s = 0, ph ^= 1u;
       };
-      for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
-        const PagedUnit w = paged_unit(p, item);
-        if (w.n_blocks == 0) continue;
-        const int n = w.n_t[t];
-        const bool both = w.n_t[0] > 0 && w.n_t[1] > 0;
-        if (n > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[t] : &q_full[t], qn & 1, abort_flag, p.status);
-        // step j: O += P(j-1) V(j-1), then S = Q K(j)^T: the items in ring order.  Items that this
-        // tile does not read are seen and passed on.
-        for (int j = 0; ok && j <= w.n_blocks; ++j) {
-          const bool pv = j >= 1 && j <= n, qk = j < n;
-          const int vs = s;  // slot of V(j-1)
-          if (j >= 1) {
-            if (!mbar_wait(&full[s], ph, abort_flag, p.status)) {
+      while (true) {
+        const PagedPiece& w = next_piece(ok);
+        const int nb = ok ? w.n_blocks : 0;
+        if (nb == 0) break;
+        const int n = w.n_s[t];
+        const bool alt = w.alt != 0, both = !alt && w.n_s[0] > 0 && w.n_s[1] > 0;
+        const int qt = alt ? 0 : t;  // query tile of this slot
+        if (n > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[qt] : &q_full[qt], qn[qt] & 1, abort_flag, p.status);
+        if (w.n_s[0] > 0) ++qn[0];
+        if (!alt && w.n_s[1] > 0) ++qn[1];
+        const uint32_t dq = q_lo + static_cast<uint32_t>((qt * C::Q_BYTES) >> 4);
+        // Step j takes K(j) and V(j-1) from the ring: O += P(j-1) V(j-1), then S = Q K(j)^T.  In an
+        // alternating piece block j is this slot's if j % 2 == t, and S = Q K(j)^T follows
+        // O += P(j-2) V(j-2).  An item that this slot does not read is seen and passed on.
+        int vs = 0;  // slot of the V to be used next
+        for (int j = 0; ok && j <= nb + (alt ? 1 : 0); ++j) {
+          const bool qk = alt ? j < nb && (j & 1) == t : j < n;
+          const bool pv = alt ? j >= 2 && (j & 1) == t : j >= 1 && j <= n;
+          const int ks = s;
+          if (j < nb) {
+            if (!mbar_wait(&full[ks], ph, abort_flag, p.status)) {
               ok = false;
               break;
             }
+            if (!qk) mbar_arrive(&empty[ks]);
             next();
-            if (!pv) mbar_arrive(&empty[vs]);
           }
-          const int ks = s;  // slot of K(j)
-          if (both && j < w.n_blocks && !mbar_wait(&full[ks], ph, abort_flag, p.status)) {
-            ok = false;
-            break;
+          const bool v_here = j >= 1 && j <= nb;
+          if (v_here && !alt) {
+            vs = s;
+            if (!mbar_wait(&full[vs], ph, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            if (!pv) mbar_arrive(&empty[vs]);
+            next();
           }
           if (pv) {
-            if (j == 1 && qn > 0 && !mbar_wait(&o_empty[t], (qn - 1) & 1, abort_flag, p.status)) {
+            if ((alt ? j < 4 : j == 1) && on > 0 && !mbar_wait(&o_empty[t], (on - 1) & 1, abort_flag, p.status)) {
               ok = false;
               break;
             }
@@ -404,13 +499,13 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
           }
           if (pv) {
             const uint32_t dv = v_lo + static_cast<uint32_t>((vs * C::SLOT) >> 4);
-            const uint32_t acc0 = (j > 1) ? 1u : 0u;
+            const uint32_t acc0 = (alt ? j >= 4 : j > 1) ? 1u : 0u;
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < C::PV_STEPS / 2; ++kk)
               mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv,
                          kk > 0 ? 1u : acc0);
-            // a tile alone starts on the first half of P while the second is computed
+            // without turns, P.V starts on the first half of P while the second is computed
             if (!both) {
               if (!mbar_wait(&p_full[t], pn & 1, abort_flag, p.status)) {
                 ok = false;
@@ -422,35 +517,39 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
             for (int kk = C::PV_STEPS / 2; kk < C::PV_STEPS; ++kk)
               mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv, 1u);
             ++pn;
-          }
-          if (!both && j < w.n_blocks && !mbar_wait(&full[ks], ph, abort_flag, p.status)) {
-            ok = false;
-            break;
+            if (!both) mma_commit(&empty[vs]);
           }
           if (qk) {
             tc_fence_after();
             const uint32_t dk = k_lo + static_cast<uint32_t>((ks * C::SLOT) >> 4);
-            if (!both && pv) mma_commit(&empty[vs]);
 #pragma unroll
             for (int kk = 0; kk < C::QK_STEPS; ++kk) {
               const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
-              mma_f16_ss(tS, q_lo + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+              mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
             }
           }
           if (both) mbar_arrive(&turn[1 - t]);
-          if (qk) mma_commit(&s_full[t]);
-          if (pv && (both || !qk)) mma_commit(&empty[vs]);
-          if (j < w.n_blocks) {
-            if (qk)
-              mma_commit(&empty[ks]);
+          if (qk) {
+            mma_commit(&s_full[t]);
+            mma_commit(&empty[ks]);
+          }
+          if (pv && both) mma_commit(&empty[vs]);
+          if (pv && (alt ? j >= nb : j == n)) mma_commit(&o_full[t]);
+          if (qk && (alt ? j + 2 >= nb : j == n - 1)) mma_commit(&q_empty[alt && t == 1 ? 2 : t]);
+          if (v_here && alt) {  // V(j-1), behind this step's MMAs
+            if (!mbar_wait(&full[s], ph, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+            if (((j - 1) & 1) == t)
+              vs = s;
             else
-              mbar_arrive(&empty[ks]);
+              mbar_arrive(&empty[s]);
             next();
           }
-          if (pv && j == n) mma_commit(&o_full[t]);
-          if (qk && j == n - 1) mma_commit(&q_empty[t]);
         }
-        if (n > 0) ++qn;
+        if (!ok) break;
+        if (n > 0) ++on;
       }
       // every MMA issued so far has finished before tensor memory is released
       mma_commit(&mma_done[t]);
@@ -462,10 +561,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       // ---------------------------------------------------------- V rows past kv_len -> 0 (one warp)
       if (warp == 2) {
         int g = 0, nr = 0;
-        for (int k = 0, item = paged_nth(0); item < n_units; item = paged_nth(++k)) {
-          const PagedUnit w = paged_unit(p, item);
-          if (w.n_blocks == 0) continue;
-          const int last = w.n_blocks - 1;  // only a unit's last block can end past kv_len
+        bool ok = true;
+        while (true) {
+          const PagedPiece& w = next_piece(ok);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok || w.n_blocks == 0) break;
+          const int last = w.n_blocks - 1;  // only the last block can end past kv_len
           const int live = w.sk - (w.jb0 + last) * kBlockK;
           if (live < kBlockK) {
             const int s = (g + 2 * last + 1) % NS;
@@ -492,12 +593,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
     int qn[2] = {0, 0};
     int g = 0, blk = 0;
     bool ok = true;
-    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
-      const PagedUnit w = paged_unit(p, item);
-      if (w.n_blocks == 0) continue;
+    while (true) {
+      const PagedPiece& w = next_piece(ok);
+      ok = __all_sync(0xffffffffu, ok);
+      const int nb = ok ? w.n_blocks : 0;
+      if (nb == 0) break;
+      const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
       if constexpr (CONVERT_Q) {
         for (int t = 0; t < kTilesPerCta && ok; ++t) {
-          if (w.n_t[t] == 0) continue;
+          if (t == 0 ? w.n_s[0] == 0 : (w.alt || w.n_s[1] == 0)) continue;
           if (!mbar_wait_warp(&q_full[t], qn[t] & 1, abort_flag, p.status)) {
             ok = false;
             break;
@@ -527,7 +631,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
           q_exp[(t * 2 + (qn[t] & 1)) * 128 + row] =
               static_cast<int8_t>(static_cast<int>(__float_as_uint(back) >> 23) - 127);
           fence_proxy_async_smem();
-          mbar_arrive(&q_ready[t]);
+          warp_arrive(&q_ready[t], lane);
           ++qn[t];
         }
         if (!ok) break;
@@ -536,61 +640,68 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
       // a block's scales: every warp looks at all 128 rows of K and V, four a lane, one block ahead
       float4 nk, nv;
       auto fetch = [&](int j) {
-        const int key = (w.jb0 + j) * kBlockK + 4 * lane;  // four keys share a page
+        const int key = (jb0 + j) * kBlockK + 4 * lane;  // four keys share a page
         nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < w.n_blocks && key < w.sk) {
+        if (j < nb && key < sk) {
           const int phys = __ldg(table + (key >> p.log2_page));
           if (phys >= 0 && phys < p.n_pages) {
-            const int64_t at = ((static_cast<int64_t>(phys) * p.Hkv + w.kvh) << p.log2_page) + (key & (p.page_size - 1));
+            const int64_t at = ((static_cast<int64_t>(phys) * p.Hkv + kvh) << p.log2_page) + (key & (p.page_size - 1));
             nk = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
             nv = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
           }
         }
       };
       fetch(0);
-      for (int j = 0; ok && j < w.n_blocks; ++j, ++blk) {
-        const int k0 = (w.jb0 + j) * kBlockK;
-        const int below = w.sk - (k0 + 4 * lane);  // rows past kv_len may hold any scale
-        int e[2];
-        float own[2];
+      uint32_t f_v = 0;  // factor of this thread's V row, one step behind
+      for (int j = 0; ok && j <= nb; ++j) {
+        const uint32_t f_prev = f_v;
+        uint32_t f_k = 0;
+        if (j < nb) {
+          const int below = sk - ((jb0 + j) * kBlockK + 4 * lane);  // rows past kv_len may hold any scale
+          int e[2];
+          uint32_t f[2];
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const float4 n = kv == 0 ? nk : nv;
+            const float s0 = below > 0 ? n.x : 0.f, s1 = below > 1 ? n.y : 0.f, s2 = below > 2 ? n.z : 0.f,
+                        s3 = below > 3 ? n.w : 0.f;
+            const unsigned top = __reduce_max_sync(
+                0xffffffffu, __float_as_uint(fmaxf(fmaxf(s0, s1), fmaxf(s2, s3))));  // scales are not negative
+            e[kv] = max(static_cast<int>(top >> 23) - 127 - kBlockExpRoom, kMinBlockExp);
+            // the scale of this thread's row: lane row / 4 of the warp holds it
+            const int src = row >> 2;
+            const float a0 = __shfl_sync(0xffffffffu, s0, src), a1 = __shfl_sync(0xffffffffu, s1, src);
+            const float a2 = __shfl_sync(0xffffffffu, s2, src), a3 = __shfl_sync(0xffffffffu, s3, src);
+            const float own = (row & 2) ? ((row & 1) ? a3 : a2) : ((row & 1) ? a1 : a0);
+            // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+            const float r = own * __uint_as_float(static_cast<uint32_t>(127 - e[kv]) << 23);
+            f[kv] = pack_f16x2(r, r);
+          }
+          f_k = f[0], f_v = f[1];
+          if (tid == 128) {
+            blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
+            mbar_arrive(&e_full[blk % kExpRing]);
+          }
+          ++blk;
+          fetch(j + 1);
+        }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          const float4 n = kv == 0 ? nk : nv;
-          const float s0 = below > 0 ? n.x : 0.f, s1 = below > 1 ? n.y : 0.f, s2 = below > 2 ? n.z : 0.f,
-                      s3 = below > 3 ? n.w : 0.f;
-          const unsigned top = __reduce_max_sync(
-              0xffffffffu, __float_as_uint(fmaxf(fmaxf(s0, s1), fmaxf(s2, s3))));  // scales are not negative
-          e[kv] = max(static_cast<int>(top >> 23) - 127 - kBlockExpRoom, kMinBlockExp);
-          // the scale of this thread's row: lane row / 4 of the warp holds it
-          const int src = row >> 2;
-          const float a0 = __shfl_sync(0xffffffffu, s0, src), a1 = __shfl_sync(0xffffffffu, s1, src);
-          const float a2 = __shfl_sync(0xffffffffu, s2, src), a3 = __shfl_sync(0xffffffffu, s3, src);
-          own[kv] = (row & 2) ? ((row & 1) ? a3 : a2) : ((row & 1) ? a1 : a0);
-        }
-        if (tid == 128) {
-          blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
-          mbar_arrive(&e_full[blk % kExpRing]);
-        }
-        fetch(j + 1);
-        const bool live = k0 + row < w.sk;  // rows past kv_len may hold anything
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv, ++g) {
+          if (kv == 0 ? j == nb : j == 0) continue;  // K(j), then V(j-1)
           const int rs = g % NR, s = g % NS;
-          // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
-          const float f32 = own[kv] * __uint_as_float(static_cast<uint32_t>(127 - e[kv]) << 23);
-          const uint32_t f = pack_f16x2(f32, f32);
           if (!mbar_wait_warp(&raw_full[rs], (g / NR) & 1, abort_flag, p.status) ||
               (g >= NS && !mbar_wait_warp(&empty[s], (g / NS - 1) & 1, abort_flag, p.status))) {
             ok = false;
             break;
           }
+          ++g;
           uint8_t* dst = sKV + s * C::SLOT;
-          if (live) {
+          if ((jb0 + j - kv) * kBlockK + row < sk) {
             if (kv == 0)
-              convert_row<D, C::KW>(sRaw + rs * C::RAW, dst, row, f);
+              convert_row<D, C::KW>(sRaw + rs * C::RAW, dst, row, f_k);
             else
-              convert_row<DV, C::VW>(sRaw + rs * C::RAW, dst, row, f);
-          } else {
+              convert_row<DV, C::VW>(sRaw + rs * C::RAW, dst, row, f_prev);
+          } else {  // rows past kv_len may hold anything
 #pragma unroll
             for (int c = 0; c < (kv == 0 ? C::NCH_D : C::NCH_V); ++c)
 #pragma unroll
@@ -598,10 +709,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
                 *reinterpret_cast<uint4*>(dst + c * kBlockK * 128 + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
-          mbar_arrive(&full[s]);
-          mbar_arrive(&raw_empty[rs]);
+          warp_arrive(&full[s], lane);
+          if (lane == 0) mbar_arrive(&raw_empty[rs]);
         }
       }
+      if (!ok) break;
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -615,32 +727,46 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
     // (token, head) of this thread's row
     const int row_tok = static_cast<int>(fast_div(static_cast<uint32_t>(row), p.div_group));
     const int row_head = row - row_tok * p.group;
-    int sn = 0, on = 0;
-    int blk = 0;
+    int sn = 0, on[2] = {0, 0};  // S blocks of this slot; pieces of each slot
+    int qn[2] = {0, 0};          // Q tiles loaded
+    int blk = 0, alts = 0;
     bool ok = true;
-    for (int k = 0, item = paged_nth(0); ok && item < n_units; item = paged_nth(++k)) {
-      const PagedUnit w = paged_unit(p, item);
+    while (true) {
+      const PagedPiece& w = next_piece(ok);
+      ok = __all_sync(0xffffffffu, ok);
+      const int nb = ok ? w.n_blocks : 0;
+      if (nb == 0) break;
       const int blk0 = blk;
-      blk += w.n_blocks;
-      const int n = w.n_t[t];
-      if (n == 0) continue;
-      const int tok = w.tok0 + t * p.tok_tile + row_tok;
+      blk += nb;
+      const int n = w.n_s[t], n_other = w.n_s[1 - t];
+      const bool alt = w.alt != 0, merge = alt && w.n_s[1] > 0;
+      const int qt = alt ? 0 : t;
+      const int q_par = qn[qt] & 1;
+      if (w.n_s[0] > 0) ++qn[0];
+      if (!alt && w.n_s[1] > 0) ++qn[1];
+      if (n == 0) {
+        if (n_other > 0) ++on[1 - t];
+        continue;
+      }
+      const int tok = w.tok0 + qt * p.tok_tile + row_tok;
       const bool row_valid = row_tok < p.tok_tile && tok < w.n;
       // keys this row sees, and those every row of the tile sees
       const int lim_row = p.causal ? min(w.sk, w.len - w.n + tok + 1) : w.sk;
-      const int lim_all = p.causal ? min(w.sk, w.len - w.n + w.tok0 + t * p.tok_tile + 1) : w.sk;
+      const int lim_all = p.causal ? min(w.sk, w.len - w.n + w.tok0 + qt * p.tok_tile + 1) : w.sk;
+      const int jb0 = w.jb0, step = alt ? 2 : 1, j0 = alt ? t : 0;  // this slot's blocks: j0 + i * step
       float row_scale2 = p.scale2;
       float m_used = -INFINITY;
       float l = 0.f;
-      for (int j = 0; j < n; ++j, ++sn) {
+      for (int i = 0; i < n; ++i, ++sn) {
+        const int j = j0 + i * step;
         if (!mbar_wait_warp(&s_full[t], sn & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
         // the query's exponent was stored before q_ready, which the MMAs behind s_full waited for
-        if (CONVERT_Q && j == 0)
+        if (CONVERT_Q && i == 0)
           row_scale2 *= __uint_as_float(
-              static_cast<uint32_t>(127 + static_cast<int>(q_exp[(t * 2 + (on & 1)) * 128 + row])) << 23);
+              static_cast<uint32_t>(127 + static_cast<int>(q_exp[(qt * 2 + q_par) * 128 + row])) << 23);
         float blk_scale2 = row_scale2, shift = 0.f, unshift = 1.f;
         if constexpr (QUANT) {
           const int be = blk0 + j;
@@ -674,7 +800,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
             s[96 + c] = __uint_as_float(r3[c]);
           }
         }
-        const int k0 = (w.jb0 + j) * kBlockK;
+        const int k0 = (jb0 + j) * kBlockK;
         if (k0 + kBlockK > lim_all) {  // the diagonal and the ragged last block
           const int lim = lim_row - k0;
 #pragma unroll
@@ -683,11 +809,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
         }
         float mx[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx[i] = fmaxf(s[i], s[8 + i]);
+        for (int q = 0; q < 8; ++q) mx[q] = fmaxf(s[q], s[8 + q]);
 #pragma unroll
         for (int gi = 1; gi < kBlockK / 16; ++gi)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) mx[i] = fmax3(mx[i], s[16 * gi + i], s[16 * gi + 8 + i]);
+          for (int q = 0; q < 8; ++q) mx[q] = fmax3(mx[q], s[16 * gi + q], s[16 * gi + 8 + q]);
         const float mb = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
         const float m_cand = fmaxf(m_used, QUANT ? fmaf(mb, blk_scale2, shift) : mb * blk_scale2);
         const bool need = m_cand > m_used + kPagedRescaleLog2;
@@ -719,7 +845,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
           }
           tmem_st32(tS + half * 32, pk);
           if (half == 1) break;
-          if (rescale && j > 0) {
+          if (rescale && i > 0) {
 #pragma unroll 1
             for (int c = 0; c < DV / 32; ++c) {
               uint32_t o[32];
@@ -727,81 +853,115 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
               tmem_ld_wait();
               reg_fence(o);
 #pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                float a = __uint_as_float(o[i]), b = __uint_as_float(o[i + 1]);
+              for (int q = 0; q < 32; q += 2) {
+                float a = __uint_as_float(o[q]), b = __uint_as_float(o[q + 1]);
                 fmul2_scalar(a, b, alpha);
-                o[i] = __float_as_uint(a);
-                o[i + 1] = __float_as_uint(b);
+                o[q] = __float_as_uint(a);
+                o[q + 1] = __float_as_uint(b);
               }
               tmem_st32(tO + c * 32, o);
             }
           }
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(&p_half[t]);
+          warp_arrive(&p_half[t], lane);
         }
         const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
         l = QUANT ? fmaf(sum, unshift, l) : l + sum;
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&p_full[t]);
+        warp_arrive(&p_full[t], lane);
       }
       if (!ok) break;
 
       // ---------------------------------------------------------- epilogue: O / l and LSE, or a partial
-      if (!mbar_wait_warp(&o_full[t], on & 1, abort_flag, p.status)) {
+      if (merge && t == 1) {
+        // slot 0's warps merge: hand them this slot's max and sum; they read O from tensor memory
+        // (o_empty: they have read the piece before)
+        if (on[1] > 0 && !mbar_wait_warp(&o_empty[1], (on[1] - 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        ml_x[row] = make_float2(m_used, l);
+        warp_arrive(ml_full, lane);
+        ++on[0], ++on[1];
+        continue;
+      }
+      if (!mbar_wait_warp(&o_full[t], on[t] & 1, abort_flag, p.status)) {
         ok = false;
         break;
       }
-      ++on;
-      tc_fence_after();
-      if (w.slot >= 0) {
-        const int64_t prow = static_cast<int64_t>(w.slot) * p.slot_rows + t * kBlockQ + row;
-#pragma unroll 1
-        for (int c = 0; c < DV / 32; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tO + c * 32, o);
-          tmem_ld_wait();
-          reg_fence(o);
-          if (row_valid) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * DV + c * 32);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          __syncwarp();
+      float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, merging, of slot 1's
+      if (merge) {
+        if (!mbar_wait_warp(ml_full, alts & 1, abort_flag, p.status) ||
+            !mbar_wait_warp(&o_full[1], on[1] & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
         }
-        tc_fence_before();
-        mbar_arrive(&o_empty[t]);
-        if (row_valid) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m_used, l);
-        continue;
+        const float2 other = ml_x[row];
+        ++alts;
+        const float top = fmaxf(m_used, other.x);
+        w0 = m_used == -INFINITY ? 0.f : ex2(m_used - top);
+        w1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
+        l = l * w0 + other.y * w1;
+        m_used = top;
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      ++on[t];
+      if (n_other > 0) ++on[1 - t];
+      tc_fence_after();
+      const bool partial = w.slot >= 0;
+      const float inv = partial ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      w0 *= inv, w1 *= inv;
+      const int64_t prow = static_cast<int64_t>(w.slot) * p.slot_rows + qt * kBlockQ + row;
       const int head = w.kvh * p.group + row_head;
-      uint16_t* orow = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(w.q_off + tok) * p.o_s + static_cast<int64_t>(head) * p.o_h;
+      const int q_row = w.q_off + tok;
+      uint16_t* orow = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_row) * p.o_s + static_cast<int64_t>(head) * p.o_h;
 #pragma unroll 1
       for (int c = 0; c < DV / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(tO + c * 32, o);
         tmem_ld_wait();
         reg_fence(o);
-        uint32_t pk[16];
+        if (merge) {
+          uint32_t o1[32];
+          tmem_ld32(tO + 128 + c * 32, o1);
+          tmem_ld_wait();
+          reg_fence(o1);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float a = __uint_as_float(o[2 * i]) * inv, b = __uint_as_float(o[2 * i + 1]) * inv;
-          pk[i] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+          for (int q = 0; q < 32; ++q)
+            o[q] = __float_as_uint(__uint_as_float(o[q]) * w0 + __uint_as_float(o1[q]) * w1);
+        } else if (!partial) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * w0);
         }
         if (row_valid) {
-          uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+          if (partial) {
+            uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * DV + c * 32);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+            for (int q = 0; q < 8; ++q) dst[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+          } else {
+            uint32_t pk[16];
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float a = __uint_as_float(o[2 * q]), b = __uint_as_float(o[2 * q + 1]);
+              pk[q] = BF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(orow + c * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+          }
         }
         __syncwarp();
       }
       tc_fence_before();
-      mbar_arrive(&o_empty[t]);
-      if (p.lse != nullptr && row_valid)
-        p.lse[static_cast<int64_t>(head) * p.total_q + w.q_off + tok] =
-            l > 0.f ? (m_used + lg2(l)) * kPagedLn2 : -INFINITY;
+      warp_arrive(&o_empty[t], lane);
+      if (merge && lane == 0) mbar_arrive(&o_empty[1]);
+      if (row_valid) {
+        if (partial)
+          *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m_used, l);
+        else if (p.lse != nullptr)
+          p.lse[static_cast<int64_t>(head) * p.total_q + q_row] = l > 0.f ? (m_used + lg2(l)) * kPagedLn2 : -INFINITY;
+      }
     }
   }
 
@@ -815,11 +975,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV>::THREADS, 1)
 }
 
 // Launches the kernel as a programmatic dependent of the plan kernel, one CTA per SM.
-template <bool BF16, bool QUANT, int D, int DV>
-cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                  const PagedParams& p, cudaStream_t st) {
-  using C = PagedCfg<QUANT, D, DV>;
-  auto kern = paged_kernel<BF16, QUANT, D, DV>;
+template <bool BF16, bool QUANT, int D, int DV, bool ONE>
+cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
+                             cudaStream_t st) {
+  using C = PagedCfg<QUANT, D, DV, ONE>;
+  auto kern = paged_kernel<BF16, QUANT, D, DV, ONE>;
   int dev = 0, sms = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
@@ -836,6 +996,13 @@ cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, 
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
+}
+
+template <bool BF16, bool QUANT, int D, int DV>
+cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                  const PagedParams& p, cudaStream_t st) {
+  return p.max_seqlen_q <= p.tok_tile ? launch_paged_one<BF16, QUANT, D, DV, true>(tq, tk, tv, p, st)
+                                      : launch_paged_one<BF16, QUANT, D, DV, false>(tq, tk, tv, p, st);
 }
 
 }  // namespace sdpa

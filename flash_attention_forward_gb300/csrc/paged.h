@@ -6,11 +6,46 @@
 
 namespace sdpa {
 
-// The plan, written by paged_plan_kernel at the start of the workspace: a header of kPlanHeader
-// ints, then three prefixes of B + 1 entries each over the sequences.
-enum PlanHeader : int { kPlanUnits = 0, kPlanSeg = 1, kPlanGroups = 2, kPlanHeader = 4 };
-// prefix 0: work units; prefix 1: partial slots (units of sequences cut into several key ranges);
-// prefix 2: groups (work tile, KV head) that the combine merges.
+// The work, as one line.  A work unit is two query tiles (2 * tok_tile tokens of one sequence) and one
+// KV head against all the key blocks the tiles see; units lie in the order (sequence, tile, KV
+// head), each as long as its key blocks plus kUnitCost for its prologue and epilogue.  CTA c takes the
+// stretch from cut c to cut c + 1, all of one length, so every SM has the same to do whatever the
+// lengths are.  A cut inside a unit divides its keys; the two or more pieces write partials that a
+// second kernel merges.  Cuts that would leave fewer than kMinPiece blocks on a side move to the
+// unit's edge.
+constexpr int kUnitCost = 2;         // blocks' time of a unit's prologue and epilogue
+constexpr int kMinPiece = 3;         // blocks
+constexpr int kMinWork = 6;          // blocks per CTA below which more CTAs do not pay (unless units are left)
+constexpr int kPagedMaxCtas = 160;
+
+// The plan, written by paged_plan_kernel at the start of the workspace.
+struct PagedPlanHeader {
+  int32_t n_ctas, n_groups, pad[2];
+};
+struct PagedPlan {
+  PagedPlanHeader* head;
+  int4* cuts;              // [kPagedMaxCtas + 1] {tile, KV head, key block, 0}
+  int4* groups;            // [kPagedMaxCtas] cut units: {tile, KV head, first CTA, pieces}
+  int2* tiles;             // [n_tiles] {sequence, tile in it}
+  long long* tile_pos;     // [n_tiles + 1] start of a tile's units on the line
+  int32_t* seq_tiles;      // [B + 1] tiles of the sequences before b
+};
+inline size_t paged_plan_bytes(int B, long long n_tiles) {
+  return split_round16(sizeof(PagedPlanHeader) + (2 * kPagedMaxCtas + 1) * sizeof(int4) +
+                       static_cast<size_t>(n_tiles) * (sizeof(int2) + sizeof(long long)) + sizeof(long long) +
+                       (static_cast<size_t>(B) + 1) * sizeof(int32_t));
+}
+inline PagedPlan paged_plan_at(void* ws, long long n_tiles) {
+  PagedPlan p;
+  char* c = static_cast<char*>(ws);
+  p.head = reinterpret_cast<PagedPlanHeader*>(c);
+  p.cuts = reinterpret_cast<int4*>(p.head + 1);
+  p.groups = p.cuts + kPagedMaxCtas + 1;
+  p.tile_pos = reinterpret_cast<long long*>(p.groups + kPagedMaxCtas);
+  p.tiles = reinterpret_cast<int2*>(p.tile_pos + n_tiles + 1);
+  p.seq_tiles = reinterpret_cast<int32_t*>(p.tiles + n_tiles);
+  return p;
+}
 
 struct PagedParams {
   void* o;                 // [total_q, Hq, Dv]
@@ -22,18 +57,19 @@ struct PagedParams {
   int64_t pt_b;
   const float* k_scale;    // quantised caches: [n_pages, Hkv, page_size]
   const float* v_scale;
-  int32_t* plan;           // workspace: the plan ...
-  float* part_o;           // ... then partial O [slot][slot_rows][DV] ...
+  PagedPlan plan;          // workspace: the plan ...
+  float* part_o;           // ... then partial O [2 * CTA + (0: the CTA's first piece, 1: its last)][slot_rows][DV] ...
   float* part_ml;          // ... and (max, sum) [slot][slot_rows][2]
   uint32_t* status;
   int B, Hq, Hkv, total_q, max_seqlen_q, group, causal;
   int tok_tile;            // tokens per 128-row query tile: 128 / group
   int page_size, log2_page, max_pages, n_pages;
   int max_kv;              // max_pages * page_size
-  int slot_rows, max_slots, sms;
+  int slot_rows, cut, sms; // cut: the workspace holds partials, units may be cut
+  int max_tiles;           // tiles the plan has room for
   int stall_first_stage;   // test hook
   float scale2;            // scale * log2(e)
-  FastDiv div_group, div_hkv;
+  FastDiv div_group;
 };
 
 // Key blocks that query tile `tile` (tok_tile tokens) of a sequence sees: 0 past its last token, else

@@ -12,221 +12,195 @@ namespace sdpa {
 
 namespace {
 
-// Costs in units of one 128-key block of a work unit: what a unit spends before its first and
-// after its last block, and what the merge adds once anything is cut.
-constexpr float kUnitOverhead = 3.f, kMergeOverhead = 4.f;
 constexpr int kPlanThreads = 1024;
-constexpr int kPlanCandidates = 64;  // segments of the longest sequence: 1 .. 64
 
-__device__ __forceinline__ int plan_tiles(const PagedParams& p, int b, int& blocks, int& n_out) {
-  const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-  const int n = max(0, q1 - q0);
-  const int sk = min(max(__ldg(p.kv_len + b), 0), p.max_kv);
-  blocks = n > 0 ? max(1, (sk + kBlockK - 1) / kBlockK) : 0;
-  n_out = n;
-  const int tok_unit = kTilesPerCta * p.tok_tile;
-  return (n + tok_unit - 1) / tok_unit;
-}
-
-// One block decides how the key ranges are cut and lays out the units.  Candidate i cuts the longest
-// sequence into i + 1 segments of `seg` blocks and every other one by the same `seg`; each warp
-// costs candidates over all sequences:
-//   rounds = ceil(units / SMs),  cost = max(rounds * blocks per unit, seg) + rounds * overhead (+ merge)
-// and the cheapest that fits the workspace's partial slots wins, the first on ties.  Offsets that are
-// not sorted within [0, total_q], or a sequence of more than max_seqlen_q tokens, raise a status and
-// leave no units, so nothing is stored.
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams p) {
-  __shared__ int s_max_blocks;
-  __shared__ unsigned long long s_best;
-  __shared__ int warp_sum[3][32];
-  __shared__ int carry[3];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  pdl_launch_dependents();  // the attention kernel may set itself up meanwhile
-  if (tid == 0) {
-    s_max_blocks = 0;
-    s_best = ~0ull;
-    carry[0] = carry[1] = carry[2] = 0;
+// Inclusive sum of v over the block's threads so far (before: the sum of earlier calls); total: the
+// sum of all of them.  Two barriers.
+__device__ __forceinline__ long long block_scan(long long v, long long before, long long (&warp_sum)[33], long long& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += y;
   }
   __syncthreads();
-  int bad = 0, top = 0;
-  for (int b = tid; b < p.B; b += kPlanThreads) {
-    const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-    if (q0 < 0 || q1 < q0 || q1 > p.total_q || q1 - q0 > p.max_seqlen_q) bad = 1;
-    int blocks, n;
-    plan_tiles(p, b, blocks, n);
-    top = max(top, blocks);
+  if (lane == 31) warp_sum[warp] = v;
+  __syncthreads();
+  long long s = warp_sum[lane];  // every warp scans the 32 sums itself
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, s, d);
+    if (lane >= d) s += y;
   }
-  top = __reduce_max_sync(0xffffffffu, top);
-  if (lane == 0) atomicMax(&s_max_blocks, top);
-  int32_t* prefix = p.plan + kPlanHeader;
-  if (__syncthreads_or(bad)) {
-    for (int i = tid; i < 3 * (p.B + 1); i += kPlanThreads) prefix[i] = 0;
+  total = before + __shfl_sync(0xffffffffu, s, 31);
+  const long long prev = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
+  return before + v + (warp > 0 ? prev : 0);
+}
+
+__device__ __forceinline__ int unit_blocks(const PagedParams& p, int b, int i) {
+  const int n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b), len = __ldg(p.kv_len + b);
+  const int sk = min(max(len, 0), p.max_kv);
+  return max(paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta),
+             paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta + 1));
+}
+
+// One block lays out the tiles, measures the line and places the cuts.  Offsets that are not sorted
+// within [0, total_q], or a sequence of more than max_seqlen_q tokens, raise a status and leave no
+// work, so nothing is stored.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams p) {
+  __shared__ long long warp_sum[33];
+  __shared__ int4 s_cuts[kPagedMaxCtas + 1];
+  __shared__ int s_groups;
+  const int tid = threadIdx.x;
+  pdl_launch_dependents();  // the attention kernel may set itself up meanwhile
+  if (tid == 0) s_groups = 0;
+  const int tok_unit = kTilesPerCta * p.tok_tile;
+  int bad = 0;
+  long long n_tiles = 0;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    int v = 0;
+    if (b < p.B) {
+      const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
+      if (q0 < 0 || q1 < q0 || q1 > p.total_q || static_cast<long long>(q1) - q0 > p.max_seqlen_q)
+        bad = 1;
+      else
+        v = (q1 - q0 + tok_unit - 1) / tok_unit;
+    }
+    const long long before = n_tiles;
+    const long long incl = block_scan(v, before, warp_sum, n_tiles);
+    if (b < p.B) p.plan.seq_tiles[b] = static_cast<int32_t>(min(incl - v, static_cast<long long>(p.max_tiles)));
+  }
+  if (__syncthreads_or(bad) || n_tiles > p.max_tiles) {
     if (tid == 0) {
-      p.plan[kPlanUnits] = p.plan[kPlanGroups] = 0;
-      p.plan[kPlanSeg] = 1;
+      p.plan.head->n_ctas = p.plan.head->n_groups = 0;
       atomicOr(p.status, kStatusBadSeqlens);
     }
     return;
   }
-  const int max_blocks = max(s_max_blocks, 1);
-  for (int i = warp; i < kPlanCandidates; i += kPlanThreads / 32) {
-    const int seg = (max_blocks + i) / (i + 1);
-    if (i > 0 && (p.max_slots == 0 || seg < 2)) break;  // the same for the whole warp
-    float units = 0.f, work = 0.f, slots = 0.f;
-    for (int b = lane; b < p.B; b += 32) {
-      int blocks, n;
-      const float tiles = static_cast<float>(plan_tiles(p, b, blocks, n)) * p.Hkv;
-      if (n == 0) continue;
-      const float segs = static_cast<float>((blocks + seg - 1) / seg);
-      units += tiles * segs;
-      work += tiles * blocks;
-      if (segs > 1.f) slots += tiles * segs;
+  long long total = 0;
+  for (int base = 0; base < n_tiles; base += kPlanThreads) {
+    const int tile = base + tid;
+    long long v = 0;
+    if (tile < n_tiles) {
+      int lo = 0, hi = p.B;  // the last sequence that starts at or before the tile
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.plan.seq_tiles[mid] <= tile) lo = mid; else hi = mid;
+      }
+      const int i = tile - p.plan.seq_tiles[lo];
+      p.plan.tiles[tile] = make_int2(lo, i);
+      v = static_cast<long long>(unit_blocks(p, lo, i) + kUnitCost) * p.Hkv;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      units += __shfl_xor_sync(0xffffffffu, units, d);
-      work += __shfl_xor_sync(0xffffffffu, work, d);
-      slots += __shfl_xor_sync(0xffffffffu, slots, d);
-    }
-    if (lane == 0 && units > 0.f && (i == 0 || slots <= static_cast<float>(p.max_slots))) {
-      const float rounds = ceilf(units / static_cast<float>(p.sms));
-      const float cost = fmaxf(rounds * work / units, static_cast<float>(min(seg, max_blocks))) + rounds * kUnitOverhead +
-                         (slots > 0.f ? kMergeOverhead : 0.f);
-      // positive floats order like their bits
-      atomicMin(&s_best, (static_cast<unsigned long long>(__float_as_uint(cost)) << 32) | static_cast<unsigned>(i));
-    }
+    const long long before = total;
+    const long long incl = block_scan(v, before, warp_sum, total);
+    if (tile < n_tiles) p.plan.tile_pos[tile] = incl - v;
   }
   __syncthreads();
-  const int best = s_best == ~0ull ? 0 : static_cast<int>(s_best & 0xFFFFFFFFu);
-  const int seg = (max_blocks + best) / (best + 1);
-  // exclusive prefixes of units, slots and groups over the sequences
-  for (int base = 0; base < p.B; base += kPlanThreads) {
-    const int b = base + tid;
-    int v[3] = {0, 0, 0};
-    if (b < p.B) {
-      int blocks, n;
-      const int tiles = plan_tiles(p, b, blocks, n) * p.Hkv;
-      const int segs = n > 0 ? (blocks + seg - 1) / seg : 0;
-      v[0] = tiles * segs;
-      v[1] = segs > 1 ? v[0] : 0;
-      v[2] = segs > 1 ? tiles : 0;
-    }
-    int x[3] = {v[0], v[1], v[2]};
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x[q], d);
-        if (lane >= d) x[q] += y;
+  // as many CTAs as have kMinWork each, and at least one for every unit
+  const int n_ctas = static_cast<int>(min(static_cast<long long>(p.sms), max(n_tiles * p.Hkv, total / kMinWork)));
+  for (int c = tid; c <= n_ctas; c += kPlanThreads) {
+    int4 cut = make_int4(static_cast<int>(n_tiles), 0, 0, 0);
+    if (c < n_ctas) {
+      const long long x = total / n_ctas * c + total % n_ctas * c / n_ctas;
+      int lo = 0, hi = static_cast<int>(n_tiles);
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.plan.tile_pos[mid] <= x) lo = mid; else hi = mid;
       }
-      if (lane == 31) warp_sum[q][warp] = x[q];
-    }
-    __syncthreads();
-    if (warp < 3) {
-      int s = warp_sum[warp][lane];
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += y;
+      const int2 at = p.plan.tiles[lo];
+      const int blocks = unit_blocks(p, at.x, at.y);
+      const int r = static_cast<int>(x - p.plan.tile_pos[lo]);
+      int kvh = r / (blocks + kUnitCost);
+      int off = r - kvh * (blocks + kUnitCost) - kUnitCost;
+      if (p.cut ? off < kMinPiece : 2 * off < blocks) {
+        off = 0;
+      } else if (!p.cut || blocks - off < kMinPiece) {
+        off = 0;
+        if (++kvh == p.Hkv) kvh = 0, ++lo;
       }
-      warp_sum[warp][lane] = s;
+      cut = make_int4(lo, kvh, off, 0);
     }
-    __syncthreads();
-    int incl[3];
-#pragma unroll
-    for (int q = 0; q < 3; ++q) {
-      incl[q] = carry[q] + x[q] + (warp > 0 ? warp_sum[q][warp - 1] : 0);
-      if (b < p.B) prefix[q * (p.B + 1) + b] = incl[q] - v[q];
-    }
-    __syncthreads();
-    if (tid == kPlanThreads - 1)
-      for (int q = 0; q < 3; ++q) carry[q] = incl[q];
-    __syncthreads();
+    s_cuts[c] = cut;
+    p.plan.cuts[c] = cut;
   }
-  if (tid < 3) prefix[tid * (p.B + 1) + p.B] = carry[tid];
+  __syncthreads();
+  // a unit that is cut: its first cut c belongs to a group of pieces that starts with CTA c - 1
+  for (int c = tid; c < n_ctas; c += kPlanThreads) {
+    const int4 cut = s_cuts[c];
+    if (cut.z == 0) continue;
+    const int4 prev = s_cuts[c - 1];  // c > 0: the line starts with a whole unit
+    if (prev.x == cut.x && prev.y == cut.y && prev.z > 0) continue;
+    int pieces = 2;
+    while (c + pieces - 1 < n_ctas && s_cuts[c + pieces - 1].x == cut.x && s_cuts[c + pieces - 1].y == cut.y) ++pieces;
+    p.plan.groups[atomicAdd(&s_groups, 1)] = make_int4(cut.x, cut.y, c - 1, pieces);
+  }
+  __syncthreads();
   if (tid == 0) {
-    p.plan[kPlanUnits] = carry[0];
-    p.plan[kPlanSeg] = seg;
-    p.plan[kPlanGroups] = carry[2];
+    p.plan.head->n_ctas = n_ctas;
+    p.plan.head->n_groups = s_groups;
   }
 }
 
-// Merges the segments of every cut (work tile, KV head): one warp per (group, row), the segments in
-// order, M = max m_i, O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
+// Merges the pieces of every cut unit: O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i, M = max m_i, the
+// pieces in order.  A CTA takes kMergeRows rows of a unit, DV / 8 threads a row, so that all its loads of
+// one piece are in flight together.
+constexpr int kMergeRows = 16;
+
 template <bool BF16, int DV>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedParams p) {
-  constexpr int VEC = DV / 32;  // columns per lane
+__global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(const PagedParams p) {
+  constexpr int LANES = DV / 8;  // threads per row, 8 columns each
   pdl_wait();
-  const int32_t* prefix = p.plan + kPlanHeader;
-  const int32_t* slot_prefix = prefix + (p.B + 1);
-  const int32_t* group_prefix = slot_prefix + (p.B + 1);
-  const int groups = ld_dep(p.plan + kPlanGroups), seg = ld_dep(p.plan + kPlanSeg);
-  const int lane = threadIdx.x & 31;
-  const int64_t items = static_cast<int64_t>(groups) * p.slot_rows;
-  for (int64_t it = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); it < items; it += static_cast<int64_t>(gridDim.x) * 8) {
-    const int grp = static_cast<int>(it / p.slot_rows), prow = static_cast<int>(it - static_cast<int64_t>(grp) * p.slot_rows);
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (ld_dep(group_prefix + mid) <= grp) lo = mid; else hi = mid;
-    }
-    const int local = grp - ld_dep(group_prefix + lo);  // rank * Hkv + kvh
-    const int q_off = __ldg(p.cu_q + lo), n = __ldg(p.cu_q + lo + 1) - q_off;
-    const int len = __ldg(p.kv_len + lo), sk = min(max(len, 0), p.max_kv);
-    const int tok_unit = kTilesPerCta * p.tok_tile;
-    const int tiles = (n + tok_unit - 1) / tok_unit;
-    const int rank = local / p.Hkv, kvh = local - rank * p.Hkv;
-    const int t = prow / kBlockQ, row = prow - t * kBlockQ;
-    const int row_tok = static_cast<int>(fast_div(row, p.div_group));
-    const int tile = (tiles - 1 - rank) * kTilesPerCta + t;
-    const int tok = tile * p.tok_tile + row_tok;
-    if (row_tok >= p.tok_tile || tok >= n) continue;  // the same for the whole warp
-    const int head = kvh * p.group + (row - row_tok * p.group);
-    const int blocks = paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, tile);
-    const int segs = (blocks + seg - 1) / seg;         // segments this tile reaches
-    const int stride = tiles * p.Hkv;                   // slots from one segment to the next
-    const int64_t slot0 = ld_dep(slot_prefix + lo) + local;
-    float M = -INFINITY;
-    for (int s = lane; s < segs; s += 32)
-      M = fmaxf(M, p.part_ml[((slot0 + static_cast<int64_t>(s) * stride) * p.slot_rows + prow) * 2]);
+  if (static_cast<int>(blockIdx.x) >= ld_dep(&p.plan.head->n_groups)) return;
+  const int4 gr = ld_dep(p.plan.groups + blockIdx.x);
+  const int2 at = ld_dep(p.plan.tiles + gr.x);
+  const int q_off = __ldg(p.cu_q + at.x), n = __ldg(p.cu_q + at.x + 1) - q_off;
+  const int len = __ldg(p.kv_len + at.x), sk = min(max(len, 0), p.max_kv);
+  // piece i: CTA gr.z + i, from its cut on; the first one may be that CTA's last piece
+  const int4 c0 = ld_dep(p.plan.cuts + gr.z);
+  const int slot0 = 2 * gr.z + ((c0.x == gr.x && c0.y == gr.y && c0.z == 0) ? 0 : 1);
+  const int prow = blockIdx.y * kMergeRows + threadIdx.x / LANES, col = 8 * (threadIdx.x % LANES);
+  const int t = prow / kBlockQ, row = prow - t * kBlockQ;
+  const int row_tok = static_cast<int>(fast_div(row, p.div_group));
+  const int tile = at.y * kTilesPerCta + t;
+  const int tok = tile * p.tok_tile + row_tok;
+  if (prow >= p.slot_rows || row_tok >= p.tok_tile || tok >= n) return;
+  const int head = gr.y * p.group + (row - row_tok * p.group);
+  const int blocks = paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, tile);
+  float M = -INFINITY, L = 0.f;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+  for (int i = 0; i < gr.w; ++i) {
+    if (i > 0 && ld_dep(&p.plan.cuts[gr.z + i].z) >= blocks) break;  // this tile ends before
+    const int64_t r = static_cast<int64_t>(i == 0 ? slot0 : 2 * (gr.z + i)) * p.slot_rows + prow;
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + r * 2);
+    const float4 a = *reinterpret_cast<const float4*>(p.part_o + r * DV + col);
+    const float4 b = *reinterpret_cast<const float4*>(p.part_o + r * DV + col + 4);
+    const float top = fmaxf(M, ml.x);
+    const float w0 = M == -INFINITY ? 0.f : ex2(M - top), w1 = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    M = top;
+    L = L * w0 + w1 * ml.y;
+    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    float acc[VEC], L = 0.f;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < segs; ++s) {
-      const int64_t at = (slot0 + static_cast<int64_t>(s) * stride) * p.slot_rows + prow;
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + at * 2);
-      const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - M);
-      L += w * ml.y;
-      const float* src = p.part_o + at * DV + lane * VEC;
-      if constexpr (VEC == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += w * v.x, acc[1] += w * v.y, acc[2] += w * v.z, acc[3] += w * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += w * v.x, acc[1] += w * v.y;
-      }
-    }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t* orow = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_off + tok) * p.o_s +
-                                                 static_cast<int64_t>(head) * p.o_h + lane * VEC);
-    uint32_t pk[VEC / 2];
-#pragma unroll
-    for (int i = 0; i < VEC / 2; ++i)
-      pk[i] = BF16 ? pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv) : pack_f16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-    if constexpr (VEC == 4)
-      *reinterpret_cast<uint2*>(orow) = make_uint2(pk[0], pk[1]);
-    else
-      *orow = pk[0];
-    if (p.lse != nullptr && lane == 0)
-      p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] =
-          L > 0.f ? (M + lg2(L)) * 0.6931471805599453f : -INFINITY;
+    for (int c = 0; c < 8; ++c) acc[c] = acc[c] * w0 + w1 * v[c];
   }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  uint32_t pk[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    pk[i] = BF16 ? pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv) : pack_f16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_off + tok) * p.o_s +
+                            static_cast<int64_t>(head) * p.o_h + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+  if (p.lse != nullptr && col == 0)
+    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L > 0.f ? (M + lg2(L)) * 0.6931471805599453f : -INFINITY;
 }
 
-size_t plan_bytes(int B) { return split_round16((kPlanHeader + 3 * (static_cast<size_t>(B) + 1)) * sizeof(int32_t)); }
+// Work tiles that calls of these sizes can have.
+long long tiles_bound(int B, int total_q, int max_seqlen_q, int group) {
+  const long long tok_unit = kTilesPerCta * (kBlockQ / group);
+  return std::min(static_cast<long long>(B) * ((max_seqlen_q + tok_unit - 1) / tok_unit),
+                  (static_cast<long long>(total_q) + (tok_unit - 1) * B) / tok_unit);
+}
 
 // Rows of a partial slot: both query tiles, or the rows of the longest chunk where one tile holds it.
 int slot_rows(int group, int max_seqlen_q) {
@@ -234,24 +208,10 @@ int slot_rows(int group, int max_seqlen_q) {
   return max_seqlen_q <= tok_tile ? max_seqlen_q * group : kCtaRows;
 }
 
-// Partial slots a workspace is sized for: 64 MB of them, at least 304 (two cuts for every SM), at
-// most 4096 and what the sizes can produce at all; none where no sequence has two blocks of keys.
-long long slots_wanted(int B, int Hkv, int total_q, int max_seqlen_q, int group, int max_kv, size_t slot_bytes) {
-  const long long blocks = (max_kv + kBlockK - 1) / kBlockK;
-  if (blocks < 2) return 0;
-  const long long tok_unit = kTilesPerCta * (kBlockQ / group);
-  const long long by_max = static_cast<long long>(B) * ((max_seqlen_q + tok_unit - 1) / tok_unit);
-  const long long by_total = (static_cast<long long>(total_q) + (tok_unit - 1) * B) / tok_unit;
-  const long long most = std::min(by_max, by_total) * Hkv * std::min<long long>(blocks, kPlanCandidates);
-  return std::min(most, std::min<long long>(4096, std::max<long long>(304, (64ll << 20) / static_cast<long long>(slot_bytes))));
-}
-
-size_t slot_size(int rows, int Dv) { return static_cast<size_t>(rows) * (Dv + 2) * sizeof(float); }
-
-size_t paged_ws_bytes(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_kv, int Dv) {
-  const int group = Hq / Hkv;
-  const size_t one = slot_size(slot_rows(group, max_seqlen_q), Dv);
-  return plan_bytes(B) + static_cast<size_t>(slots_wanted(B, Hkv, total_q, max_seqlen_q, group, max_kv, one)) * one;
+// Bytes of partial results: two slots per CTA; none where no unit is long enough to be cut.
+size_t partial_bytes(int group, int max_seqlen_q, int max_kv, int Dv) {
+  if ((max_kv + kBlockK - 1) / kBlockK < 2 * kMinPiece) return 0;
+  return 2ull * kPagedMaxCtas * slot_rows(group, max_seqlen_q) * (Dv + 2) * sizeof(float);
 }
 
 bool encode_q(CUtensorMap* map, const void* q, bool bf16, int total_q, int Hq, int D, int64_t q_s, int64_t q_h, int group) {
@@ -291,11 +251,10 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
        reinterpret_cast<uintptr_t>(lse)) & 3u)
     return SDPA_ERR_INVALID;
   const int max_kv = max_pages * page_size;
-  const long long tok_unit = kTilesPerCta * (kBlockQ / group);
-  const long long tiles = std::min(static_cast<long long>(B) * ((max_seqlen_q + tok_unit - 1) / tok_unit),
-                                   (static_cast<long long>(total_q) + (tok_unit - 1) * B) / tok_unit);
-  if (tiles * Hkv * kPlanCandidates >= (1ll << 30)) return SDPA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < plan_bytes(B)) return SDPA_ERR_INVALID;
+  const long long tiles = tiles_bound(B, total_q, max_seqlen_q, group);
+  if (tiles * Hkv >= (1ll << 30)) return SDPA_ERR_UNSUPPORTED;
+  const size_t plan = paged_plan_bytes(B, tiles), partials = partial_bytes(group, max_seqlen_q, max_kv, Dv);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < plan) return SDPA_ERR_INVALID;
 
   PagedParams p{};
   p.o = o, p.lse = lse, p.o_s = st[8], p.o_h = st[9];
@@ -307,17 +266,16 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.page_size = page_size, p.log2_page = __builtin_ctz((unsigned)page_size);
   p.max_pages = max_pages, p.n_pages = n_pages, p.max_kv = max_kv;
   p.scale2 = (float)((double)scale * 1.4426950408889634);
-  p.div_group = make_fastdiv((uint32_t)group), p.div_hkv = make_fastdiv((uint32_t)Hkv);
+  p.div_group = make_fastdiv((uint32_t)group);
   p.slot_rows = slot_rows(group, max_seqlen_q);
-  const size_t one = slot_size(p.slot_rows, Dv);
-  const long long fit = static_cast<long long>((workspace_bytes - plan_bytes(B)) / one);
-  p.max_slots = static_cast<int>(std::min(fit, slots_wanted(B, Hkv, total_q, max_seqlen_q, group, max_kv, one)));
-  char* ws = static_cast<char*>(workspace);
-  p.plan = reinterpret_cast<int32_t*>(ws);
-  p.part_o = reinterpret_cast<float*>(ws + plan_bytes(B));
-  p.part_ml = p.part_o + static_cast<size_t>(p.max_slots) * p.slot_rows * Dv;
+  p.cut = partials > 0 && workspace_bytes >= plan + partials;
+  p.max_tiles = (int)tiles;
+  p.plan = paged_plan_at(workspace, tiles);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
+  p.part_ml = p.part_o + 2ull * kPagedMaxCtas * p.slot_rows * Dv;
   int dev = 0;
   if (current_device_sms(&dev, &p.sms) != cudaSuccess || device_status_ptr(&p.status) != cudaSuccess) return SDPA_ERR_CUDA;
+  p.sms = std::min(p.sms, kPagedMaxCtas);
 
   alignas(64) CUtensorMap tq, tk, tv;
   const int rows = std::min(kBlockK, page_size);
@@ -344,7 +302,7 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   if (e == cudaSuccess)
     e = quant ? launch_paged_fp8(bf16, D, tq, tk, tv, p, s)
               : (bf16 ? launch_paged_bf16(D, tq, tk, tv, p, s) : launch_paged_f16(D, tq, tk, tv, p, s));
-  if (e == cudaSuccess && p.max_slots > 0) e = launch_paged_combine(bf16, Dv, p, s);
+  if (e == cudaSuccess && p.cut) e = launch_paged_combine(bf16, Dv, p, s);
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
@@ -360,10 +318,9 @@ cudaError_t launch_paged_combine(bool bf16, int Dv, const PagedParams& p, cudaSt
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // one warp per row, at most four CTAs per SM walking the rows
-  const long long rows = static_cast<long long>(p.max_slots) * p.slot_rows;
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>((rows + 7) / 8, 4ll * p.sms)));
-  cfg.blockDim = dim3(256);
+  // at most sms - 1 units are cut
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(p.sms - 1, 1)), static_cast<unsigned>((p.slot_rows + kMergeRows - 1) / kMergeRows));
+  cfg.blockDim = dim3(kMergeRows * Dv / 8);
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
@@ -384,7 +341,8 @@ size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int ma
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Hq / Hkv > kBlockQ || total_q < 1 || max_seqlen_q < 1 ||
       max_seqlen_q > total_q || max_kv < 1 || max_kv > (1 << 30) || Dv < 1)
     return 0;
-  return paged_ws_bytes(B, Hq, Hkv, total_q, max_seqlen_q, max_kv, Dv);
+  const int group = Hq / Hkv;
+  return paged_plan_bytes(B, tiles_bound(B, total_q, max_seqlen_q, group)) + partial_bytes(group, max_seqlen_q, max_kv, Dv);
 }
 
 int sdpa_fwd_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* page_table,

@@ -402,9 +402,9 @@ int sdpa_decode_paged_fp8(const void* q, const void* k_pool, const void* v_pool,
 /*
  * sdpa_fwd_paged_workspace_size -- bytes of device scratch for sdpa_fwd_paged and
  * sdpa_fwd_paged_fp8 (max_kv = max_pages * page_size): the work plan, which the call needs, and
- * partial results of key ranges that run on otherwise idle SMs.  With less than the full size
- * (but at least 32 + 12 * (B + 1) bytes, rounded up to 16) the call cuts fewer ranges; results agree
- * within rounding.  0 for bad sizes.
+ * partial results of query tiles whose keys are divided over several SMs.  With room for the plan
+ * (the value for max_kv = 1) but less than the full size the call divides no tile's keys; results agree within
+ * rounding.  0 for bad sizes.
  */
 size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int max_kv, int Dv);
 

@@ -202,13 +202,15 @@ def test_chunk_codes(lib, quant):
 
 def test_chunk_workspace(lib):
     size = fa.sdpa_fwd_paged_workspace_size
-    plan = lambda B: ((4 + 3 * (B + 1)) * 4 + 15) // 16 * 16  # noqa: E731
-    # one block of keys: nothing to cut
-    assert size(3, 8, 2, 30, 12, 128, 128) == plan(3)
-    # 5 tokens x 4 heads = 20 rows a slot; one tile per sequence and head, at most 64 segments
-    assert size(2, 8, 2, 10, 5, 1 << 20, 128) == plan(2) + 2 * 2 * 64 * 20 * 130 * 4
-    # long chunks take slots of 256 rows, 64 MB of them
-    one = 256 * 130 * 4
-    assert size(4, 32, 8, 8192, 2048, 16384, 128) == plan(4) + ((64 << 20) // one) * one
+
+    def plan(B, tiles):  # header, cuts and groups of 160 CTAs, tiles, sequences
+        return (16 + 321 * 16 + tiles * 16 + 8 + (B + 1) * 4 + 15) // 16 * 16
+
+    # fewer than six blocks of keys: nothing to cut
+    assert size(3, 8, 2, 30, 12, 640, 128) == plan(3, 3)
+    # 5 tokens x 4 heads = 20 rows a slot, two slots for each of 160 CTAs
+    assert size(2, 8, 2, 10, 5, 1 << 20, 128) == plan(2, 2) + 320 * 20 * 130 * 4
+    # long chunks take slots of both tiles' 256 rows; tiles of 64 tokens
+    assert size(4, 32, 8, 8192, 2048, 16384, 128) == plan(4, 128) + 320 * 256 * 130 * 4
     for bad in ((0, 8, 2, 10, 5, 64, 128), (2, 8, 3, 10, 5, 64, 128), (2, 8, 2, 10, 11, 64, 128), (2, 8, 2, 10, 5, 0, 128)):
         assert size(*bad) == 0

@@ -132,7 +132,8 @@ def test_cut_key_ranges(quant, new, lens):
     x = make(new, lens, 8, 2, 128, 128, 64, "bf16", quant, seed=4)
     o, lse = run(*x, max(new), scale=0.09, causal=True)
     check(*x, o, lse, 0.09, True)
-    small = torch.empty((4 + 3 * (len(new) + 1)) * 4 + 16, dtype=torch.uint8, device=DEV)
+    plan = fa.sdpa_fwd_paged_workspace_size(len(new), 8, 2, sum(new), max(new), 1, 128)
+    small = torch.empty(plan, dtype=torch.uint8, device=DEV)
     o2, lse2 = run(*x, max(new), scale=0.09, causal=True, workspace=small)
     check(*x, o2, lse2, 0.09, True)
 
