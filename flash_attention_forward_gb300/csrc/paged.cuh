@@ -45,7 +45,7 @@ constexpr int kMinBlockExp = -100;  // exponent floor of a block's scales: 2^100
 constexpr int kBlockExpRoom = 6;    // codes reach 448 < 2^9, fp16 65504: six powers of two to spare
 constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn masked scores into NaN
 constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
-constexpr int kExpRing = 16;        // blocks whose exponents are kept: more than the ring can run ahead
+constexpr int kExpRing = 8;         // blocks whose exponents are kept: more than the ring can run ahead
 
 // ONE: no sequence has more tokens than one query tile holds, so shared memory keeps one and the ring
 // takes the other's place (such calls are bound by reading the cache).
@@ -68,14 +68,15 @@ struct PagedCfg {
   static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
   static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
   static constexpr int BARS = D == 64 ? 768 : 640;
-  static constexpr int OFF_EXP = OFF_BAR + BARS;                    // int2 [kExpRing]
-  static constexpr int OFF_QEXP = OFF_EXP + (QUANT ? kExpRing * 8 : 0);  // int8 [2 tiles][2][128]
+  static constexpr int OFF_EXP = OFF_BAR + BARS;                    // int2 [kExpRing][4]
+  static constexpr int OFF_QEXP = OFF_EXP + (QUANT ? kExpRing * 32 : 0);  // int8 [2 tiles][2][128]
   // pieces announced by the producer: more than it can run ahead of the slowest role.  With m pieces behind
   // the one whose V is used up, 2 m - 1 items lie in the rings (each piece's V waits for its softmax).
   static constexpr int PIECES = D == 64 ? 16 : 8;
   static constexpr int OFF_PIECE = OFF_QEXP + (QUANT ? 512 : 0);
   static constexpr int OFF_ML = OFF_PIECE + PIECES * 64;            // float2 [128]: max and sum of slot 1
   static constexpr int SMEM = OFF_ML + 1024;
+  static_assert(SLOTS / 2 + 3 <= kExpRing, "the exponent ring holds what the converters write");
   static_assert((SLOTS + RAWS) / 2 + 2 <= PIECES, "the piece ring holds what the producer announces");
   // warpgroups: control (producer, MMA, helpers), converters (quantised), two softmax
   static constexpr int THREADS = QUANT ? 512 : 384;
@@ -160,40 +161,48 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// Converts row r of a raw tile (boxes of W codes a row, swizzled) into the 128-byte-swizzled fp16
-// chunks of 64 columns that the MMAs read, times the pair factor f.  One thread per row: both the reads
-// and the writes of eight neighbouring rows fall on all banks.  The reads of a half row are issued
-// together, as one converting warp per scheduler has nobody to hide their latency.
-template <int COLS, int W>
-__device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int r, uint32_t f) {
-  const int x = r & 7;
-  constexpr int UNITS = COLS / 16, BATCH = 4;
+// Converts row r of a raw tile (boxes of W codes a row, swizzled) into `chunks` 128-byte-swizzled fp16
+// chunks of 64 columns, as the MMAs read them, times the pair factor f; f = 0 stores zeros whatever
+// the codes are.  One thread per row: both the reads and the writes of eight neighbouring rows
+// fall on all banks.  The loop over chunks is not unrolled: the kernel's loops together must fit the
+// instruction cache (unrolled for K and V, fetches stalled 2 of 10 resident warps and the softmax took twice
+// as long; 2048 tokens of 8192 rows 284 us against 217 us).
+template <int W>
+__device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int chunks, int r, uint32_t f) {
+  const int x = (r & 7) << 4;
+  const bool live = f != 0u;
+#pragma unroll 1
+  for (int ch = 0; ch < chunks; ++ch) {
+    const uint8_t* src = W == 128 ? raw + (ch >> 1) * kBlockK * 128 + r * 128 : raw + ch * kBlockK * 64 + r * 64;
+    uint4 c[4];
 #pragma unroll
-  for (int u0 = 0; u0 < UNITS; u0 += BATCH) {
-    uint4 c[BATCH];
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int u = u0 + i, box = u / (W / 16), uu = u % (W / 16);
-      const int sw = W == 128 ? (uu ^ x) : (uu ^ ((r >> 1) & 3));
-      c[i] = *reinterpret_cast<const uint4*>(raw + box * kBlockK * W + r * W + (sw << 4));
+    for (int i = 0; i < 4; ++i) {
+      const int off = W == 128 ? ((((ch & 1) * 4 + i) << 4) ^ x) : ((i << 4) ^ (((r >> 1) & 3) << 4));
+      c[i] = *reinterpret_cast<const uint4*>(src + off);
     }
+    uint8_t* d = dst + ch * kBlockK * 128 + r * 128;
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i) {
-      const int u = u0 + i;
+    for (int i = 0; i < 4; ++i) {
       const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
       uint32_t h[8];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        e4m3x4_to_f16x4(w[q], h[2 * q], h[2 * q + 1]);
+        e4m3x4_to_f16x4(live ? w[q] : 0u, h[2 * q], h[2 * q + 1]);
         h[2 * q] = mul_f16x2(h[2 * q], f);
         h[2 * q + 1] = mul_f16x2(h[2 * q + 1], f);
       }
-      uint8_t* d = dst + (u / 4) * kBlockK * 128 + r * 128;
-      const int v = 2 * (u % 4);
-      *reinterpret_cast<uint4*>(d + ((v ^ x) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(d + (((v + 1) ^ x) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+      *reinterpret_cast<uint4*>(d + (((2 * i) << 4) ^ x)) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(d + (((2 * i + 1) << 4) ^ x)) = make_uint4(h[4], h[5], h[6], h[7]);
     }
   }
+}
+
+// Exponents of a block's largest scales of K and V from those of its four 32-row parts (biased as in
+// fp32), less the room that fp16 leaves above the codes.
+__device__ __forceinline__ int2 block_exp(const int2* parts) {
+  const int4 a = *reinterpret_cast<const int4*>(parts), b = *reinterpret_cast<const int4*>(parts + 2);
+  return make_int2(max(max(max(a.x, a.z), max(b.x, b.z)) - 127 - kBlockExpRoom, kMinBlockExp),
+                   max(max(max(a.y, a.w), max(b.y, b.w)) - 127 - kBlockExpRoom, kMinBlockExp));
 }
 
 // One arrival for a warp whose lanes have all done their part (their fences included).
@@ -209,7 +218,8 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
 //   full[s] / empty[s]    : ring slot s holds its item / both issuers are done with it
 //   raw_full / raw_empty  : quantised pages: codes landed / read by the converters
-//   e_full[i % 16]        : quantised pages: the exponents of block i are there
+//   e_full[i % 8]         : quantised pages: each converter warp has stored the exponents of its 32
+//                           rows of block i (the block's are the largest of the four)
 //   turn[t]               : issuer t may issue (both tiles active)
 //   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
 //                           then zeroes those rows and completes full[s] in the copy's place
@@ -285,7 +295,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&full[s], QUANT ? 4 : 1);
       mbar_init(&empty[s], 2);
     }
-    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 1);
+    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 4);
     for (int s = 0; s < NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
@@ -637,55 +647,61 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         if (!ok) break;
       }
       const int32_t* table = p.page_table + w.b * p.pt_b;
-      // a block's scales: every warp looks at all 128 rows of K and V, four a lane, one block ahead
-      float4 nk, nv;
-      auto fetch = [&](int j) {
-        const int key = (jb0 + j) * kBlockK + 4 * lane;  // four keys share a page
-        nk = nv = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (j < nb && key < sk) {
-          const int phys = __ldg(table + (key >> p.log2_page));
-          if (phys >= 0 && phys < p.n_pages) {
-            const int64_t at = ((static_cast<int64_t>(phys) * p.Hkv + kvh) << p.log2_page) + (key & (p.page_size - 1));
-            nk = __ldg(reinterpret_cast<const float4*>(p.k_scale + at));
-            nv = __ldg(reinterpret_cast<const float4*>(p.v_scale + at));
-          }
+      // Each thread's row has a scale of K and one of V per block.  The exponents of a block are stored
+      // one block ahead of their use, the scales loaded one ahead of that, and the row's page another
+      // one, as the two loads depend on each other.
+      int page2 = -1;
+      float2 cur = make_float2(0.f, 0.f), nxt = cur;  // scales of K and V
+      auto fetch_page = [&](int j) {
+        const int key = (jb0 + j) * kBlockK + row;
+        page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
+      };
+      auto fetch_scales = [&](int j) {
+        nxt = make_float2(0.f, 0.f);  // rows past kv_len or without a page: factor 0
+        if (page2 >= 0 && page2 < p.n_pages) {
+          const int64_t at = ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
+                             (((jb0 + j) * kBlockK + row) & (p.page_size - 1));
+          nxt = make_float2(ld_dep(p.k_scale + at), ld_dep(p.v_scale + at));
         }
       };
-      fetch(0);
+      auto store_exps = [&](int j) {  // scales are not negative: their bits order like they do
+        cur = nxt;
+        const int ek = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur.x)) >> 23);
+        const int ev = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur.y)) >> 23);
+        const int be = (blk + j) % kExpRing;
+        if (lane == 0) {
+          blk_exp[be * 4 + (row >> 5)] = make_int2(ek, ev);
+          mbar_arrive(&e_full[be]);
+        }
+      };
+      fetch_page(0);
+      fetch_scales(0);
+      fetch_page(1);
+      store_exps(0);
+      fetch_scales(1);
+      fetch_page(2);
       uint32_t f_v = 0;  // factor of this thread's V row, one step behind
       for (int j = 0; ok && j <= nb; ++j) {
         const uint32_t f_prev = f_v;
         uint32_t f_k = 0;
         if (j < nb) {
-          const int below = sk - ((jb0 + j) * kBlockK + 4 * lane);  // rows past kv_len may hold any scale
-          int e[2];
-          uint32_t f[2];
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const float4 n = kv == 0 ? nk : nv;
-            const float s0 = below > 0 ? n.x : 0.f, s1 = below > 1 ? n.y : 0.f, s2 = below > 2 ? n.z : 0.f,
-                        s3 = below > 3 ? n.w : 0.f;
-            const unsigned top = __reduce_max_sync(
-                0xffffffffu, __float_as_uint(fmaxf(fmaxf(s0, s1), fmaxf(s2, s3))));  // scales are not negative
-            e[kv] = max(static_cast<int>(top >> 23) - 127 - kBlockExpRoom, kMinBlockExp);
-            // the scale of this thread's row: lane row / 4 of the warp holds it
-            const int src = row >> 2;
-            const float a0 = __shfl_sync(0xffffffffu, s0, src), a1 = __shfl_sync(0xffffffffu, s1, src);
-            const float a2 = __shfl_sync(0xffffffffu, s2, src), a3 = __shfl_sync(0xffffffffu, s3, src);
-            const float own = (row & 2) ? ((row & 1) ? a3 : a2) : ((row & 1) ? a1 : a0);
-            // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
-            const float r = own * __uint_as_float(static_cast<uint32_t>(127 - e[kv]) << 23);
-            f[kv] = pack_f16x2(r, r);
+          const int be = blk + j;
+          if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
           }
-          f_k = f[0], f_v = f[1];
-          if (tid == 128) {
-            blk_exp[blk % kExpRing] = make_int2(e[0], e[1]);
-            mbar_arrive(&e_full[blk % kExpRing]);
+          const int2 e = block_exp(blk_exp + be % kExpRing * 4);
+          // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+          const float rk = cur.x * __uint_as_float(static_cast<uint32_t>(127 - e.x) << 23);
+          const float rv = cur.y * __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
+          f_k = pack_f16x2(rk, rk), f_v = pack_f16x2(rv, rv);
+          if (j + 1 < nb) {
+            store_exps(j + 1);
+            fetch_scales(j + 2);
+            fetch_page(j + 3);
           }
-          ++blk;
-          fetch(j + 1);
         }
-#pragma unroll
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           if (kv == 0 ? j == nb : j == 0) continue;  // K(j), then V(j-1)
           const int rs = g % NR, s = g % NS;
@@ -695,25 +711,21 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             break;
           }
           ++g;
+          const uint8_t* raw = sRaw + rs * C::RAW;
           uint8_t* dst = sKV + s * C::SLOT;
-          if ((jb0 + j - kv) * kBlockK + row < sk) {
-            if (kv == 0)
-              convert_row<D, C::KW>(sRaw + rs * C::RAW, dst, row, f_k);
-            else
-              convert_row<DV, C::VW>(sRaw + rs * C::RAW, dst, row, f_prev);
-          } else {  // rows past kv_len may hold anything
-#pragma unroll
-            for (int c = 0; c < (kv == 0 ? C::NCH_D : C::NCH_V); ++c)
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<uint4*>(dst + c * kBlockK * 128 + row * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
+          if (C::KW == C::VW)
+            convert_row<C::KW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, kv == 0 ? f_k : f_prev);
+          else if (kv == 0)
+            convert_row<C::KW>(raw, dst, C::NCH_D, row, f_k);
+          else
+            convert_row<C::VW>(raw, dst, C::NCH_V, row, f_prev);
           fence_proxy_async_smem();
           warp_arrive(&full[s], lane);
           if (lane == 0) mbar_arrive(&raw_empty[rs]);
         }
       }
       if (!ok) break;
+      blk += nb;
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -753,6 +765,9 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       // keys this row sees, and those every row of the tile sees
       const int lim_row = p.causal ? min(w.sk, w.len - w.n + tok + 1) : w.sk;
       const int lim_all = p.causal ? min(w.sk, w.len - w.n + w.tok0 + qt * p.tok_tile + 1) : w.sk;
+      // a warp without a valid row keeps the barriers going and leaves what tensor memory holds in P:
+      // it reaches only O rows that nobody stores
+      const bool live = __any_sync(0xffffffffu, row_valid);
       const int jb0 = w.jb0, step = alt ? 2 : 1, j0 = alt ? t : 0;  // this slot's blocks: j0 + i * step
       float row_scale2 = p.scale2;
       float m_used = -INFINITY;
@@ -762,6 +777,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         if (!mbar_wait_warp(&s_full[t], sn & 1, abort_flag, p.status)) {
           ok = false;
           break;
+        }
+        if (!live) {
+          warp_arrive(&p_half[t], lane);
+          warp_arrive(&p_full[t], lane);
+          continue;
         }
         // the query's exponent was stored before q_ready, which the MMAs behind s_full waited for
         if (CONVERT_Q && i == 0)
@@ -774,47 +794,60 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             ok = false;
             break;
           }
-          const int2 e = blk_exp[be % kExpRing];
+          const int2 e = block_exp(blk_exp + be % kExpRing * 4);
           blk_scale2 = fmaxf(blk_scale2 * __uint_as_float(static_cast<uint32_t>(127 + e.x) << 23), kMinBlkScale2);
           shift = static_cast<float>(e.y);
           unshift = __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
         }
         tc_fence_after();
-        float s[kBlockK];
-        {
-          uint32_t r0[32], r1[32], r2[32], r3[32];
-          tmem_ld32(tS + 0, r0);
-          tmem_ld32(tS + 32, r1);
-          tmem_ld32(tS + 64, r2);
-          tmem_ld32(tS + 96, r3);
-          tmem_ld_wait();
-          reg_fence(r0);
-          reg_fence(r1);
-          reg_fence(r2);
-          reg_fence(r3);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            s[c] = __uint_as_float(r0[c]);
-            s[32 + c] = __uint_as_float(r1[c]);
-            s[64 + c] = __uint_as_float(r2[c]);
-            s[96 + c] = __uint_as_float(r3[c]);
-          }
-        }
         const int k0 = (jb0 + j) * kBlockK;
-        if (k0 + kBlockK > lim_all) {  // the diagonal and the ragged last block
-          const int lim = lim_row - k0;
+        const bool edge = k0 + kBlockK > lim_all;  // the diagonal and the ragged last block hide keys
+        const int lim = lim_row - k0;
+        if (QUANT && edge) {  // in place, once for both readings
+#pragma unroll 1
+          for (int c = 0; c < kBlockK; c += 32) {
+            uint32_t r[32];
+            tmem_ld32(tS + c, r);
+            tmem_ld_wait();
+            reg_fence(r);
 #pragma unroll
-          for (int c = 0; c < kBlockK; ++c)
-            if (c >= lim) s[c] = -INFINITY;
+            for (int q = 0; q < 32; ++q)
+              if (c + q >= lim) r[q] = 0xFF800000u;
+            tmem_st32(tS + c, r);
+          }
+          tmem_st_wait();
         }
-        float mx[8];
+        // 16-bit pages: the row's 128 scores stay in registers.  Quantised pages: they are read twice,
+        // 64 columns at a time, in loops that are not unrolled (see convert_row on the instruction
+        // cache; measured 263 -> 245 us there, and 2412 -> 2582 us for 16-bit pages, which keep the short way).
+        constexpr int HELD = QUANT ? 64 : kBlockK;
+        uint32_t r[HELD / 32][32];
+        auto load = [&](int pass) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) mx[q] = fmaxf(s[q], s[8 + q]);
+          for (int q = 0; q < HELD / 32; ++q) tmem_ld32(tS + pass * HELD + q * 32, r[q]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int gi = 1; gi < kBlockK / 16; ++gi)
+          for (int q = 0; q < HELD / 32; ++q) reg_fence(r[q]);
+          if (!QUANT && edge) {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) mx[q] = fmax3(mx[q], s[16 * gi + q], s[16 * gi + 8 + q]);
-        const float mb = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+            for (int c = 0; c < HELD; ++c)
+              if (c >= lim) r[c >> 5][c & 31] = 0xFF800000u;
+          }
+        };
+        auto score = [&](int c) { return __uint_as_float(r[c >> 5][c & 31]); };
+        float mb = -INFINITY;
+#pragma unroll 1
+        for (int pass = 0; pass < kBlockK / HELD; ++pass) {
+          load(pass);
+          float mx[8];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) mx[q] = fmaxf(score(q), score(8 + q));
+#pragma unroll
+          for (int gi = 1; gi < HELD / 16; ++gi)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) mx[q] = fmax3(mx[q], score(16 * gi + q), score(16 * gi + 8 + q));
+          mb = fmaxf(mb, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+        }
         const float m_cand = fmaxf(m_used, QUANT ? fmaf(mb, blk_scale2, shift) : mb * blk_scale2);
         const bool need = m_cand > m_used + kPagedRescaleLog2;
         const bool rescale = __any_sync(0xffffffffu, need);
@@ -824,18 +857,35 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           l *= alpha;
           m_used = m_cand;
         }
+        // O holds the P.V of this slot's earlier blocks (finished: s_full covers them)
+        auto rescale_o = [&]() {
+#pragma unroll 1
+          for (int c = 0; c < DV / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + c * 32, o);
+            tmem_ld_wait();
+            reg_fence(o);
+#pragma unroll
+            for (int q = 0; q < 32; q += 2) {
+              float a = __uint_as_float(o[q]), b = __uint_as_float(o[q + 1]);
+              fmul2_scalar(a, b, alpha);
+              o[q] = __float_as_uint(a);
+              o[q + 1] = __float_as_uint(b);
+            }
+            tmem_st32(tO + c * 32, o);
+          }
+        };
         // P = 2^(y - m), rounded to 16 bits for the P.V product; the row sum takes the fp32 values.  P
-        // goes to tensor memory in two halves, so that P.V starts on the first.
+        // goes over the scores in two halves (the first one's columns hold scores that have been read),
+        // so that P.V starts on the first.
         const float neg_m = (m_used == -INFINITY) ? 0.f : (QUANT ? shift - m_used : -m_used);
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
+        auto half_row = [&](int half, int c0) {  // P of keys 64 half .. + 63, whose scores are held from c0 on
           uint32_t pk[32];
 #pragma unroll
           for (int w2 = 0; w2 < 32; ++w2) {
-            const int c = half * 64 + 2 * w2;
             float x0, x1;
-            ffma2_scalar(x0, x1, s[c], s[c + 1], blk_scale2, neg_m);
+            ffma2_scalar(x0, x1, score(c0 + 2 * w2), score(c0 + 2 * w2 + 1), blk_scale2, neg_m);
             const float p0 = ex2(x0), p1 = ex2(x1);
             pk[w2] = F16_MATH ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
             if (w2 & 1)
@@ -844,33 +894,29 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
               fadd2(ls[0], ls[1], p0, p1);
           }
           tmem_st32(tS + half * 32, pk);
-          if (half == 1) break;
-          if (rescale && i > 0) {
-#pragma unroll 1
-            for (int c = 0; c < DV / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO + c * 32, o);
-              tmem_ld_wait();
-              reg_fence(o);
-#pragma unroll
-              for (int q = 0; q < 32; q += 2) {
-                float a = __uint_as_float(o[q]), b = __uint_as_float(o[q + 1]);
-                fmul2_scalar(a, b, alpha);
-                o[q] = __float_as_uint(a);
-                o[q + 1] = __float_as_uint(b);
-              }
-              tmem_st32(tO + c * 32, o);
-            }
-          }
+        };
+        auto publish = [&](uint64_t* bar) {
           tmem_st_wait();
           tc_fence_before();
-          warp_arrive(&p_half[t], lane);
+          warp_arrive(bar, lane);
+        };
+        if constexpr (QUANT) {
+          if (rescale && i > 0) rescale_o();
+#pragma unroll 1
+          for (int half = 0; half < 2; ++half) {
+            load(half);
+            half_row(half, 0);
+            publish(half == 0 ? &p_half[t] : &p_full[t]);
+          }
+        } else {
+          half_row(0, 0);
+          if (rescale && i > 0) rescale_o();
+          publish(&p_half[t]);
+          half_row(1, 64);
+          publish(&p_full[t]);
         }
         const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
         l = QUANT ? fmaf(sum, unshift, l) : l + sum;
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&p_full[t], lane);
       }
       if (!ok) break;
 
@@ -917,7 +963,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       const int q_row = w.q_off + tok;
       uint16_t* orow = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_row) * p.o_s + static_cast<int64_t>(head) * p.o_h;
 #pragma unroll 1
-      for (int c = 0; c < DV / 32; ++c) {
+      for (int c = 0; c < (live ? DV / 32 : 0); ++c) {
         uint32_t o[32];
         tmem_ld32(tO + c * 32, o);
         tmem_ld_wait();
