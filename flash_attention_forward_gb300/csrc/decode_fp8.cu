@@ -34,7 +34,7 @@ constexpr int kF8Threads = (kDecodeWarps + 1) * 32;
 // A zero scale (the filling of pages outside the pool) counts as 2^-100, so that the maximum stays
 // finite and the sum stays below fp32's largest value.
 constexpr float kMinLog2Scale = -100.f;
-constexpr int kF8MinSplit = 256, kF8MaxSplit = 2048;
+constexpr int kF8MinSplit = 256;
 
 template <int D>
 struct DecF8Cfg {
@@ -390,7 +390,7 @@ cudaError_t launch_f8(int D, const DecodeParams& p, const CUtensorMap (&tm)[4], 
 // Keys per split: the largest of 2048 .. 256 that gives every SM of the card two CTAs (304), or
 // 256.  Longer splits write fewer partials; a few short sequences need more CTAs than that gives.
 int f8_log2_split(int B, int Hkv, int max_kv) {
-  int log2 = 11;
+  int log2 = 11;  // 2048
   while ((1 << log2) > kF8MinSplit &&
          static_cast<long long>(B) * Hkv * ((max_kv + (1 << log2) - 1) >> log2) < 304)
     --log2;

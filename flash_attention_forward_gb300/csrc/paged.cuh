@@ -15,12 +15,12 @@
 //     that few query rows over long caches, ragged batches and long chunks alike keep every SM busy to the end.
 //     A unit whose keys a cut divides writes partials (unnormalised O, max, sum) that a second
 //     kernel merges.  The cuts are planned on the device, where the lengths are (paged_plan_kernel).
-// K and V blocks take turns in one ring of equal slots, in the order of their use: K(0), then K(j) and
-// V(j-1) for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the
-// rest of the ring is loads in flight.
+// K and V blocks have a ring each and are loaded in the order of their use: K(0), then K(j) and V(j-1)
+// for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the rest of
+// the rings is loads in flight.
 //
-// Quantised pages.  Every e4m3 value is exact in fp16, so four converter warps turn a block's codes
-// into fp16 operands (one thread per row) and both products are fp16, whatever the query's type:
+// Quantised pages.  Every e4m3 value is exact in fp16, so converter warps, four for K and four for V, turn a
+// block's codes into fp16 operands (one thread per row) and both products are fp16, whatever the query's type:
 //   * K' = code * (k_scale / 2^ek), 2^(ek + 6) the power of two of the block's largest scale: the
 //     largest row lies just below fp16's largest value, rows of power-of-two scales stay exact down
 //     to 2^-21 of the largest scale and lose a bit for each one below (K' is read as 0 under
@@ -47,64 +47,69 @@ constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn mas
 constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
 constexpr int kExpRing = 8;         // blocks whose exponents are kept: more than the ring can run ahead
 
-// ONE: no sequence has more tokens than one query tile holds, so shared memory keeps one and the ring
-// takes the other's place (such calls are bound by reading the cache).
+// ONE: no sequence has more tokens than one query tile holds.  Shared memory then keeps one query tile,
+// the two accumulators take the even and the odd key blocks ("readers" 0 and 1, each with half of the
+// rings), so that one's softmax runs beside the other's MMAs, and slot 0's warps merge the two at the
+// end of a piece.  Otherwise accumulator t serves query tile t and both read every block.
 template <bool QUANT, int D, int DV, bool ONE>
 struct PagedCfg {
   static constexpr int NCH_D = D / 64, NCH_V = DV / 64;
   static constexpr int Q_BYTES = kBlockQ * D * 2;
   static constexpr int K_BYTES = kBlockK * D * 2;
   static constexpr int V_BYTES = kBlockK * DV * 2;
-  static constexpr int SLOT = K_BYTES > V_BYTES ? K_BYTES : V_BYTES;
   static constexpr int Q_TILES = ONE ? 1 : 2;
-  static constexpr int SLOTS = D == 64 ? 8 : D == 128 ? (QUANT ? 4 : ONE ? 6 : 5) : (ONE && !QUANT ? 3 : 2);
+  // slots of the rings: what 227 KB hold beside the query tiles
+  static constexpr int KS = D == 64 ? 4 : D == 128 ? (QUANT || ONE ? 2 : 3) : QUANT ? 1 : 2;
+  static constexpr int VS = D == 64 ? 4 : D == 128 ? (ONE && !QUANT ? 4 : 2) : ONE ? 2 : 1;
+  static constexpr int READERS = ONE ? 2 : 1;
+  static constexpr int KR = KS / READERS, VR = VS / READERS;  // slots of a reader
+  static_assert(KS % READERS == 0 && VS % READERS == 0, "every reader has the same slots");
   // raw codes: boxes of 128 (or 64) codes a row
   static constexpr int KW = D % 128 == 0 ? 128 : 64, VW = DV % 128 == 0 ? 128 : 64;
-  static constexpr int RAW = QUANT ? kBlockK * D : 0;
-  static constexpr int RAWS = !QUANT ? 0 : D == 64 ? 6 : D == 128 ? (ONE ? 4 : 2) : (ONE ? 3 : 1);
+  static constexpr int KRAW = QUANT ? kBlockK * D : 0, VRAW = QUANT ? kBlockK * DV : 0;
+  static constexpr int RAWS = !QUANT ? 0 : D == 64 ? 3 : ONE ? 2 : 1;  // of K, and of V
   static constexpr int QK_STEPS = D / 16, PV_STEPS = kBlockK / 16;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_SLOT = OFF_Q + Q_TILES * Q_BYTES;
-  static constexpr int OFF_RAW = OFF_SLOT + SLOTS * SLOT;
-  static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+  static constexpr int OFF_K = OFF_Q + Q_TILES * Q_BYTES;
+  static constexpr int OFF_V = OFF_K + KS * K_BYTES;
+  static constexpr int OFF_KRAW = OFF_V + VS * V_BYTES;
+  static constexpr int OFF_VRAW = OFF_KRAW + RAWS * KRAW;
+  static constexpr int OFF_BAR = OFF_VRAW + RAWS * VRAW;
   static constexpr int BARS = D == 64 ? 768 : 640;
   static constexpr int OFF_EXP = OFF_BAR + BARS;                    // int2 [kExpRing][4]
   static constexpr int OFF_QEXP = OFF_EXP + (QUANT ? kExpRing * 32 : 0);  // int8 [2 tiles][2][128]
-  // pieces announced by the producer: more than it can run ahead of the slowest role.  With m pieces behind
-  // the one whose V is used up, 2 m - 1 items lie in the rings (each piece's V waits for its softmax).
+  // pieces announced by the producer: more than it can run ahead of the slowest role.  Of the pieces
+  // behind the one whose last V is used up, each has a V that waits in the rings for its softmax.
   static constexpr int PIECES = D == 64 ? 16 : 8;
   static constexpr int OFF_PIECE = OFF_QEXP + (QUANT ? 512 : 0);
   static constexpr int OFF_ML = OFF_PIECE + PIECES * 64;            // float2 [128]: max and sum of slot 1
   static constexpr int SMEM = OFF_ML + 1024;
-  static_assert(SLOTS / 2 + 3 <= kExpRing, "the exponent ring holds what the converters write");
-  static_assert((SLOTS + RAWS) / 2 + 2 <= PIECES, "the piece ring holds what the producer announces");
-  // warpgroups: control (producer, MMA, helpers), converters (quantised), two softmax
-  static constexpr int THREADS = QUANT ? 512 : 384;
-  static constexpr int SOFTMAX_WARP = QUANT ? 8 : 4;
+  static_assert((KS > VS ? KS : VS) + 2 <= kExpRing, "the exponent ring holds what the converters write");
+  static_assert(VS + RAWS + 2 <= PIECES, "the piece ring holds what the producer announces");
+  // warpgroups: control (producer, MMA, helpers), converters of K and of V (quantised), two softmax
+  static constexpr int THREADS = QUANT ? 640 : 384;
+  static constexpr int SOFTMAX_WARP = QUANT ? 12 : 4;
   // registers per thread; the sums must stay within what the block is launched with
   static constexpr uint32_t REGS_CONTROL = QUANT ? 64 : 96;
-  static constexpr uint32_t REGS_CONVERT = 64;
-  static constexpr uint32_t REGS_SOFTMAX = QUANT ? 192 : 200;
-  static constexpr uint32_t REGS_LAUNCH = QUANT ? 128 : 168;
-  static_assert(128 * REGS_CONTROL + (QUANT ? 128 * REGS_CONVERT : 0) + 256 * REGS_SOFTMAX <= THREADS * REGS_LAUNCH,
+  static constexpr uint32_t REGS_CONVERT = 72;
+  static constexpr uint32_t REGS_SOFTMAX = QUANT ? 136 : 200;
+  static constexpr uint32_t REGS_LAUNCH = QUANT ? 96 : 168;
+  static_assert(128 * REGS_CONTROL + (QUANT ? 256 * REGS_CONVERT : 0) + 256 * REGS_SOFTMAX <= THREADS * REGS_LAUNCH,
                 "register split exceeds the launch");
   static_assert(SMEM <= 227 * 1024, "more shared memory than a CTA may opt in to");
-  static_assert(Q_BYTES % 1024 == 0 && SLOT % 1024 == 0 && RAW % 1024 == 0, "1 KB tile alignment");
+  static_assert(Q_BYTES % 1024 == 0 && K_BYTES % 1024 == 0 && V_BYTES % 1024 == 0 && KRAW % 1024 == 0 && VRAW % 1024 == 0,
+                "1 KB tile alignment");
 };
 
 // One piece of a work unit: two query tiles (2 * tok_tile tokens of one sequence, the G heads of one KV
-// head) against the key blocks [jb0, jb0 + n_blocks).  There are two S / O accumulators ("slots").
-// Normally slot t serves query tile t, and both read every block.  A unit whose tokens all lie in tile
-// 0 ("alternating") gives the even blocks to slot 0 and the odd ones to slot 1, so that one slot's
-// softmax runs beside the other's MMAs there too; slot 0's warps merge the two at the end.
+// head) against the key blocks [jb0, jb0 + n_blocks).
 struct PagedPiece {
   int b, kvh, tok0, jb0;
   int n_blocks;            // 0: no more pieces
-  int n_s[2];              // blocks of each slot
+  int n_s[2];              // blocks that each accumulator takes: those its tile sees, or the even and the odd ones
   int slot;                // partial slot, or -1: the whole unit, which stores O itself
   int q_off, n, len, sk;
-  int alt;                 // alternating
-  int pad[3];
+  int pad[4];
 };
 static_assert(sizeof(PagedPiece) == 64, "the producer announces a piece in 64 bytes");
 
@@ -124,6 +129,7 @@ struct PagedWalk {
     }
     tile = c.x, kvh = c.y, off = c.z;
   }
+  template <bool ONE>
   __device__ __forceinline__ PagedPiece next(const PagedParams& p) {
     PagedPiece w{};
     if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
@@ -143,10 +149,9 @@ struct PagedWalk {
     const int all = max(blocks[0], blocks[1]);
     const int stop = (tile == end.x && kvh == end.y) ? end.z : all;
     w.n_blocks = stop - off;
-    w.alt = blocks[1] == 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      w.n_s[t] = w.alt ? (w.n_blocks + 1 - t) / 2 : min(max(blocks[t] - off, 0), w.n_blocks);
+      w.n_s[t] = ONE ? (w.n_blocks + 1 - t) / 2 : min(max(blocks[t] - off, 0), w.n_blocks);
     w.slot = (off > 0 || stop < all) ? 2 * static_cast<int>(blockIdx.x) + 1 - first : -1;
     first = 0;
     off = 0;
@@ -213,24 +218,23 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 
 // Barriers (phases continue from piece to piece; the arrivals of warps are one each):
 //   piece[i % PIECES]     : the producer announced piece i
-//   q_full[t] / q_empty[t]: Q tile t landed / its last QK MMA finished (q_empty[2]: slot 1's last one
-//                           on tile 0 in an alternating piece)
+//   q_full[t] / q_empty[t]: Q tile t landed / accumulator t's last QK MMA of the piece finished
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
-//   full[s] / empty[s]    : ring slot s holds its item / both issuers are done with it
-//   raw_full / raw_empty  : quantised pages: codes landed / read by the converters
+//   kv_full / kv_empty    : a slot of the K or V ring holds its block / the issuers that read it are done
+//   raw_full / raw_empty  : quantised pages: codes of K (0) or V (1) landed / read by the converters
 //   e_full[i % 8]         : quantised pages: each converter warp has stored the exponents of its 32
 //                           rows of block i (the block's are the largest of the four)
 //   turn[t]               : issuer t may issue (both tiles active)
 //   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
-//                           then zeroes those rows and completes full[s] in the copy's place
-//   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels, per slot
-//   ml_full               : alternating pieces: slot 1's max and sum are there
+//                           then zeroes those rows and completes kv_full in the copy's place
+//   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels, per accumulator
+//   ml_full               : ONE: accumulator 1's max and sum are there
 template <bool BF16, bool QUANT, int D, int DV, bool ONE>
 __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
   using C = PagedCfg<QUANT, D, DV, ONE>;
-  constexpr int NS = C::SLOTS;
+  constexpr int KS = C::KS, VS = C::VS, KR = C::KR, VR = C::VR;
   constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
   constexpr bool CONVERT_Q = QUANT && BF16;
   constexpr bool F16_MATH = QUANT || !BF16;
@@ -242,12 +246,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     return;
   }
   uint8_t* sQ = smem + C::OFF_Q;
-  uint8_t* sKV = smem + C::OFF_SLOT;
-  uint8_t* sRaw = smem + C::OFF_RAW;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* q_full = bars;              // [2]
-  uint64_t* q_empty = q_full + 2;       // [3]
-  uint64_t* q_ready = q_empty + 3;      // [2]
+  uint64_t* q_empty = q_full + 2;       // [2]
+  uint64_t* q_ready = q_empty + 2;      // [2]
   uint64_t* s_full = q_ready + 2;       // [2]
   uint64_t* p_half = s_full + 2;        // [2]
   uint64_t* p_full = p_half + 2;        // [2]
@@ -256,11 +260,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   uint64_t* mma_done = o_empty + 2;     // [2]
   uint64_t* turn = mma_done + 2;        // [2]
   uint64_t* v_ragged = turn + 2;        // [kFixRing]
-  uint64_t* full = v_ragged + kFixRing;  // [NS]
-  uint64_t* empty = full + NS;          // [NS]
-  uint64_t* raw_full = empty + NS;      // [NR]
-  uint64_t* raw_empty = raw_full + NR;  // [NR]
-  uint64_t* e_full = raw_empty + NR;    // [kExpRing]
+  // one array for K (first KS or NR) and V (behind them)
+  uint64_t* kv_full = v_ragged + kFixRing;   // [KS + VS]
+  uint64_t* kv_empty = kv_full + KS + VS;    // [KS + VS]
+  uint64_t* raw_full = kv_empty + KS + VS;   // [2 NR]
+  uint64_t* raw_empty = raw_full + 2 * NR;   // [2 NR]
+  uint64_t* e_full = raw_empty + 2 * NR;    // [kExpRing]
   uint64_t* piece = e_full + kExpRing;  // [PIECES]
   uint64_t* ml_full = piece + C::PIECES;  // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ml_full + 1);
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
   PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::OFF_PIECE);
   float2* ml_x = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [128]
-  static_assert((22 + kFixRing + kExpRing + 2 * NS + 2 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
+  static_assert((21 + kFixRing + kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -289,14 +294,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&turn[t], 1);
     }
     mbar_init(ml_full, 4);
-    for (int t = 0; t < 3; ++t) mbar_init(&q_empty[t], 1);
+    for (int t = 0; t < 2; ++t) mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kFixRing; ++s) mbar_init(&v_ragged[s], 1);
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], QUANT ? 4 : 1);
-      mbar_init(&empty[s], 2);
+    for (int s = 0; s < KS + VS; ++s) {
+      mbar_init(&kv_full[s], QUANT ? 4 : 1);
+      mbar_init(&kv_empty[s], ONE ? 1 : 2);
     }
-    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 4);
-    for (int s = 0; s < NR; ++s) {
+    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 8);
+    for (int s = 0; s < 2 * NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
     }
@@ -336,17 +341,18 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     constexpr int KCOLS = QUANT ? C::KW : 64, VCOLS = QUANT ? C::VW : 64;    // columns per box
     constexpr int KROW = QUANT ? C::KW : 128, VROW = QUANT ? C::VW : 128;    // bytes of a box row
     constexpr int KTX = QUANT ? kBlockK * D : C::K_BYTES, VTX = QUANT ? kBlockK * DV : C::V_BYTES;
-    constexpr int NL = QUANT ? NR : NS;          // ring that TMA fills
-    uint64_t* ld_full = QUANT ? raw_full : full;
-    uint64_t* ld_empty = QUANT ? raw_empty : empty;
+    // the rings that TMA fills: raw ones in the order of the blocks, or those of the readers
+    constexpr int LK = QUANT ? NR : KR, LV = QUANT ? NR : VR;
+    uint64_t* ld_full = QUANT ? raw_full : kv_full;
+    uint64_t* ld_empty = QUANT ? raw_empty : kv_empty;
     const int q_tx = p.tok_tile * p.group * D * 2;
     PagedWalk walk(p);
-    int qn[2] = {0, 0}, alts = 0;
-    bool last_alt = false;  // tile 0's last piece was alternating, with blocks for slot 1
-    int g = 0, nr = 0;      // items, and ragged V blocks, issued
+    int qn[2] = {0, 0};     // pieces of each accumulator
+    int nl[2][2] = {};      // blocks of K and of V issued (16-bit pages: per reader)
+    int nr = 0;             // ragged V blocks among them
     bool ok = true;
     while (ok) {
-      const PagedPiece w = walk.next(p);
+      const PagedPiece w = walk.template next<ONE>(p);
       if (lane == 0) {
         pieces[n_piece % C::PIECES] = w;
         mbar_arrive(&piece[n_piece % C::PIECES]);
@@ -354,9 +360,10 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       ++n_piece;
       if (w.n_blocks == 0) break;
       for (int t = 0; t < kTilesPerCta && ok; ++t) {
-        if (t == 0 ? w.n_s[0] == 0 : (w.alt || w.n_s[1] == 0)) continue;
+        if (ONE ? t == 1 : w.n_s[t] == 0) continue;
+        // ONE: both accumulators have used the tile
         if ((qn[t] > 0 && !mbar_wait_warp(&q_empty[t], (qn[t] - 1) & 1, abort_flag, p.status)) ||
-            (t == 0 && last_alt && !mbar_wait_warp(&q_empty[2], (alts - 1) & 1, abort_flag, p.status))) {
+            (ONE && qn[1] > 0 && !mbar_wait_warp(&q_empty[1], (qn[1] - 1) & 1, abort_flag, p.status))) {
           ok = false;
           break;
         }
@@ -367,10 +374,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                         w.q_off + w.tok0 + t * p.tok_tile);
         }
         ++qn[t];
-        if (t == 0) {
-          last_alt = w.alt && w.n_s[1] > 0;
-          alts += last_alt;
-        }
+        if (ONE) ++qn[1];
       }
       const int32_t* table = p.page_table + w.b * p.pt_b;
       const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
@@ -388,29 +392,30 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           if (kv == 0 ? j == w.n_blocks : j == 0) continue;  // K(j), then V(j-1)
-          const int s = g % NL, r = g / NL;
-          if (r > 0 && !mbar_wait_warp(&ld_empty[s], (r - 1) & 1, abort_flag, p.status)) {
+          const int rd = ONE && !QUANT ? (j - kv) & 1 : 0;
+          const int ring = kv == 0 ? LK : LV, base = (kv == 0 ? 0 : QUANT ? NR : KS) + rd * ring;
+          const int c = rd ? nl[kv][1]++ : nl[kv][0]++;
+          const int s = c % ring, r = c / ring;
+          if (r > 0 && !mbar_wait_warp(&ld_empty[base + s], (r - 1) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          if (p.stall_first_stage && g == 0) {  // test hook: slot 0 never fills
-            ++g;
-            continue;
-          }
-          uint64_t* bar = &ld_full[s];
+          if (p.stall_first_stage && c == 0) continue;  // test hook: the first slots never fill
+          uint64_t* bar = &ld_full[base + s];
           if (!QUANT && kv == 1 && (w.jb0 + j) * kBlockK > w.sk) {
             bar = &v_ragged[nr % kFixRing];
             ++nr;
           }
           if (lane == 0) mbar_arrive_expect_tx(bar, kv == 0 ? KTX : VTX);
           __syncwarp();
-          uint8_t* dst = QUANT ? sRaw + s * C::RAW : sKV + s * C::SLOT;
+          const int at = rd * ring + s;
+          uint8_t* dst = kv == 0 ? (QUANT ? smem + C::OFF_KRAW + at * C::KRAW : sK + at * C::K_BYTES)
+                                 : (QUANT ? smem + C::OFF_VRAW + at * C::VRAW : sV + at * C::V_BYTES);
           const int parts = kv == 0 ? KPARTS : VPARTS, row_b = kv == 0 ? KROW : VROW;
           const int part = lane >> 3;  // column chunk
           if (sub < nsub && part < parts)
             tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, kv == 0 ? &tm_k : &tm_v, bar,
                         part * (kv == 0 ? KCOLS : VCOLS), w.kvh, kv == 0 ? row_k : row_v, kv == 0 ? phys_k : phys_v);
-          ++g;
         }
       }
     }
@@ -419,7 +424,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       for (int t = 0; t < kTilesPerCta; ++t)
         if (qn[t] > 0) mbar_drain(&q_full[t], (qn[t] - 1) & 1);
       for (int j = max(0, nr - kFixRing); j < nr; ++j) mbar_drain(&v_ragged[j % kFixRing], (j / kFixRing) & 1);
-      for (int j = max(0, g - NL); j < g; ++j) mbar_drain(&ld_full[j % NL], (j / NL) & 1);
+      for (int kv = 0; kv < 2; ++kv)
+        for (int rd = 0; rd < 2; ++rd) {
+          const int ring = kv == 0 ? LK : LV, base = (kv == 0 ? 0 : QUANT ? NR : KS) + rd * ring;
+          for (int j = max(0, nl[kv][rd] - ring); j < nl[kv][rd]; ++j) mbar_drain(&ld_full[base + j % ring], (j / ring) & 1);
+        }
     }
   } else if (warp == 1 || warp == 3) {
     // ------------------------------------------------------------ MMA issuers: one thread per query tile
@@ -436,129 +445,132 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       constexpr uint32_t idesc_pv = make_idesc(fmt, fmt, 0, 1, kBlockQ, DV);
       const int t = warp >> 1;
       const uint64_t dq0 = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
-      const uint64_t dk0 = make_smem_desc(smem_u32(sKV), 16, 1024, kSwizzle128B);
-      const uint64_t dv0 = make_smem_desc(smem_u32(sKV), kBlockK * 128, 1024, kSwizzle128B);
+      const uint64_t dk0 = make_smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
+      const uint64_t dv0 = make_smem_desc(smem_u32(sV), kBlockK * 128, 1024, kSwizzle128B);
       const uint32_t q_lo = static_cast<uint32_t>(dq0), q_hi = static_cast<uint32_t>(dq0 >> 32);
       const uint32_t k_lo = static_cast<uint32_t>(dk0), k_hi = static_cast<uint32_t>(dk0 >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv0), v_hi = static_cast<uint32_t>(dv0 >> 32);
       const uint32_t tS = tmem_base + t * 128;
       const uint32_t tO = tmem_base + 256 + t * 128;
-      int qn[2] = {0, 0};         // Q tiles loaded so far
+      int qn = 0;                 // loads of this accumulator's query tile so far
       int on = 0, pn = 0;         // pieces and blocks of this slot so far
       uint32_t turns = 1 - t;     // parity of the turn barrier's next phase; tile 0 begins
-      int s = 0;                  // ring slot of the next item and the parity of its phase
-      uint32_t ph = 0;
+      // slots of this reader's next K and V blocks and the parities of their phases
+      const int k0 = ONE ? t * KR : 0, v0 = ONE ? t * VR : 0;
+      int ks = k0, vs = v0;
+      uint32_t kph = 0, vph = 0;
       bool ok = true;
-      auto next = [&]() {
-        if (++s == NS) s = 0, ph ^= 1u;
+      auto next_k = [&]() {
+        if (++ks == k0 + KR) ks = k0, kph ^= 1u;
+      };
+      auto next_v = [&]() {
+        if (++vs == v0 + VR) vs = v0, vph ^= 1u;
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.status); };
+      const uint32_t dq = q_lo + static_cast<uint32_t>(((ONE ? 0 : t) * C::Q_BYTES) >> 4);
+      // O (+)= P V for keys 0-63 or 64-127 of the V block in slot v, and S = Q K^T of the K block in slot k
+      auto pv_half = [&](int half, int v, uint32_t acc) {
+        const uint32_t dv = v_lo + static_cast<uint32_t>((v * C::V_BYTES) >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < C::PV_STEPS / 2; ++kk) {
+          const int q = half * C::PV_STEPS / 2 + kk;
+          mma_f16_ts(tO, tS + q * 8, dv + static_cast<uint32_t>((q * 16 * 128) >> 4), v_hi, idesc_pv, kk > 0 ? 1u : acc);
+        }
+      };
+      auto qk = [&](int k) {
+        const uint32_t dk = k_lo + static_cast<uint32_t>((k * C::K_BYTES) >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < C::QK_STEPS; ++kk) {
+          const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
+          mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+        }
       };
       while (true) {
         const PagedPiece& w = next_piece(ok);
         const int nb = ok ? w.n_blocks : 0;
         if (nb == 0) break;
         const int n = w.n_s[t];
-        const bool alt = w.alt != 0, both = !alt && w.n_s[0] > 0 && w.n_s[1] > 0;
-        const int qt = alt ? 0 : t;  // query tile of this slot
-        if (n > 0) ok = mbar_wait(CONVERT_Q ? &q_ready[qt] : &q_full[qt], qn[qt] & 1, abort_flag, p.status);
-        if (w.n_s[0] > 0) ++qn[0];
-        if (!alt && w.n_s[1] > 0) ++qn[1];
-        const uint32_t dq = q_lo + static_cast<uint32_t>((qt * C::Q_BYTES) >> 4);
-        // Step j takes K(j) and V(j-1) from the ring: O += P(j-1) V(j-1), then S = Q K(j)^T.  In an
-        // alternating piece block j is this slot's if j % 2 == t, and S = Q K(j)^T follows
-        // O += P(j-2) V(j-2).  An item that this slot does not read is seen and passed on.
-        int vs = 0;  // slot of the V to be used next
-        for (int j = 0; ok && j <= nb + (alt ? 1 : 0); ++j) {
-          const bool qk = alt ? j < nb && (j & 1) == t : j < n;
-          const bool pv = alt ? j >= 2 && (j & 1) == t : j >= 1 && j <= n;
-          const int ks = s;
-          if (j < nb) {
-            if (!mbar_wait(&full[ks], ph, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            if (!qk) mbar_arrive(&empty[ks]);
-            next();
-          }
-          const bool v_here = j >= 1 && j <= nb;
-          if (v_here && !alt) {
-            vs = s;
-            if (!mbar_wait(&full[vs], ph, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            if (!pv) mbar_arrive(&empty[vs]);
-            next();
-          }
-          if (pv) {
-            if ((alt ? j < 4 : j == 1) && on > 0 && !mbar_wait(&o_empty[t], (on - 1) & 1, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            if (!mbar_wait(&p_half[t], pn & 1, abort_flag, p.status) ||
-                (both && !mbar_wait(&p_full[t], pn & 1, abort_flag, p.status))) {
-              ok = false;
-              break;
-            }
-          }
-          if (both) {
-            if (!mbar_wait(&turn[t], turns, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            turns ^= 1u;
-          }
-          if (pv) {
-            const uint32_t dv = v_lo + static_cast<uint32_t>((vs * C::SLOT) >> 4);
-            const uint32_t acc0 = (alt ? j >= 4 : j > 1) ? 1u : 0u;
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < C::PV_STEPS / 2; ++kk)
-              mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv,
-                         kk > 0 ? 1u : acc0);
-            // without turns, P.V starts on the first half of P while the second is computed
-            if (!both) {
-              if (!mbar_wait(&p_full[t], pn & 1, abort_flag, p.status)) {
-                ok = false;
+        if constexpr (ONE) {
+          // both issuers see every query tile and pass it on, so that none misses a phase
+          if (!(ok = wait(CONVERT_Q ? &q_ready[0] : &q_full[0], qn & 1))) break;
+          if (n == 0) mbar_arrive(&q_empty[t]);
+          if (n > 0) {
+            int vu = 0;  // slot of the last V and the parity of its phase
+            uint32_t vup = 0;
+            for (int i = 0;; ++i) {  // the reader's i-th block
+              const int ku = ks;
+              if (i < n) {
+                if (!(ok = wait(&kv_full[ku], kph))) break;
+                next_k();
+              }
+              if (i > 0) {  // O += P(i-1) V(i-1)
+                if (!(ok = (i > 1 || on == 0 || wait(&o_empty[t], (on - 1) & 1)) && wait(&kv_full[KS + vu], vup) &&
+                           wait(&p_half[t], pn & 1)))
+                  break;
+                pv_half(0, vu, i > 1 ? 1u : 0u);  // while the second half of P is computed
+                if (!(ok = wait(&p_full[t], pn & 1))) break;
+                pv_half(1, vu, 1u);
+                ++pn;
+                mma_commit(&kv_empty[KS + vu]);
+              }
+              if (i == n) {
+                mma_commit(&o_full[t]);
                 break;
               }
-              tc_fence_after();
+              qk(ku);
+              mma_commit(&s_full[t]);
+              mma_commit(&kv_empty[ku]);
+              if (i == n - 1) mma_commit(&q_empty[t]);
+              vu = vs, vup = vph;
+              next_v();
             }
-#pragma unroll
-            for (int kk = C::PV_STEPS / 2; kk < C::PV_STEPS; ++kk)
-              mma_f16_ts(tO, tS + kk * 8, dv + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi, idesc_pv, 1u);
-            ++pn;
-            if (!both) mma_commit(&empty[vs]);
+            if (!ok) break;
           }
-          if (qk) {
-            tc_fence_after();
-            const uint32_t dk = k_lo + static_cast<uint32_t>((ks * C::SLOT) >> 4);
-#pragma unroll
-            for (int kk = 0; kk < C::QK_STEPS; ++kk) {
-              const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
-              mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+          ++qn;
+        } else {
+          if (n > 0 && !(ok = wait(CONVERT_Q ? &q_ready[t] : &q_full[t], qn & 1))) break;
+          // Step j: O += P(j-1) V(j-1), then S = Q K(j)^T.  A block that this tile does not see is seen
+          // landing and passed on.
+          for (int j = 0; j <= nb; ++j) {
+            const int ku = ks, vu = vs;
+            if (j < nb) {
+              if (!(ok = wait(&kv_full[ku], kph))) break;
+              next_k();
+            }
+            if (j > 0) {
+              if (!(ok = wait(&kv_full[KS + vu], vph))) break;
+              next_v();
+            }
+            const bool pv = j > 0 && j <= n;
+            if (pv && !(ok = (j > 1 || on == 0 || wait(&o_empty[t], (on - 1) & 1)) && wait(&p_full[t], pn & 1))) break;
+            if (!(ok = wait(&turn[t], turns))) break;
+            turns ^= 1u;
+            if (pv) {
+              pv_half(0, vu, j > 1 ? 1u : 0u);
+              pv_half(1, vu, 1u);
+              ++pn;
+            }
+            if (j < n) qk(ku);
+            mbar_arrive(&turn[1 - t]);
+            if (j < n) {
+              mma_commit(&s_full[t]);
+              mma_commit(&kv_empty[ku]);
+              if (j == n - 1) mma_commit(&q_empty[t]);
+            } else if (j < nb) {
+              mbar_arrive(&kv_empty[ku]);
+            }
+            if (pv) {
+              mma_commit(&kv_empty[KS + vu]);
+              if (j == n) mma_commit(&o_full[t]);
+            } else if (j > 0) {
+              mbar_arrive(&kv_empty[KS + vu]);
             }
           }
-          if (both) mbar_arrive(&turn[1 - t]);
-          if (qk) {
-            mma_commit(&s_full[t]);
-            mma_commit(&empty[ks]);
-          }
-          if (pv && both) mma_commit(&empty[vs]);
-          if (pv && (alt ? j >= nb : j == n)) mma_commit(&o_full[t]);
-          if (qk && (alt ? j + 2 >= nb : j == n - 1)) mma_commit(&q_empty[alt && t == 1 ? 2 : t]);
-          if (v_here && alt) {  // V(j-1), behind this step's MMAs
-            if (!mbar_wait(&full[s], ph, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            if (((j - 1) & 1) == t)
-              vs = s;
-            else
-              mbar_arrive(&empty[s]);
-            next();
-          }
+          if (!ok) break;
+          if (n > 0) ++qn;
         }
-        if (!ok) break;
         if (n > 0) ++on;
       }
       // every MMA issued so far has finished before tensor memory is released
@@ -570,7 +582,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     if constexpr (!QUANT) {
       // ---------------------------------------------------------- V rows past kv_len -> 0 (one warp)
       if (warp == 2) {
-        int g = 0, nr = 0;
+        int nv[2] = {0, 0}, nr = 0;  // V blocks of each reader in the pieces before; ragged blocks
         bool ok = true;
         while (true) {
           const PagedPiece& w = next_piece(ok);
@@ -579,10 +591,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           const int last = w.n_blocks - 1;  // only the last block can end past kv_len
           const int live = w.sk - (w.jb0 + last) * kBlockK;
           if (live < kBlockK) {
-            const int s = (g + 2 * last + 1) % NS;
+            const int rd = ONE ? last & 1 : 0;
+            const int s = rd * VR + (rd ? nv[1] + (last >> 1) : nv[0] + (ONE ? last >> 1 : last)) % VR;
             if (!mbar_wait_warp(&v_ragged[nr % kFixRing], (nr / kFixRing) & 1, abort_flag, p.status)) break;
             ++nr;
-            uint8_t* v = sKV + s * C::SLOT;
+            uint8_t* v = sV + s * C::V_BYTES;
             // whole 128-byte rows of every column chunk: the swizzle stays inside a row
             for (int u = lane + max(live, 0) * 8; u < kBlockK * 8; u += 32)
 #pragma unroll
@@ -590,18 +603,22 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                 *reinterpret_cast<uint4*>(v + c * kBlockK * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
+            if (lane == 0) mbar_arrive(&kv_full[KS + s]);
           }
-          g += 2 * w.n_blocks;
+          nv[0] += ONE ? w.n_s[0] : w.n_blocks;
+          nv[1] += ONE ? w.n_s[1] : 0;
         }
       }
     }
-  } else if (QUANT && warp < 8) {
+  } else if (QUANT && warp < 12) {
     // ------------------------------------------------------------ converters: codes -> fp16 operands
     regs_dec<C::REGS_CONVERT>();
-    const int row = tid - 128;  // tile row of this thread
-    int qn[2] = {0, 0};
-    int g = 0, blk = 0;
+    const int kv = (warp - 4) >> 2;   // 0: K, 1: V
+    const int row = tid & 127;        // tile row of this thread
+    const float* scale = kv == 0 ? p.k_scale : p.v_scale;
+    int qn = 0;
+    int blk = 0;                      // blocks of the pieces before this one
+    int nc[2] = {0, 0};               // those of each reader
     bool ok = true;
     while (true) {
       const PagedPiece& w = next_piece(ok);
@@ -609,13 +626,38 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       const int nb = ok ? w.n_blocks : 0;
       if (nb == 0) break;
       const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
+      const int32_t* table = p.page_table + w.b * p.pt_b;
+      // The scale of this thread's row in each block.  The exponents of a block are stored one block
+      // ahead of their use, the scales loaded one ahead of that, and the row's page another one, as
+      // the two loads depend on each other.
+      int page2 = -1;
+      float cur = 0.f, nxt = 0.f;
+      auto fetch_page = [&](int j) {
+        const int key = (jb0 + j) * kBlockK + row;
+        page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
+      };
+      auto fetch_scale = [&](int j) {
+        nxt = 0.f;  // rows past kv_len or without a page: factor 0
+        if (page2 >= 0 && page2 < p.n_pages)
+          nxt = ld_dep(scale + ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
+                       (((jb0 + j) * kBlockK + row) & (p.page_size - 1)));
+      };
+      auto store_exp = [&](int j) {  // scales are not negative: their bits order like they do
+        cur = nxt;
+        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur)) >> 23);
+        const int be = (blk + j) % kExpRing;
+        if (lane == 0) {
+          reinterpret_cast<int*>(blk_exp + be * 4 + (row >> 5))[kv] = e;
+          mbar_arrive(&e_full[be]);
+        }
+      };
+      fetch_page(0);
+      fetch_scale(0);
+      fetch_page(1);
       if constexpr (CONVERT_Q) {
-        for (int t = 0; t < kTilesPerCta && ok; ++t) {
-          if (t == 0 ? w.n_s[0] == 0 : (w.alt || w.n_s[1] == 0)) continue;
-          if (!mbar_wait_warp(&q_full[t], qn[t] & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
+        const int t = kv;  // the converters of K take query tile 0, those of V tile 1
+        if (ONE ? t == 0 : w.n_s[t] > 0) {
+          if (!mbar_wait_warp(&q_full[t], qn & 1, abort_flag, p.status)) break;
           uint8_t* q = sQ + t * C::Q_BYTES + row * 128;
           float amax = 0.f;
 #pragma unroll 4
@@ -636,96 +678,52 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                               pack_f16x2(bf16lo_f32(v.z) * mul, bf16hi_f32(v.z) * mul),
                               pack_f16x2(bf16lo_f32(v.w) * mul, bf16hi_f32(v.w) * mul));
           }
-          // exponent of `back`, in [-126, 113]; two buffers, as the next unit's tile may be converted
+          // exponent of `back`, in [-126, 113]; two buffers, as the next piece's tile may be converted
           // before this one's softmax has begun
-          q_exp[(t * 2 + (qn[t] & 1)) * 128 + row] =
+          q_exp[(t * 2 + (qn & 1)) * 128 + row] =
               static_cast<int8_t>(static_cast<int>(__float_as_uint(back) >> 23) - 127);
           fence_proxy_async_smem();
           warp_arrive(&q_ready[t], lane);
-          ++qn[t];
+          ++qn;
         }
-        if (!ok) break;
       }
-      const int32_t* table = p.page_table + w.b * p.pt_b;
-      // Each thread's row has a scale of K and one of V per block.  The exponents of a block are stored
-      // one block ahead of their use, the scales loaded one ahead of that, and the row's page another
-      // one, as the two loads depend on each other.
-      int page2 = -1;
-      float2 cur = make_float2(0.f, 0.f), nxt = cur;  // scales of K and V
-      auto fetch_page = [&](int j) {
-        const int key = (jb0 + j) * kBlockK + row;
-        page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
-      };
-      auto fetch_scales = [&](int j) {
-        nxt = make_float2(0.f, 0.f);  // rows past kv_len or without a page: factor 0
-        if (page2 >= 0 && page2 < p.n_pages) {
-          const int64_t at = ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
-                             (((jb0 + j) * kBlockK + row) & (p.page_size - 1));
-          nxt = make_float2(ld_dep(p.k_scale + at), ld_dep(p.v_scale + at));
-        }
-      };
-      auto store_exps = [&](int j) {  // scales are not negative: their bits order like they do
-        cur = nxt;
-        const int ek = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur.x)) >> 23);
-        const int ev = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur.y)) >> 23);
-        const int be = (blk + j) % kExpRing;
-        if (lane == 0) {
-          blk_exp[be * 4 + (row >> 5)] = make_int2(ek, ev);
-          mbar_arrive(&e_full[be]);
-        }
-      };
-      fetch_page(0);
-      fetch_scales(0);
-      fetch_page(1);
-      store_exps(0);
-      fetch_scales(1);
+      store_exp(0);
+      fetch_scale(1);
       fetch_page(2);
-      uint32_t f_v = 0;  // factor of this thread's V row, one step behind
-      for (int j = 0; ok && j <= nb; ++j) {
-        const uint32_t f_prev = f_v;
-        uint32_t f_k = 0;
-        if (j < nb) {
-          const int be = blk + j;
-          if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const int2 e = block_exp(blk_exp + be % kExpRing * 4);
-          // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
-          const float rk = cur.x * __uint_as_float(static_cast<uint32_t>(127 - e.x) << 23);
-          const float rv = cur.y * __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
-          f_k = pack_f16x2(rk, rk), f_v = pack_f16x2(rv, rv);
-          if (j + 1 < nb) {
-            store_exps(j + 1);
-            fetch_scales(j + 2);
-            fetch_page(j + 3);
-          }
-        }
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          if (kv == 0 ? j == nb : j == 0) continue;  // K(j), then V(j-1)
-          const int rs = g % NR, s = g % NS;
-          if (!mbar_wait_warp(&raw_full[rs], (g / NR) & 1, abort_flag, p.status) ||
-              (g >= NS && !mbar_wait_warp(&empty[s], (g / NS - 1) & 1, abort_flag, p.status))) {
-            ok = false;
-            break;
-          }
-          ++g;
-          const uint8_t* raw = sRaw + rs * C::RAW;
-          uint8_t* dst = sKV + s * C::SLOT;
-          if (C::KW == C::VW)
-            convert_row<C::KW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, kv == 0 ? f_k : f_prev);
-          else if (kv == 0)
-            convert_row<C::KW>(raw, dst, C::NCH_D, row, f_k);
-          else
-            convert_row<C::VW>(raw, dst, C::NCH_V, row, f_prev);
-          fence_proxy_async_smem();
-          warp_arrive(&full[s], lane);
-          if (lane == 0) mbar_arrive(&raw_empty[rs]);
+      for (int j = 0; j < nb; ++j) {
+        const int be = blk + j;
+        const int rs = be % NR;
+        const int rd = ONE ? j & 1 : 0;
+        const int ring = kv == 0 ? KR : VR, c = ONE ? (rd ? nc[1] : nc[0]) + (j >> 1) : be;
+        const int s = rd * ring + c % ring, base = kv == 0 ? 0 : KS;
+        ok = mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status);
+        if (!ok) break;
+        const int2 e = block_exp(blk_exp + be % kExpRing * 4);
+        // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+        const float r = cur * __uint_as_float(static_cast<uint32_t>(127 - (kv == 0 ? e.x : e.y)) << 23);
+        const uint32_t f = pack_f16x2(r, r);
+        if (j + 1 < nb) {
+          store_exp(j + 1);
+          fetch_scale(j + 2);
+          fetch_page(j + 3);
         }
+        ok = mbar_wait_warp(&raw_full[kv * NR + rs], (be / NR) & 1, abort_flag, p.status) &&
+             (c < ring || mbar_wait_warp(&kv_empty[base + s], (c / ring - 1) & 1, abort_flag, p.status));
+        if (!ok) break;
+        const uint8_t* raw = kv == 0 ? smem + C::OFF_KRAW + rs * C::KRAW : smem + C::OFF_VRAW + rs * C::VRAW;
+        uint8_t* dst = kv == 0 ? sK + s * C::K_BYTES : sV + s * C::V_BYTES;
+        if (C::KW == C::VW || kv == 1)
+          convert_row<C::VW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, f);
+        else
+          convert_row<C::KW>(raw, dst, C::NCH_D, row, f);
+        fence_proxy_async_smem();
+        warp_arrive(&kv_full[base + s], lane);
+        if (lane == 0) mbar_arrive(&raw_empty[kv * NR + rs]);
       }
       if (!ok) break;
       blk += nb;
+      nc[0] += (nb + 1) / 2, nc[1] += nb / 2;
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -739,9 +737,9 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     // (token, head) of this thread's row
     const int row_tok = static_cast<int>(fast_div(static_cast<uint32_t>(row), p.div_group));
     const int row_head = row - row_tok * p.group;
-    int sn = 0, on[2] = {0, 0};  // S blocks of this slot; pieces of each slot
-    int qn[2] = {0, 0};          // Q tiles loaded
-    int blk = 0, alts = 0;
+    int sn = 0, on[2] = {0, 0};  // S blocks of this accumulator; pieces of each
+    int qn = 0;                  // loads of its query tile
+    int blk = 0, merges = 0;
     bool ok = true;
     while (true) {
       const PagedPiece& w = next_piece(ok);
@@ -751,11 +749,10 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       const int blk0 = blk;
       blk += nb;
       const int n = w.n_s[t], n_other = w.n_s[1 - t];
-      const bool alt = w.alt != 0, merge = alt && w.n_s[1] > 0;
-      const int qt = alt ? 0 : t;
-      const int q_par = qn[qt] & 1;
-      if (w.n_s[0] > 0) ++qn[0];
-      if (!alt && w.n_s[1] > 0) ++qn[1];
+      const bool merge = ONE && w.n_s[1] > 0;
+      const int qt = ONE ? 0 : t;
+      const int q_par = qn & 1;
+      if (ONE || n > 0) ++qn;
       if (n == 0) {
         if (n_other > 0) ++on[1 - t];
         continue;
@@ -768,7 +765,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       // a warp without a valid row keeps the barriers going and leaves what tensor memory holds in P:
       // it reaches only O rows that nobody stores
       const bool live = __any_sync(0xffffffffu, row_valid);
-      const int jb0 = w.jb0, step = alt ? 2 : 1, j0 = alt ? t : 0;  // this slot's blocks: j0 + i * step
+      const int jb0 = w.jb0, step = ONE ? 2 : 1, j0 = ONE ? t : 0;  // its blocks: j0 + i * step
       float row_scale2 = p.scale2;
       float m_used = -INFINITY;
       float l = 0.f;
@@ -857,7 +854,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           l *= alpha;
           m_used = m_cand;
         }
-        // O holds the P.V of this slot's earlier blocks (finished: s_full covers them)
+        // O holds the P.V of the earlier blocks (finished: s_full covers them)
         auto rescale_o = [&]() {
 #pragma unroll 1
           for (int c = 0; c < DV / 32; ++c) {
@@ -922,7 +919,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
 
       // ---------------------------------------------------------- epilogue: O / l and LSE, or a partial
       if (merge && t == 1) {
-        // slot 0's warps merge: hand them this slot's max and sum; they read O from tensor memory
+        // accumulator 0's warps merge: hand them the max and sum; they read O from tensor memory
         // (o_empty: they have read the piece before)
         if (on[1] > 0 && !mbar_wait_warp(&o_empty[1], (on[1] - 1) & 1, abort_flag, p.status)) {
           ok = false;
@@ -937,15 +934,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         ok = false;
         break;
       }
-      float w0 = 1.f, w1 = 0.f;  // weights of this slot's O and, merging, of slot 1's
+      float w0 = 1.f, w1 = 0.f;  // weights of this O and, merging, of accumulator 1's
       if (merge) {
-        if (!mbar_wait_warp(ml_full, alts & 1, abort_flag, p.status) ||
+        if (!mbar_wait_warp(ml_full, merges & 1, abort_flag, p.status) ||
             !mbar_wait_warp(&o_full[1], on[1] & 1, abort_flag, p.status)) {
           ok = false;
           break;
         }
         const float2 other = ml_x[row];
-        ++alts;
+        ++merges;
         const float top = fmaxf(m_used, other.x);
         w0 = m_used == -INFINITY ? 0.f : ex2(m_used - top);
         w1 = other.x == -INFINITY ? 0.f : ex2(other.x - top);
@@ -1047,8 +1044,10 @@ cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const
 template <bool BF16, bool QUANT, int D, int DV>
 cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const PagedParams& p, cudaStream_t st) {
-  return p.max_seqlen_q <= p.tok_tile ? launch_paged_one<BF16, QUANT, D, DV, true>(tq, tk, tv, p, st)
-                                      : launch_paged_one<BF16, QUANT, D, DV, false>(tq, tk, tv, p, st);
+  // three-block operands leave no room for two readers' rings beside the raw codes
+  if constexpr (!(QUANT && D == 192))
+    if (p.max_seqlen_q <= p.tok_tile) return launch_paged_one<BF16, QUANT, D, DV, true>(tq, tk, tv, p, st);
+  return launch_paged_one<BF16, QUANT, D, DV, false>(tq, tk, tv, p, st);
 }
 
 }  // namespace sdpa
