@@ -119,21 +119,15 @@ struct PagedWalk {
   int tile, kvh, off, first;
   int4 end;
 
-  __device__ __forceinline__ explicit PagedWalk(const PagedParams& p) : first(1) {
-    const int n = ld_dep(&p.plan.head->n_ctas);
-    int4 c = make_int4(0, 0, 0, 0);
-    end = c;
-    if (static_cast<int>(blockIdx.x) < n) {
-      c = ld_dep(p.plan.cuts + blockIdx.x);
-      end = ld_dep(p.plan.cuts + blockIdx.x + 1);
-    }
-    tile = c.x, kvh = c.y, off = c.z;
-  }
+  __device__ __forceinline__ PagedWalk(int4 from, int4 to) : tile(from.x), kvh(from.y), off(from.z), first(1), end(to) {}
   template <bool ONE>
   __device__ __forceinline__ PagedPiece next(const PagedParams& p) {
     PagedPiece w{};
+    // planned by this kernel, tiles are sequences, and those without tokens are passed over
+    if (ONE && p.inline_plan)
+      while (tile < end.x && __ldg(p.cu_q + tile) == __ldg(p.cu_q + tile + 1)) ++tile;
     if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
-    const int2 at = ld_dep(p.plan.tiles + tile);
+    const int2 at = ONE && p.inline_plan ? make_int2(tile, 0) : ld_dep(p.plan.tiles + tile);
     w.b = at.x;
     w.kvh = kvh;
     w.q_off = __ldg(p.cu_q + w.b);
@@ -214,6 +208,82 @@ __device__ __forceinline__ int2 block_exp(const int2* parts) {
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
+}
+
+// The plan where every sequence has one query tile, by each CTA for itself: a scan over the sequences'
+// lengths on the line, then this CTA's two cuts; CTA 0 stores all of them and the cut units for the merge.
+// Spares the launch of a planning kernel and the wait for it (some 8 us of a call of 110).
+// scratch: 8 KB of shared memory that nobody uses yet.  All threads; returns the cuts in `mine`.
+template <int THREADS>
+__device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine) {
+  static_assert(THREADS >= kInlinePlanSeqs && THREADS > kPagedMaxCtas, "one thread per sequence and per cut");
+  long long* pos = reinterpret_cast<long long*>(scratch);               // [kInlinePlanSeqs + 1]
+  long long* warp_sum = pos + kInlinePlanSeqs + 1;                       // [THREADS / 32]
+  int4* cuts = reinterpret_cast<int4*>(scratch + 4096);                  // [kPagedMaxCtas + 1]
+  int* n_groups = reinterpret_cast<int*>(cuts + kPagedMaxCtas + 1);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int bad = 0, n = 0, len = 0;
+  long long v = 0;
+  if (tid < p.B) {
+    const int q0 = __ldg(p.cu_q + tid), q1 = __ldg(p.cu_q + tid + 1);
+    len = __ldg(p.kv_len + tid);
+    bad = q0 < 0 || q1 < q0 || q1 > p.total_q || static_cast<long long>(q1) - q0 > p.max_seqlen_q;
+    n = q1 - q0;
+    if (!bad && n > 0)
+      v = static_cast<long long>(paged_tile_blocks(n, len, min(max(len, 0), p.max_kv), p.tok_tile, p.causal, 0) + kUnitCost) *
+          p.Hkv;
+  }
+  long long incl = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, incl, d);
+    if (lane >= d) incl += y;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  if (tid == 0) *n_groups = 0;
+  bad = __syncthreads_or(bad);
+  const int units = __syncthreads_count(v > 0) * p.Hkv;
+  for (int w = 0; w < warp; ++w) incl += warp_sum[w];
+  if (tid < p.B) pos[tid + 1] = incl;
+  if (tid == 0) pos[0] = 0;
+  __syncthreads();
+  const long long total = pos[p.B];
+  const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / kMinWork)));
+  const int cta = blockIdx.x;
+  auto cut_at = [&](int c) {
+    if (c >= n_ctas) return make_int4(bad ? 0 : p.B, 0, 0, 0);
+    const long long x = total / n_ctas * c + total % n_ctas * c / n_ctas;
+    int lo = 0, hi = p.B;  // the last sequence that starts at or before x (it has tokens)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pos[mid] <= x) lo = mid; else hi = mid;
+    }
+    return paged_cut(p, x, pos[lo], lo, static_cast<int>((pos[lo + 1] - pos[lo]) / p.Hkv) - kUnitCost);
+  };
+  if (cta < n_ctas) {
+    if (tid == 0) mine[0] = cut_at(cta);
+    if (tid == 32) mine[1] = cut_at(cta + 1);
+  } else if (tid == 0) {
+    mine[0] = mine[1] = make_int4(0, 0, 0, 0);
+  }
+  if (cta == 0) {  // for the merge
+    if (tid <= n_ctas) p.plan.cuts[tid] = cuts[tid] = cut_at(tid);
+    __syncthreads();
+    if (tid < n_ctas && cuts[tid].z != 0) {
+      const int b = cuts[tid].x, q0 = __ldg(p.cu_q + b);
+      PagedGroup g;
+      if (paged_group(cuts, tid, n_ctas, make_int2(b, 0), q0, __ldg(p.cu_q + b + 1) - q0, __ldg(p.kv_len + b), g))
+        p.plan.groups[atomicAdd(n_groups, 1)] = g;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      p.plan.head->n_ctas = n_ctas;
+      p.plan.head->n_groups = *n_groups;
+      if (bad) atomicOr(p.status, kStatusBadSeqlens);
+    }
+  }
+  fence_proxy_async_smem();  // TMA writes the scratch next
+  __syncthreads();
 }
 
 // Barriers (phases continue from piece to piece; the arrivals of warps are one each):
@@ -317,7 +387,18 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  pdl_wait();  // the plan comes from the kernel launched before
+  int4 cuts[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
+  if (ONE && p.inline_plan) {
+    int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // not announced before the producer has read it
+    paged_inline_plan<C::THREADS>(p, sQ, mine);
+    if (warp == 0) cuts[0] = mine[0], cuts[1] = mine[1];
+  } else {
+    pdl_wait();  // the plan comes from the kernel launched before
+    if (warp == 0 && static_cast<int>(blockIdx.x) < ld_dep(&p.plan.head->n_ctas)) {
+      cuts[0] = ld_dep(p.plan.cuts + blockIdx.x);
+      cuts[1] = ld_dep(p.plan.cuts + blockIdx.x + 1);
+    }
+  }
   // the next announced piece, for the other roles
   int n_piece = 0;
   auto next_piece = [&](bool& ok) -> const PagedPiece& {
@@ -346,7 +427,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     uint64_t* ld_full = QUANT ? raw_full : kv_full;
     uint64_t* ld_empty = QUANT ? raw_empty : kv_empty;
     const int q_tx = p.tok_tile * p.group * D * 2;
-    PagedWalk walk(p);
+    PagedWalk walk(cuts[0], cuts[1]);
     int qn[2] = {0, 0};     // pieces of each accumulator
     int nl[2][2] = {};      // blocks of K and of V issued (16-bit pages: per reader)
     int nr = 0;             // ragged V blocks among them
@@ -1017,7 +1098,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   }
 }
 
-// Launches the kernel as a programmatic dependent of the plan kernel, one CTA per SM.
+// Launches the kernel, one CTA per SM: as a programmatic dependent of the plan kernel, if there is one.
 template <bool BF16, bool QUANT, int D, int DV, bool ONE>
 cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
                              cudaStream_t st) {
@@ -1037,7 +1118,7 @@ cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
   cfg.attrs = pdl;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = p.inline_plan ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
 }
 

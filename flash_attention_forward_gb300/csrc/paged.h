@@ -18,20 +18,30 @@ constexpr int kMinPiece = 3;         // blocks
 constexpr int kMinWork = 6;          // blocks per CTA below which more CTAs do not pay (unless units are left)
 constexpr int kPagedMaxCtas = 160;
 
-// The plan, written by paged_plan_kernel at the start of the workspace.
+// The plan, at the start of the workspace: written by paged_plan_kernel, or by the attention kernel
+// itself where every sequence has one query tile (kInlinePlanSeqs sequences at most); a "tile" is then a sequence.
+constexpr int kInlinePlanSeqs = 256;
+// A cut unit, for the merge.
+struct PagedGroup {
+  int32_t tile, kvh;       // tile in its sequence, KV head
+  int32_t first, pieces;   // CTA of the first piece; the others follow
+  int32_t slot0;           // partial slot of the first piece (the others: 2 * CTA)
+  int32_t q_off, n, len;   // the sequence's packed offset, tokens and cache length
+};
+static_assert(sizeof(PagedGroup) == 2 * sizeof(int4), "read as two vectors");
 struct PagedPlanHeader {
   int32_t n_ctas, n_groups, pad[2];
 };
 struct PagedPlan {
   PagedPlanHeader* head;
   int4* cuts;              // [kPagedMaxCtas + 1] {tile, KV head, key block, 0}
-  int4* groups;            // [kPagedMaxCtas] cut units: {tile, KV head, first CTA, pieces}
+  PagedGroup* groups;      // [kPagedMaxCtas] cut units
   int2* tiles;             // [n_tiles] {sequence, tile in it}
   long long* tile_pos;     // [n_tiles + 1] start of a tile's units on the line
   int32_t* seq_tiles;      // [B + 1] tiles of the sequences before b
 };
 inline size_t paged_plan_bytes(int B, long long n_tiles) {
-  return split_round16(sizeof(PagedPlanHeader) + (2 * kPagedMaxCtas + 1) * sizeof(int4) +
+  return split_round16(sizeof(PagedPlanHeader) + (kPagedMaxCtas + 1) * sizeof(int4) + kPagedMaxCtas * sizeof(PagedGroup) +
                        static_cast<size_t>(n_tiles) * (sizeof(int2) + sizeof(long long)) + sizeof(long long) +
                        (static_cast<size_t>(B) + 1) * sizeof(int32_t));
 }
@@ -40,7 +50,7 @@ inline PagedPlan paged_plan_at(void* ws, long long n_tiles) {
   char* c = static_cast<char*>(ws);
   p.head = reinterpret_cast<PagedPlanHeader*>(c);
   p.cuts = reinterpret_cast<int4*>(p.head + 1);
-  p.groups = p.cuts + kPagedMaxCtas + 1;
+  p.groups = reinterpret_cast<PagedGroup*>(p.cuts + kPagedMaxCtas + 1);
   p.tile_pos = reinterpret_cast<long long*>(p.groups + kPagedMaxCtas);
   p.tiles = reinterpret_cast<int2*>(p.tile_pos + n_tiles + 1);
   p.seq_tiles = reinterpret_cast<int32_t*>(p.tiles + n_tiles);
@@ -67,6 +77,7 @@ struct PagedParams {
   int max_kv;              // max_pages * page_size
   int slot_rows, cut, sms; // cut: the workspace holds partials, units may be cut
   int max_tiles;           // tiles the plan has room for
+  int inline_plan;         // the attention kernel plans for itself
   int stall_first_stage;   // test hook
   float scale2;            // scale * log2(e)
   FastDiv div_group;
@@ -85,6 +96,37 @@ __host__ __device__ __forceinline__ int paged_tile_blocks(int n, int len, int sk
     keys = keys < vis ? keys : vis;
   }
   return keys > kBlockK ? (keys + kBlockK - 1) / kBlockK : 1;
+}
+#endif
+
+#ifdef __CUDACC__
+// Where cut c of n_ctas lies: position x of the line falls into a unit of `blocks` key blocks that starts
+// at `start` for KV head 0 (the tile's units follow one another).  {tile, KV head, block}.
+__device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, long long start, int tile, int blocks) {
+  const int r = static_cast<int>(x - start);
+  int kvh = r / (blocks + kUnitCost);
+  int off = r - kvh * (blocks + kUnitCost) - kUnitCost;
+  if (p.cut ? off < kMinPiece : 2 * off < blocks) {
+    off = 0;
+  } else if (!p.cut || blocks - off < kMinPiece) {
+    off = 0;
+    if (++kvh == p.Hkv) kvh = 0, ++tile;
+  }
+  return make_int4(tile, kvh, off, 0);
+}
+// The group of a unit whose first cut is cut c (cuts[c].z > 0 and not cut before), or false.
+__device__ __forceinline__ bool paged_group(const int4* cuts, int c, int n_ctas, int2 at, int q_off, int n, int len,
+                                            PagedGroup& g) {
+  const int4 cut = cuts[c];
+  if (cut.z == 0) return false;
+  const int4 prev = cuts[c - 1];  // c > 0: the line starts with a whole unit
+  if (prev.x == cut.x && prev.y == cut.y && prev.z > 0) return false;
+  int pieces = 2;
+  while (c + pieces - 1 < n_ctas && cuts[c + pieces - 1].x == cut.x && cuts[c + pieces - 1].y == cut.y) ++pieces;
+  // the first piece is CTA c - 1's last one, and its first one too if the CTA starts with it
+  const int slot0 = 2 * (c - 1) + (prev.x == cut.x && prev.y == cut.y ? 0 : 1);
+  g = PagedGroup{at.y, cut.y, c - 1, pieces, slot0, q_off, n, len};
+  return true;
 }
 #endif
 

@@ -37,8 +37,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long before, l
   return before + v + (warp > 0 ? prev : 0);
 }
 
-__device__ __forceinline__ int unit_blocks(const PagedParams& p, int b, int i) {
-  const int n = __ldg(p.cu_q + b + 1) - __ldg(p.cu_q + b), len = __ldg(p.kv_len + b);
+__device__ __forceinline__ int unit_blocks(const PagedParams& p, int n, int len, int i) {
   const int sk = min(max(len, 0), p.max_kv);
   return max(paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta),
              paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta + 1));
@@ -46,11 +45,16 @@ __device__ __forceinline__ int unit_blocks(const PagedParams& p, int b, int i) {
 
 // One block lays out the tiles, measures the line and places the cuts.  Offsets that are not sorted
 // within [0, total_q], or a sequence of more than max_seqlen_q tokens, raise a status and leave no
-// work, so nothing is stored.
+// work, so nothing is stored.  Up to kSmall sequences and tiles are kept in shared memory as well.
+constexpr int kSmall = 1024;
+
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedParams p) {
   __shared__ long long warp_sum[33];
   __shared__ int4 s_cuts[kPagedMaxCtas + 1];
   __shared__ int s_groups;
+  __shared__ int s_seq[kSmall];
+  __shared__ int2 s_tile[kSmall];
+  __shared__ long long s_pos[kSmall];
   const int tid = threadIdx.x;
   pdl_launch_dependents();  // the attention kernel may set itself up meanwhile
   if (tid == 0) s_groups = 0;
@@ -69,7 +73,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     }
     const long long before = n_tiles;
     const long long incl = block_scan(v, before, warp_sum, n_tiles);
-    if (b < p.B) p.plan.seq_tiles[b] = static_cast<int32_t>(min(incl - v, static_cast<long long>(p.max_tiles)));
+    if (b < p.B) {
+      const int at = static_cast<int>(min(incl - v, static_cast<long long>(p.max_tiles)));
+      if (p.B <= kSmall)
+        s_seq[b] = at;
+      else
+        p.plan.seq_tiles[b] = at;
+    }
   }
   if (__syncthreads_or(bad) || n_tiles > p.max_tiles) {
     if (tid == 0) {
@@ -78,6 +88,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     }
     return;
   }
+  const int* seq = p.B <= kSmall ? s_seq : p.plan.seq_tiles;
+  const bool small = n_tiles <= kSmall;
   long long total = 0;
   for (int base = 0; base < n_tiles; base += kPlanThreads) {
     const int tile = base + tid;
@@ -86,17 +98,26 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
       int lo = 0, hi = p.B;  // the last sequence that starts at or before the tile
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.plan.seq_tiles[mid] <= tile) lo = mid; else hi = mid;
+        if (seq[mid] <= tile) lo = mid; else hi = mid;
       }
-      const int i = tile - p.plan.seq_tiles[lo];
-      p.plan.tiles[tile] = make_int2(lo, i);
-      v = static_cast<long long>(unit_blocks(p, lo, i) + kUnitCost) * p.Hkv;
+      const int2 at = make_int2(lo, tile - seq[lo]);
+      p.plan.tiles[tile] = at;
+      if (small) s_tile[tile] = at;
+      const int n = __ldg(p.cu_q + lo + 1) - __ldg(p.cu_q + lo);
+      v = static_cast<long long>(unit_blocks(p, n, __ldg(p.kv_len + lo), at.y) + kUnitCost) * p.Hkv;
     }
     const long long before = total;
     const long long incl = block_scan(v, before, warp_sum, total);
-    if (tile < n_tiles) p.plan.tile_pos[tile] = incl - v;
+    if (tile < n_tiles) {
+      if (small)
+        s_pos[tile] = incl - v;
+      else
+        p.plan.tile_pos[tile] = incl - v;
+    }
   }
   __syncthreads();
+  const long long* pos = small ? s_pos : p.plan.tile_pos;
+  const int2* tiles = small ? s_tile : p.plan.tiles;
   // as many CTAs as have kMinWork each, and at least one for every unit
   const int n_ctas = static_cast<int>(min(static_cast<long long>(p.sms), max(n_tiles * p.Hkv, total / kMinWork)));
   for (int c = tid; c <= n_ctas; c += kPlanThreads) {
@@ -106,34 +127,23 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
       int lo = 0, hi = static_cast<int>(n_tiles);
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.plan.tile_pos[mid] <= x) lo = mid; else hi = mid;
+        if (pos[mid] <= x) lo = mid; else hi = mid;
       }
-      const int2 at = p.plan.tiles[lo];
-      const int blocks = unit_blocks(p, at.x, at.y);
-      const int r = static_cast<int>(x - p.plan.tile_pos[lo]);
-      int kvh = r / (blocks + kUnitCost);
-      int off = r - kvh * (blocks + kUnitCost) - kUnitCost;
-      if (p.cut ? off < kMinPiece : 2 * off < blocks) {
-        off = 0;
-      } else if (!p.cut || blocks - off < kMinPiece) {
-        off = 0;
-        if (++kvh == p.Hkv) kvh = 0, ++lo;
-      }
-      cut = make_int4(lo, kvh, off, 0);
+      const int2 at = tiles[lo];
+      const int n = __ldg(p.cu_q + at.x + 1) - __ldg(p.cu_q + at.x);
+      cut = paged_cut(p, x, pos[lo], lo, unit_blocks(p, n, __ldg(p.kv_len + at.x), at.y));
     }
     s_cuts[c] = cut;
     p.plan.cuts[c] = cut;
   }
   __syncthreads();
-  // a unit that is cut: its first cut c belongs to a group of pieces that starts with CTA c - 1
   for (int c = tid; c < n_ctas; c += kPlanThreads) {
-    const int4 cut = s_cuts[c];
-    if (cut.z == 0) continue;
-    const int4 prev = s_cuts[c - 1];  // c > 0: the line starts with a whole unit
-    if (prev.x == cut.x && prev.y == cut.y && prev.z > 0) continue;
-    int pieces = 2;
-    while (c + pieces - 1 < n_ctas && s_cuts[c + pieces - 1].x == cut.x && s_cuts[c + pieces - 1].y == cut.y) ++pieces;
-    p.plan.groups[atomicAdd(&s_groups, 1)] = make_int4(cut.x, cut.y, c - 1, pieces);
+    if (s_cuts[c].z == 0) continue;
+    const int2 at = tiles[s_cuts[c].x];
+    const int q0 = __ldg(p.cu_q + at.x);
+    PagedGroup g;
+    if (paged_group(s_cuts, c, n_ctas, at, q0, __ldg(p.cu_q + at.x + 1) - q0, __ldg(p.kv_len + at.x), g))
+      p.plan.groups[atomicAdd(&s_groups, 1)] = g;
   }
   __syncthreads();
   if (tid == 0) {
@@ -151,28 +161,27 @@ template <bool BF16, int DV>
 __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(const PagedParams p) {
   constexpr int LANES = DV / 8;  // threads per row, 8 columns each
   pdl_wait();
-  if (static_cast<int>(blockIdx.x) >= ld_dep(&p.plan.head->n_groups)) return;
-  const int4 gr = ld_dep(p.plan.groups + blockIdx.x);
-  const int2 at = ld_dep(p.plan.tiles + gr.x);
-  const int q_off = __ldg(p.cu_q + at.x), n = __ldg(p.cu_q + at.x + 1) - q_off;
-  const int len = __ldg(p.kv_len + at.x), sk = min(max(len, 0), p.max_kv);
-  // piece i: CTA gr.z + i, from its cut on; the first one may be that CTA's last piece
-  const int4 c0 = ld_dep(p.plan.cuts + gr.z);
-  const int slot0 = 2 * gr.z + ((c0.x == gr.x && c0.y == gr.y && c0.z == 0) ? 0 : 1);
+  // read at once, whether the group exists or not
+  const int n_groups = ld_dep(&p.plan.head->n_groups);
+  const int4* record = reinterpret_cast<const int4*>(p.plan.groups + blockIdx.x);
+  const int4 g0 = ld_dep(record), g1 = ld_dep(record + 1);
+  if (static_cast<int>(blockIdx.x) >= n_groups) return;
+  const int tile_u = g0.x, kvh = g0.y, first = g0.z, pieces = g0.w, slot0 = g1.x, q_off = g1.y, n = g1.z, len = g1.w;
+  const int sk = min(max(len, 0), p.max_kv);
   const int prow = blockIdx.y * kMergeRows + threadIdx.x / LANES, col = 8 * (threadIdx.x % LANES);
   const int t = prow / kBlockQ, row = prow - t * kBlockQ;
   const int row_tok = static_cast<int>(fast_div(row, p.div_group));
-  const int tile = at.y * kTilesPerCta + t;
+  const int tile = tile_u * kTilesPerCta + t;
   const int tok = tile * p.tok_tile + row_tok;
   if (prow >= p.slot_rows || row_tok >= p.tok_tile || tok >= n) return;
-  const int head = gr.y * p.group + (row - row_tok * p.group);
+  const int head = kvh * p.group + (row - row_tok * p.group);
   const int blocks = paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, tile);
   float M = -INFINITY, L = 0.f;
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-  for (int i = 0; i < gr.w; ++i) {
-    if (i > 0 && ld_dep(&p.plan.cuts[gr.z + i].z) >= blocks) break;  // this tile ends before
-    const int64_t r = static_cast<int64_t>(i == 0 ? slot0 : 2 * (gr.z + i)) * p.slot_rows + prow;
+  for (int i = 0; i < pieces; ++i) {
+    if (i > 0 && ld_dep(&p.plan.cuts[first + i].z) >= blocks) break;  // this tile ends before
+    const int64_t r = static_cast<int64_t>(i == 0 ? slot0 : 2 * (first + i)) * p.slot_rows + prow;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + r * 2);
     const float4 a = *reinterpret_cast<const float4*>(p.part_o + r * DV + col);
     const float4 b = *reinterpret_cast<const float4*>(p.part_o + r * DV + col + 4);
@@ -270,6 +279,7 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.slot_rows = slot_rows(group, max_seqlen_q);
   p.cut = partials > 0 && workspace_bytes >= plan + partials;
   p.max_tiles = (int)tiles;
+  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= p.tok_tile && !(quant && D == 192);
   p.plan = paged_plan_at(workspace, tiles);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
   p.part_ml = p.part_o + 2ull * kPagedMaxCtas * p.slot_rows * Dv;
@@ -298,7 +308,7 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.stall_first_stage = take_stall_flag();
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == SDPA_BF16;
-  cudaError_t e = launch_paged_plan(p, s);
+  cudaError_t e = p.inline_plan ? cudaSuccess : launch_paged_plan(p, s);
   if (e == cudaSuccess)
     e = quant ? launch_paged_fp8(bf16, D, tq, tk, tv, p, s)
               : (bf16 ? launch_paged_bf16(D, tq, tk, tv, p, s) : launch_paged_f16(D, tq, tk, tv, p, s));

@@ -204,7 +204,7 @@ def test_chunk_workspace(lib):
     size = fa.sdpa_fwd_paged_workspace_size
 
     def plan(B, tiles):  # header, cuts and groups of 160 CTAs, tiles, sequences
-        return (16 + 321 * 16 + tiles * 16 + 8 + (B + 1) * 4 + 15) // 16 * 16
+        return (16 + 161 * 16 + 160 * 32 + tiles * 16 + 8 + (B + 1) * 4 + 15) // 16 * 16
 
     # fewer than six blocks of keys: nothing to cut
     assert size(3, 8, 2, 30, 12, 640, 128) == plan(3, 3)
