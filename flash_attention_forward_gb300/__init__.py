@@ -34,6 +34,7 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -61,6 +62,8 @@ class SdpaError(RuntimeError):
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -508,23 +511,61 @@ def sdpa_decode_noalloc(q, k_cache, v_cache, kv_len, *, scale: float | None = No
     return out, lse
 
 
-def _check_pages(q_rows, page_table):
-    if page_table.dim() != 2 or page_table.dtype != torch.int32 or (q_rows is not None and
-                                                                      page_table.shape[0] != q_rows):
+# The paged and quantised calls below are made for every layer of every step, where a call's time on
+# the host counts: contiguous tensors take the library's default strides, stride arrays are kept by
+# their values, and a tensor's name is looked for only when something is wrong with it.
+
+@functools.lru_cache(maxsize=4096)
+def _stride_array(strides):
+    return (ctypes.c_int64 * len(strides))(*strides)
+
+
+def _current_device(names, tensors):
+    """Index of the current device, which every tensor (None skipped) must be on; unit innermost strides are
+    checked by _strides or follow from contiguity."""
+    dev = tensors[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device() or any(t is not None and t.get_device() != dev for t in tensors):
+        _on_device(**dict(zip(names, tensors)))
+        raise ValueError("all tensors must be on the current device")
+    return dev
+
+
+def _strides(names, tensors, dims):
+    """None if all tensors are contiguous, else the array of the first dims[i] strides of each."""
+    if all(t.is_contiguous() for t in tensors):
+        return None
+    _on_device(**dict(zip(names, tensors)))
+    return _stride_array(tuple(s for t, n in zip(tensors, dims) for s in t.stride()[:n]))
+
+
+def _unit_vectors(names, tensors):
+    for name, t in zip(names, tensors):
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must have a unit innermost stride")
+
+
+def _raw_stream(stream, dev):
+    """Handle of the stream (the current one of the current device by default)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _check_page_table(B, page_table):
+    if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.shape[0] != B:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
 
 
 def _check_fp8_pools(k_pool, v_pool, k_scale, v_scale):
-    """e4m3 pools [n_pages, page_size, Hkv, D | Dv] and their scales [n_pages, Hkv, page_size]."""
+    """e4m3 pools [n_pages, page_size, Hkv, D | Dv] and their scales [n_pages, Hkv, page_size]; the sizes."""
     if k_pool.dim() != 4 or v_pool.dim() != 4 or k_pool.shape[:3] != v_pool.shape[:3]:
         raise ValueError("the pools must be [n_pages, page_size, Hkv, D | Dv]")
     if k_pool.dtype != torch.float8_e4m3fn or v_pool.dtype != torch.float8_e4m3fn:
         raise ValueError("the pools must hold float8_e4m3fn codes")
-    n_pages, page_size, Hkv, _ = k_pool.shape
+    n_pages, page_size, Hkv, D = k_pool.shape
+    want = (n_pages, Hkv, page_size)
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dtype != torch.float32 or tuple(t.shape) != (n_pages, Hkv, page_size) or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {(n_pages, Hkv, page_size)}")
-    _on_device(k_pool=k_pool, v_pool=v_pool, k_scale=k_scale, v_scale=v_scale)
+        if t.dtype != torch.float32 or t.shape != want or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous fp32 tensor of shape {want}")
+    return n_pages, page_size, Hkv, D, v_pool.shape[3]
 
 
 def sdpa_cache_write_fp8(k, v, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens, *, stream=None):
@@ -534,26 +575,27 @@ def sdpa_cache_write_fp8(k, v, k_pool, v_pool, k_scale, v_scale, page_table, kv_
     each sequence's rows after the call; its new tokens are the last of them.  Writes in place."""
     if k.dim() != 3 or v.dim() != 3 or k.shape[:2] != v.shape[:2]:
         raise ValueError("k and v must be packed [total, Hkv, D | Dv]")
-    if k.dtype not in (torch.float16, torch.bfloat16) or v.dtype != k.dtype:
+    dtype = k.dtype
+    if dtype not in (torch.float16, torch.bfloat16) or v.dtype != dtype:
         raise ValueError("sdpa_cache_write_fp8 takes fp16 or bf16 rows of one type")
-    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
-    total, Hkv, D = k.shape
-    n_pages, page_size, pool_heads, pool_d = k_pool.shape
-    Dv = v.shape[2]
-    if pool_heads != Hkv or pool_d != D or v_pool.shape[3] != Dv:
+    n_pages, page_size, Hkv, D, Dv = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    total = k.shape[0]
+    if k.shape[1] != Hkv or k.shape[2] != D or v.shape[2] != Dv:
         raise ValueError("the pools' heads and head dims must be those of k and v")
-    _on_device(k=k, v=v, page_table=page_table, kv_len=kv_len, cu_seqlens=cu_seqlens)
     _int32_vector("kv_len", kv_len)
     B = kv_len.shape[0]
     _int32_vector("cu_seqlens", cu_seqlens, B + 1)
-    _check_pages(B, page_table)
-    strides = _i64((*k.stride()[:2], *v.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3],
-                    page_table.stride(0)))
+    _check_page_table(B, page_table)
+    dev = _current_device(("k", "v", "k_pool", "v_pool", "k_scale", "v_scale", "page_table", "kv_len", "cu_seqlens"),
+                          (k, v, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens))
+    _unit_vectors(("kv_len", "cu_seqlens"), (kv_len, cu_seqlens))
+    strides = _strides(("k", "v", "k_pool", "v_pool", "page_table"), (k, v, k_pool, v_pool, page_table), (2, 2, 3, 3, 1))
     rc = _load().sdpa_cache_write_fp8(
         k.data_ptr(), v.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         page_table.data_ptr(), kv_len.data_ptr(), cu_seqlens.data_ptr(), B, Hkv, total, page_size,
-        page_table.shape[1], n_pages, D, Dv, strides, _DT[k.dtype], _stream_ptr(stream))
-    _check("sdpa_cache_write_fp8", rc)
+        page_table.shape[1], n_pages, D, Dv, strides, _DT[dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_cache_write_fp8", rc)
 
 
 def sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens, total: int, *,
@@ -561,72 +603,83 @@ def sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens
     """Read a quantised paged cache back: the first cu_seqlens[b+1] - cu_seqlens[b] rows of each sequence as
     packed rows, (k [total,Hkv,D], v [total,Hkv,Dv]) in ``dtype`` (fp16 or bf16) or the type of the outputs
     that are passed."""
-    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
-    n_pages, page_size, Hkv, D = k_pool.shape
-    Dv = v_pool.shape[3]
+    n_pages, page_size, Hkv, D, Dv = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
     if k_out is None:
         k_out = torch.empty((total, Hkv, D), dtype=dtype if v_out is None else v_out.dtype, device=k_pool.device)
+    elif k_out.shape != (total, Hkv, D):
+        raise ValueError(f"k_out must have shape {(total, Hkv, D)}")
     if v_out is None:
         v_out = torch.empty((total, Hkv, Dv), dtype=k_out.dtype, device=k_pool.device)
-    if tuple(k_out.shape) != (total, Hkv, D) or tuple(v_out.shape) != (total, Hkv, Dv) or k_out.dtype != v_out.dtype:
-        raise ValueError(f"outputs must be tensors of one type of shapes {(total, Hkv, D)} and {(total, Hkv, Dv)}")
+    elif v_out.shape != (total, Hkv, Dv) or v_out.dtype != k_out.dtype:
+        raise ValueError(f"v_out must have shape {(total, Hkv, Dv)} and k's type")
     if k_out.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("sdpa_cache_read_fp8 writes fp16 or bf16")
-    _on_device(k_out=k_out, v_out=v_out, page_table=page_table, cu_seqlens=cu_seqlens)
     _int32_vector("cu_seqlens", cu_seqlens)
     B = cu_seqlens.shape[0] - 1
-    _check_pages(B, page_table)
-    strides = _i64((*k_out.stride()[:2], *v_out.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3],
-                    page_table.stride(0)))
+    _check_page_table(B, page_table)
+    dev = _current_device(("k_pool", "v_pool", "k_scale", "v_scale", "page_table", "cu_seqlens", "k_out", "v_out"),
+                          (k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens, k_out, v_out))
+    _unit_vectors(("cu_seqlens",), (cu_seqlens,))
+    strides = _strides(("k_out", "v_out", "k_pool", "v_pool", "page_table"), (k_out, v_out, k_pool, v_pool, page_table),
+                       (2, 2, 3, 3, 1))
     rc = _load().sdpa_cache_read_fp8(
         k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), page_table.data_ptr(),
         cu_seqlens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), B, Hkv, total, page_size, page_table.shape[1],
-        n_pages, D, Dv, strides, _DT[k_out.dtype], _stream_ptr(stream))
-    _check("sdpa_cache_read_fp8", rc)
+        n_pages, D, Dv, strides, _DT[k_out.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_cache_read_fp8", rc)
     return k_out, v_out
 
 
 def sdpa_decode_paged_fp8_workspace_size(B: int, Hq: int, Hkv: int, max_kv: int, Dv: int) -> int:
     """Bytes of workspace for sdpa_decode_paged_fp8 (max_kv = max_pages * page_size)."""
-    return int(_load().sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_kv, Dv))
+    return _load().sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_kv, Dv)
+
+
+def _paged_outputs(q, Dv, lse_shape, out, lse, return_lse):
+    shape = (q.shape[0], q.shape[1], Dv)
+    if out is None:
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif out.shape != shape or out.dtype != q.dtype:
+        raise ValueError(f"out must be a {q.dtype} tensor of shape {shape}")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+    elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {lse_shape}")
+    return out, lse
 
 
 def sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, *, scale: float | None = None,
                           out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
     """sdpa_decode_paged over a quantised cache: q [B,Hq,D] fp16/bf16, e4m3 pools [n_pages,page_size,Hkv,D|Dv],
     scales [n_pages,Hkv,page_size] fp32.  Returns (o [B,Hq,Dv] in q's type, lse [B,Hq] fp32 or None)."""
-    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    n_pages, page_size, Hkv, D, Dv = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
     if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("q must be an fp16 or bf16 [B, Hq, D] tensor")
-    B, Hq, D = q.shape
-    n_pages, page_size, Hkv, pool_d = k_pool.shape
-    Dv = v_pool.shape[3]
-    if pool_d != D:
+    B, Hq = q.shape[:2]
+    if q.shape[2] != D:
         raise ValueError("q and the K pool must share one head dim")
-    _check_pages(B, page_table)
+    _check_page_table(B, page_table)
+    _int32_vector("kv_len", kv_len, B)
     max_pages = page_table.shape[1]
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    if out is None:
-        out = torch.empty((B, Hq, Dv), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (B, Hq, Dv) or out.dtype != q.dtype:
-        raise ValueError(f"out must be a {q.dtype} tensor of shape {(B, Hq, Dv)}")
-    if lse is None:
-        lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-    elif tuple(lse.shape) != (B, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(B, Hq)}")
+    out, lse = _paged_outputs(q, Dv, (B, Hq), out, lse, return_lse)
+    lib = _load()
     if workspace is None:
-        workspace = torch.empty(sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_pages * page_size, Dv),
+        workspace = torch.empty(lib.sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_pages * page_size, Dv),
                                 dtype=torch.uint8, device=q.device)
-    _on_device(q=q, page_table=page_table, kv_len=kv_len, out=out, lse=lse, workspace=workspace)
-    _int32_vector("kv_len", kv_len, B)
-    strides = _i64((*q.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3], *out.stride()[:2],
-                    page_table.stride(0)))
-    rc = _load().sdpa_decode_paged_fp8(
+    dev = _current_device(("q", "k_pool", "v_pool", "k_scale", "v_scale", "page_table", "kv_len", "out", "lse", "workspace"),
+                          (q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, out, lse, workspace))
+    _unit_vectors(("kv_len", "workspace"), (kv_len, workspace))
+    strides = _strides(("q", "k_pool", "v_pool", "out", "page_table"), (q, k_pool, v_pool, out, page_table), (2, 3, 3, 2, 1))
+    rc = lib.sdpa_decode_paged_fp8(
         q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        page_table.data_ptr(), kv_len.data_ptr(), out.data_ptr(), _ptr(lse), B, Hq, Hkv, page_size, max_pages,
-        n_pages, D, Dv, strides, scale, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        _DT[q.dtype], _stream_ptr(stream))
-    _check("sdpa_decode_paged_fp8", rc)
+        page_table.data_ptr(), kv_len.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv,
+        page_size, max_pages, n_pages, D, Dv, strides, scale, workspace.data_ptr(), workspace.nbytes, _DT[q.dtype],
+        _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_decode_paged_fp8", rc)
     return out, lse
 
 
@@ -634,42 +687,43 @@ def sdpa_fwd_paged_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_s
                                   Dv: int) -> int:
     """Bytes of workspace for sdpa_fwd_paged and sdpa_fwd_paged_fp8: the work plan (required), then
     partial results of cut key ranges (optional)."""
-    return int(_load().sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_kv, Dv))
+    return _load().sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_kv, Dv)
 
 
-def _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q, scale, out, lse, return_lse,
-                    workspace):
+def _fwd_paged(name, q, pools, sizes, page_table, kv_len, cu_seqlens_q, max_seqlen_q, scale, causal, out, lse,
+               return_lse, workspace, stream):
+    """The two chunk calls: pools is (k_pool, v_pool[, k_scale, v_scale])."""
+    n_pages, page_size, Hkv, D, Dv = sizes
     if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("q must be a packed fp16 or bf16 [total_q, Hq, D] tensor")
-    total_q, Hq, D = q.shape
-    n_pages, page_size, Hkv, pool_d = k_pool.shape
-    Dv = v_pool.shape[3]
-    if pool_d != D:
+    total_q, Hq = q.shape[:2]
+    if q.shape[2] != D:
         raise ValueError("q and the K pool must share one head dim")
     _int32_vector("kv_len", kv_len)
     B = kv_len.shape[0]
     _int32_vector("cu_seqlens_q", cu_seqlens_q, B + 1)
-    _check_pages(B, page_table)
-    max_pages = page_table.shape[1]
+    _check_page_table(B, page_table)
+    max_pages, max_seqlen_q = page_table.shape[1], int(max_seqlen_q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    if out is None:
-        out = torch.empty((total_q, Hq, Dv), dtype=q.dtype, device=q.device)
-    elif tuple(out.shape) != (total_q, Hq, Dv) or out.dtype != q.dtype:
-        raise ValueError(f"out must be a {q.dtype} tensor of shape {(total_q, Hq, Dv)}")
-    if lse is None:
-        lse = torch.empty((Hq, total_q), dtype=torch.float32, device=q.device) if return_lse else None
-    elif tuple(lse.shape) != (Hq, total_q) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 tensor of shape {(Hq, total_q)}")
-    max_seqlen_q = int(max_seqlen_q)
+    out, lse = _paged_outputs(q, Dv, (Hq, total_q), out, lse, return_lse)
+    lib = _load()
     if workspace is None:
-        need = sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_pages * page_size, Dv)
+        need = lib.sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_pages * page_size, Dv)
         workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
-    _on_device(q=q, page_table=page_table, kv_len=kv_len, cu_seqlens_q=cu_seqlens_q, out=out, lse=lse,
-               workspace=workspace)
-    strides = _i64((*q.stride()[:2], *k_pool.stride()[:3], *v_pool.stride()[:3], *out.stride()[:2],
-                    page_table.stride(0)))
-    sizes = (B, Hq, Hkv, total_q, max_seqlen_q, page_size, max_pages, n_pages, D, Dv, strides, scale)
-    return out, lse, workspace, sizes
+    dev = _current_device(("q", "k_pool", "v_pool", "page_table", "kv_len", "cu_seqlens_q", "out", "lse", "workspace",
+                           "k_scale", "v_scale"),
+                          (q, pools[0], pools[1], page_table, kv_len, cu_seqlens_q, out, lse, workspace, *pools[2:]))
+    _unit_vectors(("kv_len", "cu_seqlens_q", "workspace"), (kv_len, cu_seqlens_q, workspace))
+    strides = _strides(("q", "k_pool", "v_pool", "out", "page_table"), (q, pools[0], pools[1], out, page_table),
+                       (2, 3, 3, 2, 1))
+    rc = getattr(lib, name)(
+        q.data_ptr(), *(t.data_ptr() for t in pools), page_table.data_ptr(), kv_len.data_ptr(),
+        cu_seqlens_q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, total_q,
+        max_seqlen_q, page_size, max_pages, n_pages, D, Dv, strides, scale, int(bool(causal)), workspace.data_ptr(),
+        workspace.nbytes, _DT[q.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError(name, rc)
+    return out, lse
 
 
 def sdpa_fwd_paged(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q: int, *,
@@ -684,15 +738,9 @@ def sdpa_fwd_paged(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seql
         raise ValueError("the pools must be [n_pages, page_size, Hkv, D | Dv]")
     if k_pool.dtype != q.dtype or v_pool.dtype != q.dtype:
         raise ValueError("q and the pools must share one dtype (use sdpa_fwd_paged_fp8 for e4m3 pools)")
-    out, lse, workspace, sizes = _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q,
-                                                 scale, out, lse, return_lse, workspace)
-    _on_device(k_pool=k_pool, v_pool=v_pool)
-    rc = _load().sdpa_fwd_paged(
-        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(),
-        cu_seqlens_q.data_ptr(), out.data_ptr(), _ptr(lse), *sizes, int(bool(causal)), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _DT[q.dtype], _stream_ptr(stream))
-    _check("sdpa_fwd_paged", rc)
-    return out, lse
+    return _fwd_paged("sdpa_fwd_paged", q, (k_pool, v_pool),
+                      (*k_pool.shape, v_pool.shape[3]), page_table, kv_len, cu_seqlens_q, max_seqlen_q, scale, causal,
+                      out, lse, return_lse, workspace, stream)
 
 
 def sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens_q, max_seqlen_q: int, *,
@@ -700,13 +748,6 @@ def sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, 
                        workspace=None, stream=None):
     """sdpa_fwd_paged over a quantised cache: e4m3 pools and scales [n_pages,Hkv,page_size] fp32; q and o in
     fp16 or bf16."""
-    _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
-    out, lse, workspace, sizes = _fwd_paged_args(q, k_pool, v_pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q,
-                                                 scale, out, lse, return_lse, workspace)
-    rc = _load().sdpa_fwd_paged_fp8(
-        q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-        page_table.data_ptr(), kv_len.data_ptr(), cu_seqlens_q.data_ptr(), out.data_ptr(), _ptr(lse), *sizes,
-        int(bool(causal)), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _DT[q.dtype],
-        _stream_ptr(stream))
-    _check("sdpa_fwd_paged_fp8", rc)
-    return out, lse
+    sizes = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
+    return _fwd_paged("sdpa_fwd_paged_fp8", q, (k_pool, v_pool, k_scale, v_scale), sizes, page_table, kv_len,
+                      cu_seqlens_q, max_seqlen_q, scale, causal, out, lse, return_lse, workspace, stream)
