@@ -13,7 +13,11 @@
 //     over y, P_j = 2^(y_j - m) feeds the P.V product against the bare codes and
 //     l = sum 2^(s_j - m) is the matching denominator.  P then stays in fp16's best range whatever
 //     the scales are, where a product P * v_scale could leave it.
-// Bound by memory: D + Dv + 8 bytes per row against 2 (D + Dv) flops per query head.
+// Bound by memory: D + Dv + 8 bytes per row against 2 (D + Dv) flops per query head.  64 sequences of
+// 1024-16384 rows, 32 / 8 heads of 128, pages of 64: 196 us with the combine, 6.0 TB/s of codes and
+// scales; the same loads without the arithmetic take 194.  The products with keys and value dims in
+// the 16 rows of an MMA (below) brought it from 225: with heads there, half of each MMA, of the
+// accumulators and of the softmax's shuffles were for empty rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>
@@ -62,6 +66,13 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values held as an MMA fragment (thread (g, t): row g, columns 2t, 2t + 1).
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
 __device__ __forceinline__ uint32_t byte_perm(uint32_t a, uint32_t b, uint32_t sel) {
   uint32_t d;
   asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
@@ -76,7 +87,7 @@ __device__ __forceinline__ uint4 lds16(const uint8_t* base, int row, int unit) {
   return *reinterpret_cast<const uint4*>(base + row * 128 + ((unit ^ (row & 7)) << 4));
 }
 
-// WIDE: groups of 9-16 query heads per KV head (rows 8-15 of the tiles carry heads 8-15).
+// WIDE: groups of 9-16 query heads per KV head (a second tile of 8 columns).
 template <bool BF16, int D, bool WIDE>
 __global__ void __launch_bounds__(kF8Threads, 2)
     decode_f8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -86,6 +97,7 @@ __global__ void __launch_bounds__(kF8Threads, 2)
   constexpr int ST = C::STAGES;
   constexpr int RH = WIDE ? 2 : 1;
   constexpr int R = 8 * RH;
+  constexpr int CH = WIDE ? 1 : 2;  // chains of MMAs per score: two in all hide half of their latency
   extern __shared__ uint8_t f8_smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(f8_smem_raw) + 1023) & ~uintptr_t(1023));
   float* scales = reinterpret_cast<float*>(smem + ST * C::CODES);  // [ST][K, V][128]
@@ -158,17 +170,19 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       for (int j = max(0, c - ST); j < c; ++j) mbar_drain(&full[j % ST], (j / ST) & 1);
   } else {
     // ---------------------------------------------------------- consumers
-    // Fragments: g = lane / 4 is the head (A/C rows), the key (K as B operand) or the V unit (V as
-    // B operand), t = lane % 4.  Head dim: thread t owns dims [64 i + 16 t, +16), i < D / 64; one
-    // 32-bit word of four codes is one k-step.  Keys and value units in kOrder; C column 2t (+1) of
-    // P.V tile nt is value dim 16 kOrder[2t] (16 kOrder[2t + 1]) + nt.
+    // Both products are taken transposed, S^T = K Q^T and O^T = V^T P^T: the 16 rows of an MMA are
+    // keys and value dims, its 8 columns the heads of the group, so that no row of it is empty.
+    // g = lane / 4, t = lane % 4.  K (A operand): thread (g, t) holds dims [64 i + 16 t, +16), i < D / 64,
+    // of the keys g and g + 8 (in kOrder); one 32-bit word of four codes is one k-step.  V^T (A operand):
+    // keys 2t, 2t + 1 (+ 8) in kOrder, dims [16 kOrder[g], +16), two of them per tile.  Accumulators:
+    // acc[rh][i] holds dims 16 kOrder[g] + 2 i (+ 1) of the heads 2t, 2t + 1 (+ 8 rh).
     const int g = lane >> 2, t = lane & 3;
-    uint32_t qf[RH][C::UNITS][8];
-    float qs[RH];  // score scale of heads g and g + 8 (exp2 units)
+    uint32_t qf[RH][C::UNITS][8];  // head g + 8 rh (B operand)
+    float qs[RH][2];               // score scale of heads 2t, 2t + 1 (+ 8 rh), exp2 units
 #pragma unroll
     for (int rh = 0; rh < RH; ++rh) {
       const int head = g + 8 * rh;
-      qs[rh] = p.scale2;
+      qs[rh][0] = qs[rh][1] = p.scale2;
 #pragma unroll
       for (int i = 0; i < C::UNITS; ++i)
 #pragma unroll
@@ -194,7 +208,8 @@ __global__ void __launch_bounds__(kF8Threads, 2)
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         float mul, back;
         q_f16_scale(amax, mul, back);
-        qs[rh] *= back;
+        qs[rh][0] *= __shfl_sync(0xffffffffu, back, 8 * t);
+        qs[rh][1] *= __shfl_sync(0xffffffffu, back, 8 * t + 4);
 #pragma unroll
         for (int i = 0; i < C::UNITS; ++i)
 #pragma unroll
@@ -203,20 +218,20 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       }
     }
     const int order_g = kOrder[g];
-    int sig_v[4];  // chunk rows of this thread's four keys (score columns and V rows)
-    int sig_s[4];  // where their scales lie: 16-row pages take 32 floats each
+    const int krow = 16 * warp + order_g;                             // chunk rows krow, krow + 8: this thread's scores
+    const int srow = krow + (p.page_size == 16 ? 16 * warp : 0);      // ... and scales: 16-row pages take 32 floats each
+    int vrow[4];                                                      // chunk rows of its V codes
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      sig_v[u] = 16 * warp + 8 * (u >> 1) + kOrder[2 * t + (u & 1)];
-      sig_s[u] = sig_v[u] + (p.page_size == 16 ? 16 * warp : 0);
-    }
+    for (int u = 0; u < 4; ++u) vrow[u] = 16 * warp + 8 * (u >> 1) + kOrder[2 * t + (u & 1)];
 
-    float acc[16][4];
+    float acc[RH][8][4];
+    float m[RH][2], l[RH][2];  // m is the same in all lanes of one t; l is this thread's part of the sum
 #pragma unroll
-    for (int nt = 0; nt < 16; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
-    float m[RH], l[RH];
+    for (int rh = 0; rh < RH; ++rh) {
 #pragma unroll
-    for (int rh = 0; rh < RH; ++rh) m[rh] = -INFINITY, l[rh] = 0.f;
+      for (int i = 0; i < 8; ++i) acc[rh][i][0] = acc[rh][i][1] = acc[rh][i][2] = acc[rh][i][3] = 0.f;
+      m[rh][0] = m[rh][1] = -INFINITY, l[rh][0] = l[rh][1] = 0.f;
+    }
     bool ok = true;
 
     for (int c = 0; c < nchunks; ++c) {
@@ -228,120 +243,131 @@ __global__ void __launch_bounds__(kF8Threads, 2)
       const uint8_t* kS = smem + s * C::CODES;
       const uint8_t* vS = kS + C::KBOX * kF8Box;
       const float* sc_s = scales + s * 256;
-      const int row0 = start + c * kF8Chunk;
+      const int left = end - (start + c * kF8Chunk);  // rows of the chunk before kv_len
       uint4 kr[2][C::UNITS], vr[4];
-      float ks[4], vs[4];
+      float ks[2], lvs[2];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int h = 0; h < 2; ++h) {
+        ks[h] = sc_s[srow + 8 * h];
+        lvs[h] = sc_s[128 + srow + 8 * h];
 #pragma unroll
-        for (int i = 0; i < C::UNITS; ++i)
-          kr[nt][i] = lds16(kS + (i >> 1) * kF8Box, 16 * warp + 8 * nt + order_g, (i & 1) * 4 + t);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const bool valid = row0 + sig_v[u] < end;  // rows past kv_len may hold anything
-        const uint4 x = lds16(vS, sig_v[u], order_g);
-        vr[u] = valid ? x : make_uint4(0u, 0u, 0u, 0u);
-        ks[u] = sc_s[sig_s[u]];
-        vs[u] = sc_s[128 + sig_s[u]];
+        for (int i = 0; i < C::UNITS; ++i) kr[h][i] = lds16(kS + (i >> 1) * kF8Box, krow + 8 * h, (i & 1) * 4 + t);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);  // everything is in registers: the stage may refill
-
-      float sc[2][4];
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < C::UNITS; ++i)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16x4(word_of(kr[nt][i], w), b0, b1);
-            mma_f16_16816(sc[nt], qf[0][i][2 * w], WIDE ? qf[RH - 1][i][2 * w] : 0u, qf[0][i][2 * w + 1],
-                          WIDE ? qf[RH - 1][i][2 * w + 1] : 0u, b0, b1);
-          }
-      }
-      float lvs[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) lvs[u] = fmaxf(lg2(vs[u]), kMinLog2Scale);
-      float x[RH][4], y[RH][4], m_cand[RH];
-      bool need = false;
-#pragma unroll
-      for (int rh = 0; rh < RH; ++rh) {
+      auto load_v = [&]() {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          x[rh][u] = sc[u >> 1][2 * rh + (u & 1)] * qs[rh] * ks[u];
-          y[rh][u] = x[rh][u] + lvs[u];
-          if (row0 + sig_v[u] >= end) x[rh][u] = y[rh][u] = -INFINITY;
+          const uint4 x = lds16(vS, vrow[u], order_g);
+          vr[u] = vrow[u] < left ? x : make_uint4(0u, 0u, 0u, 0u);  // rows past kv_len may hold anything
         }
-        float mb = fmaxf(fmaxf(y[rh][0], y[rh][1]), fmaxf(y[rh][2], y[rh][3]));
-        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-        m_cand[rh] = fmaxf(m[rh], mb);
-        need |= m_cand[rh] > m[rh] + kRescaleLog2F8;
-      }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);  // everything is in registers: the stage may refill
+      };
+      if constexpr (!WIDE) load_v();  // two tiles of heads leave no registers for V's codes yet
+
+      float sc[RH][CH][4];
+#pragma unroll
+      for (int rh = 0; rh < RH; ++rh)
+#pragma unroll
+        for (int e = 0; e < CH; ++e) sc[rh][e][0] = sc[rh][e][1] = sc[rh][e][2] = sc[rh][e][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < C::UNITS; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(word_of(kr[0][i], w), a0, a2);
+          e4m3x4_to_f16x4(word_of(kr[1][i], w), a1, a3);
+#pragma unroll
+          for (int rh = 0; rh < RH; ++rh)
+            mma_f16_16816(sc[rh][w % CH], a0, a1, a2, a3, qf[rh][i][2 * w], qf[rh][i][2 * w + 1]);
+        }
+      if constexpr (WIDE) load_v();
+#pragma unroll
+      for (int h = 0; h < 2; ++h) lvs[h] = fmaxf(lg2(lvs[h]), kMinLog2Scale);
+      float x[RH][4], y[RH][4];  // [2 h + e]: key h, head e
+      bool need = false;
+#pragma unroll
+      for (int rh = 0; rh < RH; ++rh)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          x[rh][u] = (CH == 1 ? sc[rh][0][u] : sc[rh][0][u] + sc[rh][CH - 1][u]) * qs[rh][u & 1] * ks[u >> 1];
+          y[rh][u] = x[rh][u] + lvs[u >> 1];
+          if (krow + 8 * (u >> 1) >= left) x[rh][u] = y[rh][u] = -INFINITY;
+          need |= y[rh][u] > m[rh][u & 1] + kRescaleLog2F8;
+        }
       if (__any_sync(0xffffffffu, need)) {
 #pragma unroll
-        for (int rh = 0; rh < RH; ++rh) {
-          const float alpha = (m_cand[rh] == -INFINITY) ? 1.f : ex2(m[rh] - m_cand[rh]);
-          l[rh] *= alpha;
+        for (int rh = 0; rh < RH; ++rh)
 #pragma unroll
-          for (int nt = 0; nt < 16; ++nt) acc[nt][2 * rh] *= alpha, acc[nt][2 * rh + 1] *= alpha;
-          m[rh] = m_cand[rh];
-        }
+          for (int e = 0; e < 2; ++e) {
+            float mb = fmaxf(y[rh][e], y[rh][2 + e]);
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, d));
+            mb = fmaxf(mb, m[rh][e]);
+            const float alpha = (mb == -INFINITY) ? 1.f : ex2(m[rh][e] - mb);
+            l[rh][e] *= alpha;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[rh][i][e] *= alpha, acc[rh][i][2 + e] *= alpha;
+            m[rh][e] = mb;
+          }
       }
-      uint32_t a[RH][2];
+      uint32_t pt[RH][2];  // P^T (B operand): keys 2t, 2t + 1 (+ 8) of head g
 #pragma unroll
       for (int rh = 0; rh < RH; ++rh) {
-        const float neg_m = (m[rh] == -INFINITY) ? 0.f : -m[rh];
-        a[rh][0] = pack_f16x2(ex2(y[rh][0] + neg_m), ex2(y[rh][1] + neg_m));
-        a[rh][1] = pack_f16x2(ex2(y[rh][2] + neg_m), ex2(y[rh][3] + neg_m));
-        l[rh] += (ex2(x[rh][0] + neg_m) + ex2(x[rh][1] + neg_m)) + (ex2(x[rh][2] + neg_m) + ex2(x[rh][3] + neg_m));
+        float neg_m[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          neg_m[e] = (m[rh][e] == -INFINITY) ? 0.f : -m[rh][e];
+          l[rh][e] += ex2(x[rh][e] + neg_m[e]) + ex2(x[rh][2 + e] + neg_m[e]);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          pt[rh][h] = movmatrix_trans(pack_f16x2(ex2(y[rh][2 * h] + neg_m[0]), ex2(y[rh][2 * h + 1] + neg_m[1])));
       }
-      // O += P V: bytes of two keys interleaved, so that one conversion gives a B register
+      // O^T += V^T P^T: bytes of two keys interleaved, so that one conversion gives an A register
 #pragma unroll
       for (int w = 0; w < 4; ++w)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const uint32_t sel = h ? 0x7362u : 0x5140u;
-          uint32_t b0[2], b1[2];
-          e4m3x4_to_f16x4(byte_perm(word_of(vr[0], w), word_of(vr[1], w), sel), b0[0], b0[1]);
-          e4m3x4_to_f16x4(byte_perm(word_of(vr[2], w), word_of(vr[3], w), sel), b1[0], b1[1]);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x4(byte_perm(word_of(vr[0], w), word_of(vr[1], w), sel), a0, a1);
+          e4m3x4_to_f16x4(byte_perm(word_of(vr[2], w), word_of(vr[3], w), sel), a2, a3);
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            mma_f16_16816(acc[4 * w + 2 * h + j], a[0][0], WIDE ? a[RH - 1][0] : 0u, a[0][1], WIDE ? a[RH - 1][1] : 0u,
-                          b0[j], b1[j]);
+          for (int rh = 0; rh < RH; ++rh) mma_f16_16816(acc[rh][2 * w + h], a0, a1, a2, a3, pt[rh][0], pt[rh][1]);
         }
     }
 
 #pragma unroll
-    for (int rh = 0; rh < RH; ++rh) {
-      l[rh] += __shfl_xor_sync(0xffffffffu, l[rh], 1);
-      l[rh] += __shfl_xor_sync(0xffffffffu, l[rh], 2);
-      if (!ok) {
-        m[rh] = -INFINITY;
-        l[rh] = 0.f;
+    for (int rh = 0; rh < RH; ++rh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d *= 2) l[rh][e] += __shfl_xor_sync(0xffffffffu, l[rh][e], d);
+        if (!ok) {
+          m[rh][e] = -INFINITY;
+          l[rh][e] = 0.f;
+        }
       }
-    }
     // merge the four warps: per-warp O goes to the (now idle) ring memory
     __syncwarp();
     asm volatile("bar.sync 1, %0;" ::"n"(kDecodeWarps * 32));
     float* sm_o = reinterpret_cast<float*>(smem);  // [warp][head][dv]
 #pragma unroll
-    for (int rh = 0; rh < RH; ++rh) {
-      const int head = g + 8 * rh;
-      if (head < G) {
+    for (int rh = 0; rh < RH; ++rh)
 #pragma unroll
-        for (int nt = 0; nt < 16; ++nt) {
-          sm_o[(warp * R + head) * kDecodeDv + 16 * kOrder[2 * t] + nt] = acc[nt][2 * rh];
-          sm_o[(warp * R + head) * kDecodeDv + 16 * kOrder[2 * t + 1] + nt] = acc[nt][2 * rh + 1];
-        }
-        if (t == 0) {
-          sm_m[warp][head] = m[rh];
-          sm_l[warp][head] = l[rh];
+      for (int e = 0; e < 2; ++e) {
+        const int head = 2 * t + e + 8 * rh;
+        if (head < G) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float2*>(sm_o + (warp * R + head) * kDecodeDv + 16 * order_g + 2 * i) =
+                make_float2(acc[rh][i][e], acc[rh][i][2 + e]);
+          if (g == 0) {
+            sm_m[warp][head] = m[rh][e];
+            sm_l[warp][head] = l[rh][e];
+          }
         }
       }
-    }
     asm volatile("bar.sync 1, %0;" ::"n"(kDecodeWarps * 32));
     const int dv = threadIdx.x;  // kDecodeWarps * 32 == kDecodeDv
     for (int r = 0; r < G; ++r) {
@@ -388,7 +414,8 @@ cudaError_t launch_f8(int D, const DecodeParams& p, const CUtensorMap (&tm)[4], 
 }
 
 // Keys per split: the largest of 2048 .. 256 that gives every SM of the card two CTAs (304), or
-// 256.  Longer splits write fewer partials; a few short sequences need more CTAs than that gives.
+// 256.  Longer splits write fewer partials and start fewer CTAs (the batch above: 205 us with 4096,
+// 201 with 2048, 215 with 1024, 245 with 512); a few short sequences need more CTAs than that gives.
 int f8_log2_split(int B, int Hkv, int max_kv) {
   int log2 = 11;  // 2048
   while ((1 << log2) > kF8MinSplit &&

@@ -171,3 +171,18 @@ def test_two_streams_and_a_captured_graph():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(o, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_cuts_anywhere(seed):
+    # batches whose equal stretches cut units everywhere: next to their edges, several times, in the last unit
+    # of a sequence, behind sequences without rows
+    g = torch.Generator().manual_seed(100 + seed)
+    B = int(torch.randint(1, 60, (1,), generator=g))
+    lens = torch.randint(0, 2000 if seed % 2 else 300, (B,), generator=g)
+    lens[torch.rand(B, generator=g) < 0.3] = 0
+    lens[torch.rand(B, generator=g) < 0.1] = 4096
+    w = W.with_shape(B=B, Hq=8, Hkv=4 if seed < 3 else 2, Sk=4096)
+    x, pools, table = make(w, lens.tolist(), 64, seed=seed)
+    o, lse = run(x, pools, table, w.scale)
+    check(x, pools, table, w.scale, o, lse)
