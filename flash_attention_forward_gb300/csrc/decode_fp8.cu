@@ -414,8 +414,8 @@ cudaError_t launch_f8(int D, const DecodeParams& p, const CUtensorMap (&tm)[4], 
 }
 
 // Keys per split: the largest of 2048 .. 256 that gives every SM of the card two CTAs (304), or
-// 256.  Longer splits write fewer partials and start fewer CTAs (the batch above: 205 us with 4096,
-// 201 with 2048, 215 with 1024, 245 with 512); a few short sequences need more CTAs than that gives.
+// 256.  Longer splits write fewer partials and start fewer CTAs (the batch above: 4096 cost
+// 4 us more, 1024 14, 512 44); a few short sequences need more CTAs than that gives.
 int f8_log2_split(int B, int Hkv, int max_kv) {
   int log2 = 11;  // 2048
   while ((1 << log2) > kF8MinSplit &&
