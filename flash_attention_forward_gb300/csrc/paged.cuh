@@ -19,8 +19,11 @@
 // for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the rest of
 // the rings is loads in flight.
 //
-// Quantised pages.  Every e4m3 value is exact in fp16, so converter warps, four for K and four for V, turn a
-// block's codes into fp16 operands (one thread per row) and both products are fp16, whatever the query's type:
+// Quantised pages.  Every e4m3 value is exact in fp16, so converter warps turn a block's codes into fp16
+// operands (one thread per row) and both products are fp16, whatever the query's type.  Long chunks have four
+// such warps, which alternate between K and V and leave the softmax registers for a row's 128 scores; short ones,
+// where the conversion of a block stands between its arrival and its MMAs, four for K and four for V (one
+// warpgroup for all took the long ones from 1760 to 1590 us, four sequences' 2048 tokens of 16384 rows):
 //   * K' = code * (k_scale / 2^ek), 2^(ek + 6) the power of two of the block's largest scale: the
 //     largest row lies just below fp16's largest value, rows of power-of-two scales stay exact down
 //     to 2^-21 of the largest scale and lose a bit for each one below (K' is read as 0 under
@@ -86,15 +89,18 @@ struct PagedCfg {
   static constexpr int SMEM = OFF_ML + 1024;
   static_assert((KS > VS ? KS : VS) + 2 <= kExpRing, "the exponent ring holds what the converters write");
   static_assert(VS + RAWS + 2 <= PIECES, "the piece ring holds what the producer announces");
-  // warpgroups: control (producer, MMA, helpers), converters of K and of V (quantised), two softmax
-  static constexpr int THREADS = QUANT ? 640 : 384;
-  static constexpr int SOFTMAX_WARP = QUANT ? 12 : 4;
+  // warpgroups: control (producer, MMA, helpers), converters (quantised: of K and of V, or one of both), two softmax
+  static constexpr int CONVERTERS = !QUANT ? 0 : ONE ? 2 : 1;
+  static constexpr int SOFTMAX_WARP = 4 + 4 * CONVERTERS;
+  static constexpr int THREADS = SOFTMAX_WARP * 32 + 256;
+  // scores of its row that a softmax thread holds at a time
+  static constexpr int HELD = CONVERTERS == 2 ? 64 : kBlockK;
   // registers per thread; the sums must stay within what the block is launched with
-  static constexpr uint32_t REGS_CONTROL = QUANT ? 64 : 96;
+  static constexpr uint32_t REGS_CONTROL = CONVERTERS == 1 ? 56 : QUANT ? 64 : 96;
   static constexpr uint32_t REGS_CONVERT = 72;
-  static constexpr uint32_t REGS_SOFTMAX = QUANT ? 136 : 200;
-  static constexpr uint32_t REGS_LAUNCH = QUANT ? 96 : 168;
-  static_assert(128 * REGS_CONTROL + (QUANT ? 256 * REGS_CONVERT : 0) + 256 * REGS_SOFTMAX <= THREADS * REGS_LAUNCH,
+  static constexpr uint32_t REGS_SOFTMAX = CONVERTERS == 1 ? 192 : QUANT ? 136 : 200;
+  static constexpr uint32_t REGS_LAUNCH = CONVERTERS == 1 ? 128 : QUANT ? 96 : 168;
+  static_assert(128 * REGS_CONTROL + 128 * CONVERTERS * REGS_CONVERT + 256 * REGS_SOFTMAX <= THREADS * REGS_LAUNCH,
                 "register split exceeds the launch");
   static_assert(SMEM <= 227 * 1024, "more shared memory than a CTA may opt in to");
   static_assert(Q_BYTES % 1024 == 0 && K_BYTES % 1024 == 0 && V_BYTES % 1024 == 0 && KRAW % 1024 == 0 && VRAW % 1024 == 0,
@@ -164,8 +170,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // chunks of 64 columns, as the MMAs read them, times the pair factor f; f = 0 stores zeros whatever
 // the codes are.  One thread per row: both the reads and the writes of eight neighbouring rows
 // fall on all banks.  The loop over chunks is not unrolled: the kernel's loops together must fit the
-// instruction cache (unrolled for K and V, fetches stalled 2 of 10 resident warps and the softmax took twice
-// as long; 2048 tokens of 8192 rows 284 us against 217 us).
+// instruction cache (with both unrolled, 2048 tokens of 8192 rows took 284 us instead of 263).
 template <int W>
 __device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int chunks, int r, uint32_t f) {
   const int x = (r & 7) << 4;
@@ -212,7 +217,7 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 
 // The plan where every sequence has one query tile, by each CTA for itself: a scan over the sequences'
 // lengths on the line, then this CTA's two cuts; CTA 0 stores all of them and the cut units for the merge.
-// Spares the launch of a planning kernel and the wait for it (some 8 us of a call of 110).
+// Spares the launch of a planning kernel and the wait for it (112 -> 108 us for the drafts of 16 sequences).
 // scratch: 8 KB of shared memory that nobody uses yet.  All threads; returns the cuts in `mine`.
 template <int THREADS>
 __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine) {
@@ -306,6 +311,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   using C = PagedCfg<QUANT, D, DV, ONE>;
   constexpr int KS = C::KS, VS = C::VS, KR = C::KR, VR = C::VR;
   constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
+  constexpr int HELD = C::HELD;
   constexpr bool CONVERT_Q = QUANT && BF16;
   constexpr bool F16_MATH = QUANT || !BF16;
   // D = 128 fills the shared memory, without room to align the window by hand
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&kv_full[s], QUANT ? 4 : 1);
       mbar_init(&kv_empty[s], ONE ? 1 : 2);
     }
-    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], 8);
+    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], C::CONVERTERS == 1 ? 4 : 8);
     for (int s = 0; s < 2 * NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
@@ -691,120 +697,221 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         }
       }
     }
-  } else if (QUANT && warp < 12) {
+  } else if (QUANT && warp < C::SOFTMAX_WARP) {
     // ------------------------------------------------------------ converters: codes -> fp16 operands
     regs_dec<C::REGS_CONVERT>();
-    const int kv = (warp - 4) >> 2;   // 0: K, 1: V
     const int row = tid & 127;        // tile row of this thread
-    const float* scale = kv == 0 ? p.k_scale : p.v_scale;
-    int qn = 0;
-    int blk = 0;                      // blocks of the pieces before this one
-    int nc[2] = {0, 0};               // those of each reader
-    bool ok = true;
-    while (true) {
-      const PagedPiece& w = next_piece(ok);
-      ok = __all_sync(0xffffffffu, ok);
-      const int nb = ok ? w.n_blocks : 0;
-      if (nb == 0) break;
-      const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
-      const int32_t* table = p.page_table + w.b * p.pt_b;
-      // The scale of this thread's row in each block.  The exponents of a block are stored one block
-      // ahead of their use, the scales loaded one ahead of that, and the row's page another one, as
-      // the two loads depend on each other.
-      int page2 = -1;
-      float cur = 0.f, nxt = 0.f;
-      auto fetch_page = [&](int j) {
-        const int key = (jb0 + j) * kBlockK + row;
-        page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
-      };
-      auto fetch_scale = [&](int j) {
-        nxt = 0.f;  // rows past kv_len or without a page: factor 0
-        if (page2 >= 0 && page2 < p.n_pages)
-          nxt = ld_dep(scale + ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
-                       (((jb0 + j) * kBlockK + row) & (p.page_size - 1)));
-      };
-      auto store_exp = [&](int j) {  // scales are not negative: their bits order like they do
-        cur = nxt;
-        const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur)) >> 23);
-        const int be = (blk + j) % kExpRing;
-        if (lane == 0) {
-          reinterpret_cast<int*>(blk_exp + be * 4 + (row >> 5))[kv] = e;
-          mbar_arrive(&e_full[be]);
-        }
-      };
-      fetch_page(0);
-      fetch_scale(0);
-      fetch_page(1);
-      if constexpr (CONVERT_Q) {
-        const int t = kv;  // the converters of K take query tile 0, those of V tile 1
-        if (ONE ? t == 0 : w.n_s[t] > 0) {
-          if (!mbar_wait_warp(&q_full[t], qn & 1, abort_flag, p.status)) break;
-          uint8_t* q = sQ + t * C::Q_BYTES + row * 128;
-          float amax = 0.f;
+    // A bf16 query tile into fp16's range; two buffers of exponents, as the next piece's tile may be
+    // converted before this one's softmax has begun.
+    auto convert_q = [&](int t, int buf) {
+      uint8_t* q = sQ + t * C::Q_BYTES + row * 128;
+      float amax = 0.f;
 #pragma unroll 4
-          for (int u = 0; u < D / 8; ++u) {
-            const uint4 v = *reinterpret_cast<const uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int u = 0; u < D / 8; ++u) {
+        const uint4 v = *reinterpret_cast<const uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_f32(x[i])), fabsf(bf16hi_f32(x[i]))));
-          }
-          float mul, back;
-          q_f16_scale(amax, mul, back);
+        for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fmaxf(fabsf(bf16lo_f32(x[i])), fabsf(bf16hi_f32(x[i]))));
+      }
+      float mul, back;
+      q_f16_scale(amax, mul, back);
 #pragma unroll 4
-          for (int u = 0; u < D / 8; ++u) {
-            uint4* ptr = reinterpret_cast<uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
-            const uint4 v = *ptr;
-            *ptr = make_uint4(pack_f16x2(bf16lo_f32(v.x) * mul, bf16hi_f32(v.x) * mul),
-                              pack_f16x2(bf16lo_f32(v.y) * mul, bf16hi_f32(v.y) * mul),
-                              pack_f16x2(bf16lo_f32(v.z) * mul, bf16hi_f32(v.z) * mul),
-                              pack_f16x2(bf16lo_f32(v.w) * mul, bf16hi_f32(v.w) * mul));
+      for (int u = 0; u < D / 8; ++u) {
+        uint4* ptr = reinterpret_cast<uint4*>(q + (u >> 3) * kBlockQ * 128 + (((u & 7) ^ (row & 7)) << 4));
+        const uint4 v = *ptr;
+        *ptr = make_uint4(pack_f16x2(bf16lo_f32(v.x) * mul, bf16hi_f32(v.x) * mul),
+                          pack_f16x2(bf16lo_f32(v.y) * mul, bf16hi_f32(v.y) * mul),
+                          pack_f16x2(bf16lo_f32(v.z) * mul, bf16hi_f32(v.z) * mul),
+                          pack_f16x2(bf16lo_f32(v.w) * mul, bf16hi_f32(v.w) * mul));
+      }
+      // exponent of `back`, in [-126, 113]
+      q_exp[(t * 2 + buf) * 128 + row] = static_cast<int8_t>(static_cast<int>(__float_as_uint(back) >> 23) - 127);
+      fence_proxy_async_smem();
+      warp_arrive(&q_ready[t], lane);
+    };
+    if constexpr (C::CONVERTERS == 1) {
+      // One warpgroup: K(0), then K(j) and V(j-1), the order in which the issuers use them.
+      int qn[2] = {0, 0};
+      int blk = 0;
+      bool ok = true;
+      while (true) {
+        const PagedPiece& w = next_piece(ok);
+        ok = __all_sync(0xffffffffu, ok);
+        const int nb = ok ? w.n_blocks : 0;
+        if (nb == 0) break;
+        const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
+        const int32_t* table = p.page_table + w.b * p.pt_b;
+        // as for two warpgroups (below): exponents one block ahead of their use, scales two, pages three
+        int page2 = -1;
+        float cur_k = 0.f, cur_v = 0.f, nxt_k = 0.f, nxt_v = 0.f;
+        auto fetch_page = [&](int j) {
+          const int key = (jb0 + j) * kBlockK + row;
+          page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
+        };
+        auto fetch_scale = [&](int j) {
+          nxt_k = nxt_v = 0.f;  // rows past kv_len or without a page: factor 0
+          if (page2 >= 0 && page2 < p.n_pages) {
+            const int64_t at = ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
+                               (((jb0 + j) * kBlockK + row) & (p.page_size - 1));
+            nxt_k = ld_dep(p.k_scale + at);
+            nxt_v = ld_dep(p.v_scale + at);
           }
-          // exponent of `back`, in [-126, 113]; two buffers, as the next piece's tile may be converted
-          // before this one's softmax has begun
-          q_exp[(t * 2 + (qn & 1)) * 128 + row] =
-              static_cast<int8_t>(static_cast<int>(__float_as_uint(back) >> 23) - 127);
-          fence_proxy_async_smem();
-          warp_arrive(&q_ready[t], lane);
-          ++qn;
-        }
-      }
-      store_exp(0);
-      fetch_scale(1);
-      fetch_page(2);
+        };
+        auto store_exp = [&](int j) {
+          cur_k = nxt_k, cur_v = nxt_v;
+          const int ek = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur_k)) >> 23);
+          const int ev = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur_v)) >> 23);
+          const int be = (blk + j) % kExpRing;
+          if (lane == 0) {
+            blk_exp[be * 4 + (row >> 5)] = make_int2(ek, ev);
+            mbar_arrive(&e_full[be]);
+          }
+        };
+        fetch_page(0);
+        fetch_scale(0);
+        fetch_page(1);
+        if constexpr (CONVERT_Q) {
 #pragma unroll 1
-      for (int j = 0; j < nb; ++j) {
-        const int be = blk + j;
-        const int rs = be % NR;
-        const int rd = ONE ? j & 1 : 0;
-        const int ring = kv == 0 ? KR : VR, c = ONE ? (rd ? nc[1] : nc[0]) + (j >> 1) : be;
-        const int s = rd * ring + c % ring, base = kv == 0 ? 0 : KS;
-        ok = mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status);
-        if (!ok) break;
-        const int2 e = block_exp(blk_exp + be % kExpRing * 4);
-        // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
-        const float r = cur * __uint_as_float(static_cast<uint32_t>(127 - (kv == 0 ? e.x : e.y)) << 23);
-        const uint32_t f = pack_f16x2(r, r);
-        if (j + 1 < nb) {
-          store_exp(j + 1);
-          fetch_scale(j + 2);
-          fetch_page(j + 3);
+          for (int t = 0; t < 2; ++t) {
+            if (w.n_s[t] == 0) continue;
+            const int n = t ? qn[1]++ : qn[0]++;
+            if (!(ok = mbar_wait_warp(&q_full[t], n & 1, abort_flag, p.status))) break;
+            convert_q(t, n & 1);
+          }
+          if (!ok) break;
         }
-        ok = mbar_wait_warp(&raw_full[kv * NR + rs], (be / NR) & 1, abort_flag, p.status) &&
-             (c < ring || mbar_wait_warp(&kv_empty[base + s], (c / ring - 1) & 1, abort_flag, p.status));
+        store_exp(0);
+        fetch_scale(1);
+        fetch_page(2);
+        uint32_t f_v = 0u;  // factors of V(j-1)
+#pragma unroll 1
+        for (int j = 0; j <= nb; ++j) {
+          uint32_t f[2] = {0u, f_v};
+          if (j < nb) {
+            const int be = (blk + j) % kExpRing;
+            if (!(ok = mbar_wait_warp(&e_full[be], ((blk + j) / kExpRing) & 1, abort_flag, p.status))) break;
+            const int2 e = block_exp(blk_exp + be * 4);
+            // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+            const float rk = cur_k * __uint_as_float(static_cast<uint32_t>(127 - e.x) << 23);
+            const float rv = cur_v * __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
+            f[0] = pack_f16x2(rk, rk);
+            f_v = pack_f16x2(rv, rv);
+            if (j + 1 < nb) {
+              store_exp(j + 1);
+              fetch_scale(j + 2);
+              fetch_page(j + 3);
+            }
+          }
+#pragma unroll 1
+          for (int kv = 0; kv < 2; ++kv) {
+            if (kv == 0 ? j == nb : j == 0) continue;
+            const int c = blk + j - kv;
+            const int rs = c % NR, ring = kv == 0 ? KR : VR, s = c % ring, at = (kv == 0 ? 0 : KS) + s;
+            ok = mbar_wait_warp(&raw_full[kv * NR + rs], (c / NR) & 1, abort_flag, p.status) &&
+                 (c < ring || mbar_wait_warp(&kv_empty[at], (c / ring - 1) & 1, abort_flag, p.status));
+            if (!ok) break;
+            const uint8_t* raw = kv == 0 ? smem + C::OFF_KRAW + rs * C::KRAW : smem + C::OFF_VRAW + rs * C::VRAW;
+            uint8_t* dst = kv == 0 ? sK + s * C::K_BYTES : sV + s * C::V_BYTES;
+            if (C::KW == C::VW || kv == 1)
+              convert_row<C::VW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, kv == 0 ? f[0] : f[1]);
+            else
+              convert_row<C::KW>(raw, dst, C::NCH_D, row, f[0]);
+            fence_proxy_async_smem();
+            warp_arrive(&kv_full[at], lane);
+            if (lane == 0) mbar_arrive(&raw_empty[kv * NR + rs]);
+          }
+          if (!ok) break;
+        }
         if (!ok) break;
-        const uint8_t* raw = kv == 0 ? smem + C::OFF_KRAW + rs * C::KRAW : smem + C::OFF_VRAW + rs * C::VRAW;
-        uint8_t* dst = kv == 0 ? sK + s * C::K_BYTES : sV + s * C::V_BYTES;
-        if (C::KW == C::VW || kv == 1)
-          convert_row<C::VW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, f);
-        else
-          convert_row<C::KW>(raw, dst, C::NCH_D, row, f);
-        fence_proxy_async_smem();
-        warp_arrive(&kv_full[base + s], lane);
-        if (lane == 0) mbar_arrive(&raw_empty[kv * NR + rs]);
+        blk += nb;
       }
-      if (!ok) break;
-      blk += nb;
-      nc[0] += (nb + 1) / 2, nc[1] += nb / 2;
+    } else {
+      const int kv = (warp - 4) >> 2;   // 0: K, 1: V
+      const float* scale = kv == 0 ? p.k_scale : p.v_scale;
+      int qn = 0;
+      int blk = 0;                      // blocks of the pieces before this one
+      int nc[2] = {0, 0};               // those of each reader
+      bool ok = true;
+      while (true) {
+        const PagedPiece& w = next_piece(ok);
+        ok = __all_sync(0xffffffffu, ok);
+        const int nb = ok ? w.n_blocks : 0;
+        if (nb == 0) break;
+        const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
+        const int32_t* table = p.page_table + w.b * p.pt_b;
+        // The scale of this thread's row in each block.  The exponents of a block are stored one block
+        // ahead of their use, the scales loaded one ahead of that, and the row's page another one, as
+        // the two loads depend on each other.
+        int page2 = -1;
+        float cur = 0.f, nxt = 0.f;
+        auto fetch_page = [&](int j) {
+          const int key = (jb0 + j) * kBlockK + row;
+          page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
+        };
+        auto fetch_scale = [&](int j) {
+          nxt = 0.f;  // rows past kv_len or without a page: factor 0
+          if (page2 >= 0 && page2 < p.n_pages)
+            nxt = ld_dep(scale + ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
+                         (((jb0 + j) * kBlockK + row) & (p.page_size - 1)));
+        };
+        auto store_exp = [&](int j) {  // scales are not negative: their bits order like they do
+          cur = nxt;
+          const int e = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur)) >> 23);
+          const int be = (blk + j) % kExpRing;
+          if (lane == 0) {
+            reinterpret_cast<int*>(blk_exp + be * 4 + (row >> 5))[kv] = e;
+            mbar_arrive(&e_full[be]);
+          }
+        };
+        fetch_page(0);
+        fetch_scale(0);
+        fetch_page(1);
+        if constexpr (CONVERT_Q) {
+          const int t = kv;  // the converters of K take query tile 0, those of V tile 1
+          if (ONE ? t == 0 : w.n_s[t] > 0) {
+            if (!mbar_wait_warp(&q_full[t], qn & 1, abort_flag, p.status)) break;
+            convert_q(t, qn & 1);
+            ++qn;
+          }
+        }
+        store_exp(0);
+        fetch_scale(1);
+        fetch_page(2);
+#pragma unroll 1
+        for (int j = 0; j < nb; ++j) {
+          const int be = blk + j;
+          const int rs = be % NR;
+          const int rd = ONE ? j & 1 : 0;
+          const int ring = kv == 0 ? KR : VR, c = ONE ? (rd ? nc[1] : nc[0]) + (j >> 1) : be;
+          const int s = rd * ring + c % ring, base = kv == 0 ? 0 : KS;
+          ok = mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status);
+          if (!ok) break;
+          const int2 e = block_exp(blk_exp + be % kExpRing * 4);
+          // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
+          const float r = cur * __uint_as_float(static_cast<uint32_t>(127 - (kv == 0 ? e.x : e.y)) << 23);
+          const uint32_t f = pack_f16x2(r, r);
+          if (j + 1 < nb) {
+            store_exp(j + 1);
+            fetch_scale(j + 2);
+            fetch_page(j + 3);
+          }
+          ok = mbar_wait_warp(&raw_full[kv * NR + rs], (be / NR) & 1, abort_flag, p.status) &&
+               (c < ring || mbar_wait_warp(&kv_empty[base + s], (c / ring - 1) & 1, abort_flag, p.status));
+          if (!ok) break;
+          const uint8_t* raw = kv == 0 ? smem + C::OFF_KRAW + rs * C::KRAW : smem + C::OFF_VRAW + rs * C::VRAW;
+          uint8_t* dst = kv == 0 ? sK + s * C::K_BYTES : sV + s * C::V_BYTES;
+          if (C::KW == C::VW || kv == 1)
+            convert_row<C::VW>(raw, dst, kv == 0 ? C::NCH_D : C::NCH_V, row, f);
+          else
+            convert_row<C::KW>(raw, dst, C::NCH_D, row, f);
+          fence_proxy_async_smem();
+          warp_arrive(&kv_full[base + s], lane);
+          if (lane == 0) mbar_arrive(&raw_empty[kv * NR + rs]);
+        }
+        if (!ok) break;
+        blk += nb;
+        nc[0] += (nb + 1) / 2, nc[1] += nb / 2;
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax warpgroups
@@ -848,6 +955,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       const bool live = __any_sync(0xffffffffu, row_valid);
       const int jb0 = w.jb0, step = ONE ? 2 : 1, j0 = ONE ? t : 0;  // its blocks: j0 + i * step
       float row_scale2 = p.scale2;
+      // Exponents of a block.  Its predecessor in the ring is stored: for the first block of a piece because
+      // its scores are there, for the others because those of the block before were.
+      int2 exps = make_int2(0, 0);
+      auto get_exp = [&](int j) {
+        const int be = blk0 + j;
+        if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) return false;
+        exps = block_exp(blk_exp + be % kExpRing * 4);
+        return true;
+      };
       float m_used = -INFINITY;
       float l = 0.f;
       for (int i = 0; i < n; ++i, ++sn) {
@@ -865,23 +981,16 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         if (CONVERT_Q && i == 0)
           row_scale2 *= __uint_as_float(
               static_cast<uint32_t>(127 + static_cast<int>(q_exp[(qt * 2 + q_par) * 128 + row])) << 23);
-        float blk_scale2 = row_scale2, shift = 0.f, unshift = 1.f;
-        if constexpr (QUANT) {
-          const int be = blk0 + j;
-          if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const int2 e = block_exp(blk_exp + be % kExpRing * 4);
-          blk_scale2 = fmaxf(blk_scale2 * __uint_as_float(static_cast<uint32_t>(127 + e.x) << 23), kMinBlkScale2);
-          shift = static_cast<float>(e.y);
-          unshift = __uint_as_float(static_cast<uint32_t>(127 - e.y) << 23);
-        }
+        if (QUANT && i == 0 && !(ok = get_exp(j))) break;
+        const float blk_scale2 =
+            QUANT ? fmaxf(row_scale2 * __uint_as_float(static_cast<uint32_t>(127 + exps.x) << 23), kMinBlkScale2) : row_scale2;
+        const float shift = static_cast<float>(exps.y);
+        const float unshift = __uint_as_float(static_cast<uint32_t>(127 - exps.y) << 23);
         tc_fence_after();
         const int k0 = (jb0 + j) * kBlockK;
         const bool edge = k0 + kBlockK > lim_all;  // the diagonal and the ragged last block hide keys
         const int lim = lim_row - k0;
-        if (QUANT && edge) {  // in place, once for both readings
+        if (HELD < kBlockK && edge) {  // in place, once for both readings
 #pragma unroll 1
           for (int c = 0; c < kBlockK; c += 32) {
             uint32_t r[32];
@@ -895,10 +1004,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           }
           tmem_st_wait();
         }
-        // 16-bit pages: the row's 128 scores stay in registers.  Quantised pages: they are read twice,
-        // 64 columns at a time, in loops that are not unrolled (see convert_row on the instruction
-        // cache; measured 263 -> 245 us there, and 2412 -> 2582 us for 16-bit pages, which keep the short way).
-        constexpr int HELD = QUANT ? 64 : kBlockK;
+        // The row's 128 scores stay in registers where there are enough.  Beside two warpgroups of
+        // converters they are read twice, 64 columns at a time, in loops that are not unrolled.
         uint32_t r[HELD / 32][32];
         auto load = [&](int pass) {
 #pragma unroll
@@ -906,7 +1013,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int q = 0; q < HELD / 32; ++q) reg_fence(r[q]);
-          if (!QUANT && edge) {
+          if (HELD == kBlockK && edge) {
 #pragma unroll
             for (int c = 0; c < HELD; ++c)
               if (c >= lim) r[c >> 5][c & 31] = 0xFF800000u;
@@ -978,7 +1085,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           tc_fence_before();
           warp_arrive(bar, lane);
         };
-        if constexpr (QUANT) {
+        if constexpr (HELD < kBlockK) {
           if (rescale && i > 0) rescale_o();
 #pragma unroll 1
           for (int half = 0; half < 2; ++half) {
@@ -995,6 +1102,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         }
         const float sum = (ls[0] + ls[1]) + (ls[2] + ls[3]);
         l = QUANT ? fmaf(sum, unshift, l) : l + sum;
+        // the next block's, while its scores are on their way
+        if (QUANT && i + 1 < n && !(ok = get_exp(j + step))) break;
       }
       if (!ok) break;
 
