@@ -149,6 +149,32 @@ def test_many_sequences_on_each_sm(quant, B, new):
     check(*x, o, lse, 0.09, True)
 
 
+@pytest.mark.parametrize("quant", [False, True])
+def test_sequences_without_new_tokens_between_short_chunks(quant):
+    # one query tile a sequence: the plan passes over the empty ones, at both ends too
+    x = make([0, 0, 3, 0, 1, 16, 0, 2, 0], [9, 0, 900, 40, 1, 5000, 300, 70, 128], 8, 2, 128, 128, 64, "bf16", quant, seed=11)
+    o, lse = run(*x, 16, scale=0.09, causal=True)
+    check(*x, o, lse, 0.09, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+def test_more_sequences_than_the_plan_keeps_in_shared_memory(quant):
+    g = np.random.default_rng(12)
+    new, lens = g.integers(0, 4, 1100).tolist(), g.integers(1, 150, 1100).tolist()
+    x = make(new, lens, 4, 2, 64, 64, 16, "f16", quant, seed=12)
+    o, lse = run(*x, max(new), scale=0.125, causal=True)
+    check(*x, o, lse, 0.125, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("D", [64, 192])
+def test_the_widest_group_and_more_tiles_than_the_plan_keeps_in_shared_memory(quant, D):
+    # 128 heads of one KV head: a query tile is one token, 2300 tokens are 1150 units
+    x = make([2203, 97], [200, 64], 128, 1, D, 64 if D == 64 else 128, 32, "bf16", quant, seed=13)
+    o, lse = run(*x, 2203, scale=D ** -0.5, causal=False)
+    check(*x, o, lse, D ** -0.5, False)
+
+
 def test_rows_of_very_different_scales():
     # scales up to 2^12 apart inside a block, bf16 queries far outside fp16's range
     gain = lambda g, rows: torch.exp2(torch.randint(-12, 1, rows.shape[:-1], generator=g).float())[..., None]  # noqa: E731
