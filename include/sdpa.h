@@ -347,7 +347,7 @@ int sdpa_decode_paged(const void* q, const void* k_pool, const void* v_pool, con
  * A row whose slot lies outside the page table or the pool (a negative position, a page index not in
  * [0, n_pages)) is not written, and the call raises a status that sdpa_check_device_status()
  * reports as SDPA_ERR_INVALID.  No two rows of a call may share a slot (a page that several sequences
- * share is only read).  total * Hkv < 2^30; no workspace; one kernel.
+ * share is only read).  total >= 1, total * Hkv < 2^30; no workspace; one kernel.
  */
 int sdpa_cache_write_fp8(const void* k, const void* v, void* k_pool, void* v_pool, float* k_scale, float* v_scale,
                          const int32_t* page_table, const int32_t* kv_len, const int32_t* cu_seqlens, int B, int Hkv,
@@ -433,8 +433,9 @@ size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int ma
  *
  * Rows of a page at or past kv_len never contribute and may hold anything; the visible rows must be
  * finite.  (D, Dv) in {(64, 64), (128, 128), (192, 128)}; Hq / Hkv <= 128; page_size a power of
- * two >= 16; pointers 16-byte aligned.  Two kernels run in `stream` (the plan, the attention), three where
- * the workspace allows cuts.
+ * two >= 16; pointers 16-byte aligned; total_q >= 1.  The kernels in `stream`: the plan (which the attention makes
+ * itself for up to 256 sequences of max_seqlen_q <= 128 / (Hq / Hkv) tokens; not over quantised pages with D = 192),
+ * the attention, and the merge of divided tiles where the workspace allows any.
  */
 int sdpa_fwd_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
                    const int32_t* kv_len, const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int Hkv,
