@@ -297,8 +297,8 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
 //   kv_full / kv_empty    : a slot of the K or V ring holds its block / the issuers that read it are done
 //   raw_full / raw_empty  : quantised pages: codes of K (0) or V (1) landed / read by the converters
-//   e_full[i % 8]         : quantised pages: each converter warp has stored the exponents of its 32
-//                           rows of block i (the block's are the largest of the four)
+//   e_full[i % 8 (+ 8)]   : quantised pages: each converter warp of K (of V, where those are others) has stored
+//                           the exponents of its 32 rows of block i (the block's are the largest of the four)
 //   turn[t]               : issuer t may issue (both tiles active)
 //   v_ragged[i % 8]       : 16-bit pages: the i-th V block that ends past kv_len landed; a helper warp
 //                           then zeroes those rows and completes kv_full in the copy's place
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   uint64_t* kv_empty = kv_full + KS + VS;    // [KS + VS]
   uint64_t* raw_full = kv_empty + KS + VS;   // [2 NR]
   uint64_t* raw_empty = raw_full + 2 * NR;   // [2 NR]
-  uint64_t* e_full = raw_empty + 2 * NR;    // [kExpRing]
-  uint64_t* piece = e_full + kExpRing;  // [PIECES]
+  uint64_t* e_full = raw_empty + 2 * NR;    // [2 kExpRing]
+  uint64_t* piece = e_full + 2 * kExpRing;  // [PIECES]
   uint64_t* ml_full = piece + C::PIECES;  // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ml_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
   PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::OFF_PIECE);
   float2* ml_x = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [128]
-  static_assert((21 + kFixRing + kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
+  static_assert((21 + kFixRing + 2 * kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&kv_full[s], QUANT ? 4 : 1);
       mbar_init(&kv_empty[s], ONE ? 1 : 2);
     }
-    for (int s = 0; s < kExpRing; ++s) mbar_init(&e_full[s], C::CONVERTERS == 1 ? 4 : 8);
+    for (int s = 0; s < 2 * kExpRing; ++s) mbar_init(&e_full[s], 4);
     for (int s = 0; s < 2 * NR; ++s) {
       mbar_init(&raw_full[s], 1);
       mbar_init(&raw_empty[s], 4);
@@ -742,23 +742,25 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         const int sk = w.sk, jb0 = w.jb0, kvh = w.kvh;
         const int32_t* table = p.page_table + w.b * p.pt_b;
         // as for two warpgroups (below): exponents one block ahead of their use, scales two, pages three
-        int page2 = -1;
+        // (always loaded, from the first page where there is none: a load under a condition is waited for at once);
+        // rows past kv_len or without a page take the factor 0.
+        int page2 = 0;
+        bool has_page = false, has_scale = false;
         float cur_k = 0.f, cur_v = 0.f, nxt_k = 0.f, nxt_v = 0.f;
         auto fetch_page = [&](int j) {
           const int key = (jb0 + j) * kBlockK + row;
-          page2 = j < nb && key < sk ? ld_dep(table + (key >> p.log2_page)) : -1;
+          has_page = j < nb && key < sk;
+          page2 = ld_dep(table + (has_page ? key >> p.log2_page : 0));
         };
         auto fetch_scale = [&](int j) {
-          nxt_k = nxt_v = 0.f;  // rows past kv_len or without a page: factor 0
-          if (page2 >= 0 && page2 < p.n_pages) {
-            const int64_t at = ((static_cast<int64_t>(page2) * p.Hkv + kvh) << p.log2_page) +
-                               (((jb0 + j) * kBlockK + row) & (p.page_size - 1));
-            nxt_k = ld_dep(p.k_scale + at);
-            nxt_v = ld_dep(p.v_scale + at);
-          }
+          has_scale = has_page && page2 >= 0 && page2 < p.n_pages;
+          const int64_t at = ((static_cast<int64_t>(has_scale ? page2 : 0) * p.Hkv + kvh) << p.log2_page) +
+                             (((jb0 + j) * kBlockK + row) & (p.page_size - 1));
+          nxt_k = ld_dep(p.k_scale + at);
+          nxt_v = ld_dep(p.v_scale + at);
         };
         auto store_exp = [&](int j) {
-          cur_k = nxt_k, cur_v = nxt_v;
+          cur_k = has_scale ? nxt_k : 0.f, cur_v = has_scale ? nxt_v : 0.f;
           const int ek = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur_k)) >> 23);
           const int ev = static_cast<int>(__reduce_max_sync(0xffffffffu, __float_as_uint(cur_v)) >> 23);
           const int be = (blk + j) % kExpRing;
@@ -860,7 +862,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           const int be = (blk + j) % kExpRing;
           if (lane == 0) {
             reinterpret_cast<int*>(blk_exp + be * 4 + (row >> 5))[kv] = e;
-            mbar_arrive(&e_full[be]);
+            mbar_arrive(&e_full[kv * kExpRing + be]);
           }
         };
         fetch_page(0);
@@ -884,7 +886,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           const int rd = ONE ? j & 1 : 0;
           const int ring = kv == 0 ? KR : VR, c = ONE ? (rd ? nc[1] : nc[0]) + (j >> 1) : be;
           const int s = rd * ring + c % ring, base = kv == 0 ? 0 : KS;
-          ok = mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status);
+          ok = mbar_wait_warp(&e_full[kv * kExpRing + be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status);
           if (!ok) break;
           const int2 e = block_exp(blk_exp + be % kExpRing * 4);
           // scale / 2^e, below 2^7: exact in fp16 for power-of-two scales down to 2^-24
@@ -960,7 +962,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       int2 exps = make_int2(0, 0);
       auto get_exp = [&](int j) {
         const int be = blk0 + j;
-        if (!mbar_wait_warp(&e_full[be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) return false;
+        for (int kv = 0; kv < C::CONVERTERS; ++kv)
+          if (!mbar_wait_warp(&e_full[kv * kExpRing + be % kExpRing], (be / kExpRing) & 1, abort_flag, p.status)) return false;
         exps = block_exp(blk_exp + be % kExpRing * 4);
         return true;
       };
