@@ -549,6 +549,15 @@ def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """torch.empty from the memory of the stream that will write it: the allocator hands memory of the current
+    stream out again as soon as a tensor is dropped, as a workspace is when its call returns."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _check_page_table(B, page_table):
     if page_table.dim() != 2 or page_table.dtype != torch.int32 or page_table.shape[0] != B:
         raise ValueError("page_table must be an int32 [B, max_pages] tensor")
@@ -605,11 +614,11 @@ def sdpa_cache_read_fp8(k_pool, v_pool, k_scale, v_scale, page_table, cu_seqlens
     that are passed."""
     n_pages, page_size, Hkv, D, Dv = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
     if k_out is None:
-        k_out = torch.empty((total, Hkv, D), dtype=dtype if v_out is None else v_out.dtype, device=k_pool.device)
+        k_out = _empty((total, Hkv, D), dtype if v_out is None else v_out.dtype, k_pool.device, stream)
     elif k_out.shape != (total, Hkv, D):
         raise ValueError(f"k_out must have shape {(total, Hkv, D)}")
     if v_out is None:
-        v_out = torch.empty((total, Hkv, Dv), dtype=k_out.dtype, device=k_pool.device)
+        v_out = _empty((total, Hkv, Dv), k_out.dtype, k_pool.device, stream)
     elif v_out.shape != (total, Hkv, Dv) or v_out.dtype != k_out.dtype:
         raise ValueError(f"v_out must have shape {(total, Hkv, Dv)} and k's type")
     if k_out.dtype not in (torch.float16, torch.bfloat16):
@@ -636,15 +645,15 @@ def sdpa_decode_paged_fp8_workspace_size(B: int, Hq: int, Hkv: int, max_kv: int,
     return _load().sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_kv, Dv)
 
 
-def _paged_outputs(q, Dv, lse_shape, out, lse, return_lse):
+def _paged_outputs(q, Dv, lse_shape, out, lse, return_lse, stream):
     shape = (q.shape[0], q.shape[1], Dv)
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
+        out = _empty(shape, q.dtype, q.device, stream)
     elif out.shape != shape or out.dtype != q.dtype:
         raise ValueError(f"out must be a {q.dtype} tensor of shape {shape}")
     if lse is None:
         if return_lse:
-            lse = torch.empty(lse_shape, dtype=torch.float32, device=q.device)
+            lse = _empty(lse_shape, torch.float32, q.device, stream)
     elif lse.shape != lse_shape or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous fp32 tensor of shape {lse_shape}")
     return out, lse
@@ -664,11 +673,11 @@ def sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_le
     _int32_vector("kv_len", kv_len, B)
     max_pages = page_table.shape[1]
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out, lse = _paged_outputs(q, Dv, (B, Hq), out, lse, return_lse)
+    out, lse = _paged_outputs(q, Dv, (B, Hq), out, lse, return_lse, stream)
     lib = _load()
     if workspace is None:
-        workspace = torch.empty(lib.sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_pages * page_size, Dv),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _empty(lib.sdpa_decode_paged_fp8_workspace_size(B, Hq, Hkv, max_pages * page_size, Dv),
+                           torch.uint8, q.device, stream)
     dev = _current_device(("q", "k_pool", "v_pool", "k_scale", "v_scale", "page_table", "kv_len", "out", "lse", "workspace"),
                           (q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, out, lse, workspace))
     _unit_vectors(("kv_len", "workspace"), (kv_len, workspace))
@@ -705,11 +714,11 @@ def _fwd_paged(name, q, pools, sizes, page_table, kv_len, cu_seqlens_q, max_seql
     _check_page_table(B, page_table)
     max_pages, max_seqlen_q = page_table.shape[1], int(max_seqlen_q)
     scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out, lse = _paged_outputs(q, Dv, (Hq, total_q), out, lse, return_lse)
+    out, lse = _paged_outputs(q, Dv, (Hq, total_q), out, lse, return_lse, stream)
     lib = _load()
     if workspace is None:
         need = lib.sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, max_pages * page_size, Dv)
-        workspace = torch.empty(max(16, need), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(16, need), torch.uint8, q.device, stream)
     dev = _current_device(("q", "k_pool", "v_pool", "page_table", "kv_len", "cu_seqlens_q", "out", "lse", "workspace",
                            "k_scale", "v_scale"),
                           (q, pools[0], pools[1], page_table, kv_len, cu_seqlens_q, out, lse, workspace, *pools[2:]))

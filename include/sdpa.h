@@ -363,7 +363,7 @@ int sdpa_cache_write_fp8(const void* k, const void* v, void* k_pool, void* v_poo
  * each code * scale rounded once (exact in bf16 for the scales sdpa_cache_write_fp8 writes).  The
  * result is what sdpa_fwd_varlen takes.  Rows no sequence owns are left as they are; a row whose slot
  * lies outside the page table or the pool is written as zeros and reported as in
- * sdpa_cache_write_fp8.  strides as there.
+ * sdpa_cache_write_fp8.  strides and limits as there.
  */
 int sdpa_cache_read_fp8(const void* k_pool, const void* v_pool, const float* k_scale, const float* v_scale,
                         const int32_t* page_table, const int32_t* cu_seqlens, void* k, void* v, int B, int Hkv,
@@ -386,7 +386,8 @@ size_t sdpa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int max_kv, 
  *
  *   q [B, Hq, D], o [B, Hq, Dv] in dtype (SDPA_F16 or SDPA_BF16); the pools, scales and page table as above
  *   strides: NULL or the 11 element strides of sdpa_decode_paged (pool strides multiples of 16)
- *   workspace: at least sdpa_decode_paged_fp8_workspace_size(...) bytes, 16-byte aligned
+ *   workspace: at least sdpa_decode_paged_fp8_workspace_size(...) bytes, 16-byte aligned; calls that overlap
+ *           on the GPU need separate ones
  * (D, Dv) in {(128, 128), (192, 128)}, Hq / Hkv <= 16; kv_len, table entries past a sequence's pages,
  * lse and the other arguments and limits as in sdpa_decode_paged.
  */

@@ -292,6 +292,33 @@ def test_streams_graph_and_repeatability(quant):
     assert fa.sdpa_check_device_status() == fa.SDPA_OK
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(monkeypatch):
+    q, pools, table, kv, cu = make([3, 2], [900, 77], 8, 2, 128, 128, 64, "bf16", True, seed=6)
+    kc, ks, vc, vs = (t.to(DEV) for t in pools)
+    q, table, kv, cu = (t.to(DEV) for t in (q, table, kv, cu))
+    rows = torch.tensor([0, 900, 977], dtype=torch.int32, device=DEV)
+    pools16 = [oracle.dequantise_pool(*pools[i:i + 2]).to(torch.bfloat16).to(DEV) for i in (0, 2)]
+    calls = [lambda **kw: fa.sdpa_fwd_paged_fp8(q, kc, vc, ks, vs, table, kv, cu, 3, causal=True, **kw),
+             lambda **kw: fa.sdpa_fwd_paged(q, *pools16, table, kv, cu, 3, causal=True, **kw),
+             lambda **kw: fa.sdpa_decode_paged_fp8(q[:2], kc, vc, ks, vs, table, kv, **kw),
+             lambda **kw: fa.sdpa_cache_read_fp8(kc, vc, ks, vs, table, rows, 977, **kw)]
+    want = [call() for call in calls]
+    torch.cuda.synchronize()
+    side, used, empty = torch.cuda.Stream(), [], torch.empty
+
+    def noted(*a, **kw):
+        used.append(torch.cuda.current_stream())
+        return empty(*a, **kw)
+
+    monkeypatch.setattr(torch, "empty", noted)
+    got = [call(stream=side) for call in calls]
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert len(used) == 3 + 3 + 3 + 2 and all(s == side for s in used)
+    for g, w in zip(got, want):
+        assert torch.equal(g[0], w[0]) and torch.equal(g[1], w[1])
+
+
 @pytest.mark.parametrize("quant", [False, True])
 def test_a_wait_that_gives_up_is_reported(quant):
     x = make([3, 200], [300, 900], 8, 2, 128, 128, 64, "bf16", quant)
