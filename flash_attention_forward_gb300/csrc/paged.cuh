@@ -15,6 +15,10 @@
 //     that few query rows over long caches, ragged batches and long chunks alike keep every SM busy to the end.
 //     A unit whose keys a cut divides writes partials (unnormalised O, max, sum) that a second
 //     kernel merges.  The cuts are planned on the device, where the lengths are (paged_plan_kernel).
+// Bound by the tensor cores for long chunks and by memory for short ones.  32 / 8 heads of 128, pages of 64, bf16:
+// 8192 tokens over 32768 rows 2400 us in a short run (1.6 PFLOP/s) and 2700 under the power cap, drafts of 3-8
+// tokens of 16 sequences of 1024-16384 rows 103 us (5.5 TB/s); over e4m3 pages 4 x 2048 tokens of 16384 rows
+// 1530 us (1.35 PFLOP/s), the drafts 89 us (3.3 TB/s).
 // K and V blocks have a ring each and are loaded in the order of their use: K(0), then K(j) and V(j-1)
 // for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the rest of
 // the rings is loads in flight.
@@ -23,7 +27,7 @@
 // operands (one thread per row) and both products are fp16, whatever the query's type.  Long chunks have four
 // such warps, which alternate between K and V and leave the softmax registers for a row's 128 scores; short ones,
 // where the conversion of a block stands between its arrival and its MMAs, four for K and four for V (one
-// warpgroup for all took the long ones from 1760 to 1590 us, four sequences' 2048 tokens of 16384 rows):
+// warpgroup for both: 1760 -> 1590 us for 2048 tokens of 16384 rows of four sequences, but 95 -> 103 for drafts):
 //   * K' = code * (k_scale / 2^ek), 2^(ek + 6) the power of two of the block's largest scale: the
 //     largest row lies just below fp16's largest value, rows of power-of-two scales stay exact down
 //     to 2^-21 of the largest scale and lose a bit for each one below (K' is read as 0 under
@@ -50,7 +54,8 @@ constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn mas
 constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
 constexpr int kExpRing = 8;         // blocks whose exponents are kept: more than the ring can run ahead
 
-// ONE: no sequence has more tokens than one query tile holds.  Shared memory then keeps one query tile,
+// ONE: no sequence has more tokens than one query tile holds (drafts of 16 sequences: 109 us over 16-bit pages and
+// 94 over e4m3 ones, 114 and 118 by the other form).  Shared memory then keeps one query tile,
 // the two accumulators take the even and the odd key blocks ("readers" 0 and 1, each with half of the
 // rings), so that one's softmax runs beside the other's MMAs, and slot 0's warps merge the two at the
 // end of a piece.  Otherwise accumulator t serves query tile t and both read every block.
@@ -170,7 +175,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 // chunks of 64 columns, as the MMAs read them, times the pair factor f; f = 0 stores zeros whatever
 // the codes are.  One thread per row: both the reads and the writes of eight neighbouring rows
 // fall on all banks.  The loop over chunks is not unrolled: the kernel's loops together must fit the
-// instruction cache (with both unrolled, 2048 tokens of 8192 rows took 284 us instead of 263).
+// instruction cache (drafts of 16 sequences: 92.5 us so, 100 with two chunks an iteration, 96 with half a one).
 template <int W>
 __device__ __forceinline__ void convert_row(const uint8_t* raw, uint8_t* dst, int chunks, int r, uint32_t f) {
   const int x = (r & 7) << 4;
