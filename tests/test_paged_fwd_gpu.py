@@ -236,6 +236,30 @@ def test_strides_interleaved_pools_and_untouched_rows(quant):
     check(q, pools, table, kv, cu, os_[:27].contiguous(), lse[:, :27].contiguous(), 0.1, True)
 
 
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new", [[3, 2, 4], [150, 70, 200]])
+def test_lengths_outside_the_table_are_clamped(quant, new):
+    q, pools, table, kv, cu = make(new, [100, 40, 300], 8, 2, 128, 128, 32, "bf16", quant, seed=15)
+    for i, t in enumerate(pools):  # every row of every page may be visible now
+        pools[i] = torch.nan_to_num(t.float(), nan=0.5).to(t.dtype)
+    table[1] = torch.arange(table.shape[1], dtype=torch.int32) % pools[0].shape[0]
+    cap = table.shape[1] * 32
+    kv = torch.tensor([-(1 << 31), (1 << 31) - 1, 300], dtype=torch.int32)
+    clamped = torch.tensor([0, cap, 300], dtype=torch.int32)
+    o, lse = run(q, pools, table, kv, cu, max(new), scale=0.09, causal=False)
+    check(q, pools, table, clamped, cu, o, lse, 0.09, False)
+    # a position far behind the table sees all of it, one before the first row nothing
+    o, lse = run(q, pools, table, kv, cu, max(new), scale=0.09, causal=True)
+    ref, ref_lse = oracle.sdpa_fwd_paged(q, *values(pools), table, clamped, cu, scale=0.09, causal=False)
+    rows = slice(int(cu[1]), int(cu[2]))
+    vmax = float(oracle.gather_pages(values(pools)[1], table, clamped.tolist())[1].abs().max())
+    u_p = 2.0 ** -11 if quant else 2.0 ** -8
+    err = np.abs(o.double().cpu().numpy()[rows] - ref[rows])
+    assert (err <= 2.0 ** -8 * np.abs(ref[rows]) + (u_p + 2.0 ** -14 + 2.0 ** -16) * vmax).all()
+    assert np.abs(lse.double().cpu().numpy()[:, rows] - ref_lse[:, rows]).max() <= TOL_LSE
+    assert (o[:new[0]] == 0).all() and torch.isneginf(lse[:, :new[0]]).all()
+
+
 def test_bad_offsets_store_nothing_and_are_reported():
     q, pools, table, kv, cu = make([5, 6], [50, 40], 4, 2, 128, 128, 16, "bf16", False)
     d = [t.to(DEV) for t in pools]
@@ -246,6 +270,19 @@ def test_bad_offsets_store_nothing_and_are_reported():
         torch.cuda.synchronize()
         assert fa.sdpa_check_device_status() == fa.SDPA_ERR_INVALID
         assert (out == 3).all()
+
+
+@pytest.mark.parametrize("new", [[200, 90], [1] * 300])
+def test_bad_offsets_where_a_kernel_of_its_own_plans(new):
+    # long chunks, and more sequences than the attention kernel plans for
+    q, pools, table, kv, cu = make(new, [250] * len(new), 4, 2, 128, 128, 16, "bf16", False)
+    d = [t.to(DEV) for t in pools]
+    cu[1] = cu[2] + 1
+    out = torch.full((sum(new), 4, 128), 3.0, dtype=q.dtype, device=DEV)
+    fa.sdpa_fwd_paged(q.to(DEV), d[0], d[1], table.to(DEV), kv.to(DEV), cu.to(DEV), max(new), out=out)
+    torch.cuda.synchronize()
+    assert fa.sdpa_check_device_status() == fa.SDPA_ERR_INVALID
+    assert (out == 3).all()
 
 
 @pytest.mark.parametrize("quant", [False, True])
