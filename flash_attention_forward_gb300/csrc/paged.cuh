@@ -124,26 +124,43 @@ struct PagedPiece {
 };
 static_assert(sizeof(PagedPiece) == 64, "the producer announces a piece in 64 bytes");
 
-// The pieces of this CTA's stretch of the line, in order (the producer's walk; the other roles read
+// Loads of the walk; the host, where tests replay it, has neither form.
+__host__ __device__ __forceinline__ int walk_ld(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+__host__ __device__ __forceinline__ int2 walk_ld(const int2* p) {
+#ifdef __CUDA_ARCH__
+  return ld_dep(p);
+#else
+  return *p;
+#endif
+}
+
+// The pieces of a CTA's stretch of the line, in order (the producer's walk; the other roles read
 // what it announces).
 struct PagedWalk {
-  int tile, kvh, off, first;
+  int cta, tile, kvh, off, first;
   int4 end;
 
-  __device__ __forceinline__ PagedWalk(int4 from, int4 to) : tile(from.x), kvh(from.y), off(from.z), first(1), end(to) {}
+  __host__ __device__ __forceinline__ PagedWalk(int cta, int4 from, int4 to)
+      : cta(cta), tile(from.x), kvh(from.y), off(from.z), first(1), end(to) {}
   template <bool ONE>
-  __device__ __forceinline__ PagedPiece next(const PagedParams& p) {
+  __host__ __device__ __forceinline__ PagedPiece next(const PagedParams& p) {
     PagedPiece w{};
     // planned by this kernel, tiles are sequences, and those without tokens are passed over
     if (ONE && p.inline_plan)
-      while (tile < end.x && __ldg(p.cu_q + tile) == __ldg(p.cu_q + tile + 1)) ++tile;
+      while (tile < end.x && walk_ld(p.cu_q + tile) == walk_ld(p.cu_q + tile + 1)) ++tile;
     if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
-    const int2 at = ONE && p.inline_plan ? make_int2(tile, 0) : ld_dep(p.plan.tiles + tile);
+    const int2 at = ONE && p.inline_plan ? make_int2(tile, 0) : walk_ld(p.plan.tiles + tile);
     w.b = at.x;
     w.kvh = kvh;
-    w.q_off = __ldg(p.cu_q + w.b);
-    w.n = __ldg(p.cu_q + w.b + 1) - w.q_off;
-    w.len = __ldg(p.kv_len + w.b);
+    w.q_off = walk_ld(p.cu_q + w.b);
+    w.n = walk_ld(p.cu_q + w.b + 1) - w.q_off;
+    w.len = walk_ld(p.kv_len + w.b);
     w.sk = min(max(w.len, 0), p.max_kv);
     w.tok0 = at.y * kTilesPerCta * p.tok_tile;
     w.jb0 = off;
@@ -157,7 +174,7 @@ struct PagedWalk {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       w.n_s[t] = ONE ? (w.n_blocks + 1 - t) / 2 : min(max(blocks[t] - off, 0), w.n_blocks);
-    w.slot = (off > 0 || stop < all) ? 2 * static_cast<int>(blockIdx.x) + 1 - first : -1;
+    w.slot = (off > 0 || stop < all) ? 2 * cta + 1 - first : -1;
     first = 0;
     off = 0;
     if (++kvh == p.Hkv) kvh = 0, ++tile;
@@ -260,16 +277,7 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   const long long total = pos[p.B];
   const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / kMinWork)));
   const int cta = blockIdx.x;
-  auto cut_at = [&](int c) {
-    if (c >= n_ctas) return make_int4(bad ? 0 : p.B, 0, 0, 0);
-    const long long x = total / n_ctas * c + total % n_ctas * c / n_ctas;
-    int lo = 0, hi = p.B;  // the last sequence that starts at or before x (it has tokens)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pos[mid] <= x) lo = mid; else hi = mid;
-    }
-    return paged_cut(p, x, pos[lo], lo, static_cast<int>((pos[lo + 1] - pos[lo]) / p.Hkv) - kUnitCost);
-  };
+  auto cut_at = [&](int c) { return bad ? make_int4(0, 0, 0, 0) : paged_inline_cut(p, pos, c, n_ctas); };
   if (cta < n_ctas) {
     if (tid == 0) mine[0] = cut_at(cta);
     if (tid == 32) mine[1] = cut_at(cta + 1);
@@ -438,7 +446,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     uint64_t* ld_full = QUANT ? raw_full : kv_full;
     uint64_t* ld_empty = QUANT ? raw_empty : kv_empty;
     const int q_tx = p.tok_tile * p.group * D * 2;
-    PagedWalk walk(cuts[0], cuts[1]);
+    PagedWalk walk(blockIdx.x, cuts[0], cuts[1]);
     int qn[2] = {0, 0};     // pieces of each accumulator
     int nl[2][2] = {};      // blocks of K and of V issued (16-bit pages: per reader)
     int nr = 0;             // ragged V blocks among them

@@ -102,7 +102,7 @@ __host__ __device__ __forceinline__ int paged_tile_blocks(int n, int len, int sk
 #ifdef __CUDACC__
 // Where cut c of n_ctas lies: position x of the line falls into a unit of `blocks` key blocks that starts
 // at `start` for KV head 0 (the tile's units follow one another).  {tile, KV head, block}.
-__device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, long long start, int tile, int blocks) {
+__host__ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, long long start, int tile, int blocks) {
   const int r = static_cast<int>(x - start);
   int kvh = r / (blocks + kUnitCost);
   int off = r - kvh * (blocks + kUnitCost) - kUnitCost;
@@ -114,9 +114,25 @@ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, lon
   }
   return make_int4(tile, kvh, off, 0);
 }
+// Cut c of n_ctas where tiles are sequences and sequence b lies from pos[b] to pos[b + 1].  Those without tokens
+// have no length, and no cut names one: the walk passes over them, and the unit that it begins with has to be the
+// one that the cut names, as paged_group tells a CTA's first piece by that.
+__host__ __device__ __forceinline__ int4 paged_inline_cut(const PagedParams& p, const long long* pos, int c, int n_ctas) {
+  if (c >= n_ctas) return make_int4(p.B, 0, 0, 0);
+  const long long total = pos[p.B];
+  const long long x = total / n_ctas * c + total % n_ctas * c / n_ctas;
+  int lo = 0, hi = p.B;  // the last sequence that starts at or before x (it has tokens)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pos[mid] <= x) lo = mid; else hi = mid;
+  }
+  int4 cut = paged_cut(p, x, pos[lo], lo, static_cast<int>((pos[lo + 1] - pos[lo]) / p.Hkv) - kUnitCost);
+  while (cut.x < p.B && pos[cut.x + 1] == pos[cut.x]) ++cut.x;
+  return cut;
+}
 // The group of a unit whose first cut is cut c (cuts[c].z > 0 and not cut before), or false.
-__device__ __forceinline__ bool paged_group(const int4* cuts, int c, int n_ctas, int2 at, int q_off, int n, int len,
-                                            PagedGroup& g) {
+__host__ __device__ __forceinline__ bool paged_group(const int4* cuts, int c, int n_ctas, int2 at, int q_off, int n,
+                                                     int len, PagedGroup& g) {
   const int4 cut = cuts[c];
   if (cut.z == 0) return false;
   const int4 prev = cuts[c - 1];  // c > 0: the line starts with a whole unit

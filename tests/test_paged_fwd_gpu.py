@@ -409,3 +409,36 @@ def test_a_quantised_cache_in_use():
     torch.cuda.synchronize()
     assert (o2.float() - od.float()).abs().max().item() <= 2 * 2.0 ** -8 * 4.5
     assert fa.sdpa_check_device_status() == fa.SDPA_OK
+
+
+def nan_workspace(q, pools, table, cu, maxq, Hkv):
+    """A workspace of the full size filled with NaN: a partial that nobody wrote shows in the result."""
+    n = fa.sdpa_fwd_paged_workspace_size(len(cu) - 1, q.shape[1], Hkv, q.shape[0], maxq, table.shape[1] * pools[0].shape[1],
+                                         pools[-2].shape[-1] if len(pools) == 4 else pools[1].shape[-1])
+    return torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("new,lens,Hq,Hkv", [([4, 0, 2], [8600, 6600, 1200], 8, 2), ([1, 0, 1], [550, 5, 3000], 1, 1),
+                                             ([1, 0, 1], [550, 5, 5000], 1, 1), ([1, 0, 1], [550, 5, 8000], 1, 1)])
+def test_a_cut_next_to_a_sequence_without_tokens(quant, new, lens, Hq, Hkv):
+    x = make(new, lens, Hq, Hkv, 128, 128, 64, "bf16", quant, seed=21)
+    ws = nan_workspace(x[0], x[1], x[2], x[4], max(new), Hkv)
+    o, lse = run(*x, max(new), scale=0.09, causal=True, workspace=ws)
+    check(*x, o, lse, 0.09, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("seed", range(6))
+def test_cuts_anywhere_in_batches_with_idle_sequences(quant, seed):
+    # the equal stretches of the SMs cut units next to their edges, several times, and beside sequences without
+    # new tokens; odd seeds have chunks of more than a query tile, which a kernel of its own plans
+    g = np.random.default_rng(40 + seed)
+    B, Hkv = int(g.integers(2, 21)), [1, 2, 8][seed % 3]
+    new = g.integers(1, 9 if seed % 2 == 0 else 90, B) * (g.random(B) >= 0.33)
+    new[int(g.integers(B))] = 3
+    lens = np.exp(g.uniform(np.log(500), np.log(6000), B)).astype(int).tolist()
+    x = make(new.tolist(), lens, 4 * Hkv, Hkv, 64, 64, 64, "f16", quant, seed=seed)
+    ws = nan_workspace(x[0], x[1], x[2], x[4], int(new.max()), Hkv)
+    o, lse = run(*x, int(new.max()), scale=0.125, causal=True, workspace=ws)
+    check(*x, o, lse, 0.125, True)
