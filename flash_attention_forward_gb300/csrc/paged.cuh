@@ -1050,7 +1050,10 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           mb = fmaxf(mb, fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         }
         const float m_cand = fmaxf(m_used, QUANT ? fmaf(mb, blk_scale2, shift) : mb * blk_scale2);
-        const bool need = m_cand > m_used + kPagedRescaleLog2;
+        // Rows without a token have no say in when the warp rescales: they may be another sequence's queries or, behind
+        // the last full token of a tile, what an earlier kernel left in shared memory, and the others' rounding
+        // would depend on them.
+        const bool need = row_valid && m_cand > m_used + kPagedRescaleLog2;
         const bool rescale = __any_sync(0xffffffffu, need);
         float alpha = 1.f;
         if (rescale) {

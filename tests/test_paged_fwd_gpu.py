@@ -442,3 +442,21 @@ def test_cuts_anywhere_in_batches_with_idle_sequences(quant, seed):
     ws = nan_workspace(x[0], x[1], x[2], x[4], int(new.max()), Hkv)
     o, lse = run(*x, int(new.max()), scale=0.125, causal=True, workspace=ws)
     check(*x, o, lse, 0.125, True)
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new", [[18, 17], [300, 210]])
+def test_rows_of_a_tile_without_a_token_change_nothing(quant, dtype, new):
+    # 7 heads a KV head fill 126 of a tile's 128 rows; the other two hold what an earlier kernel left in shared memory,
+    # here the queries of calls whose rows are all in use and whose scores are small or very large
+    x = make(new, [3000, 1700], 14, 2, 128, 128, 64, dtype, quant, seed=31)
+    q8, *rest = make([64, 64], [3000, 1700], 16, 2, 128, 128, 64, dtype, quant, seed=32)
+    got = []
+    for gain in (0.0, 1.0, 100.0):
+        for _ in range(2):
+            run((q8 * gain).to(q8.dtype), *rest, 64, scale=0.09, causal=True)
+        got.append(run(*x, max(new), scale=0.09, causal=True))
+    same = [torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1]) for o, lse in got]
+    assert all(same), same
+    check(*x, *got[0], 0.09, True)
