@@ -103,9 +103,9 @@ __host__ __device__ __forceinline__ int paged_tile_blocks(int n, int len, int sk
 // Where cut c of n_ctas lies: position x of the line falls into a unit of `blocks` key blocks that starts
 // at `start` for KV head 0 (the tile's units follow one another).  {tile, KV head, block}.
 __host__ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, long long start, int tile, int blocks) {
-  const int r = static_cast<int>(x - start);
-  int kvh = r / (blocks + kUnitCost);
-  int off = r - kvh * (blocks + kUnitCost) - kUnitCost;
+  const long long unit = blocks + kUnitCost, r = x - start;  // many KV heads of a long sequence: past 32 bits
+  int kvh = static_cast<int>(r / unit);
+  int off = static_cast<int>(r - kvh * unit) - kUnitCost;
   if (p.cut ? off < kMinPiece : 2 * off < blocks) {
     off = 0;
   } else if (!p.cut || blocks - off < kMinPiece) {

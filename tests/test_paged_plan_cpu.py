@@ -48,3 +48,10 @@ def test_random_batches(replay, one, idle):
         kv = np.exp(g.uniform(0, np.log(16384), B)).astype(int)
         kv[g.random(B) < 0.05] = 0
         replay(new, kv, Hkv * group, Hkv, int(g.integers(1, 161)), one, bool(g.integers(2)), cut=bool(g.random() < 0.9))
+
+
+@pytest.mark.parametrize("one", [True, False])
+def test_a_sequence_whose_units_pass_32_bits(replay, one):
+    # 300 KV heads of 2^23 key blocks each: the line of one sequence is longer than 2^31
+    for kv in ([1 << 30], [1 << 30, 700, 1 << 30]):
+        replay([1] * len(kv), kv, 300, 300, one=one, max_kv=1 << 30)
