@@ -87,13 +87,14 @@ struct PagedCfg {
   static constexpr int OFF_EXP = OFF_BAR + BARS;                    // int2 [kExpRing][4]
   static constexpr int OFF_QEXP = OFF_EXP + (QUANT ? kExpRing * 32 : 0);  // int8 [2 tiles][2][128]
   // pieces announced by the producer: more than it can run ahead of the slowest role.  Of the pieces
-  // behind the one whose last V is used up, each has a V that waits in the rings for its softmax.
+  // behind the one whose last V is used up, each has a V that waits in the rings for its softmax; of those
+  // in which a role has no block, one at a time waits for it (passed).
   static constexpr int PIECES = D == 64 ? 16 : 8;
   static constexpr int OFF_PIECE = OFF_QEXP + (QUANT ? 512 : 0);
   static constexpr int OFF_ML = OFF_PIECE + PIECES * 64;            // float2 [128]: max and sum of slot 1
   static constexpr int SMEM = OFF_ML + 1024;
   static_assert((KS > VS ? KS : VS) + 2 <= kExpRing, "the exponent ring holds what the converters write");
-  static_assert(VS + RAWS + 2 <= PIECES, "the piece ring holds what the producer announces");
+  static_assert(VS + RAWS + 4 <= PIECES, "the piece ring holds what the producer announces");
   // warpgroups: control (producer, MMA, helpers), converters (quantised: of K and of V, or one of both), two softmax
   static constexpr int CONVERTERS = !QUANT ? 0 : ONE ? 2 : 1;
   static constexpr int SOFTMAX_WARP = 4 + 4 * CONVERTERS;
@@ -306,6 +307,9 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
 
 // Barriers (phases continue from piece to piece; the arrivals of warps are one each):
 //   piece[i % PIECES]     : the producer announced piece i
+//   passed[r]             : softmax r (all its threads), or the helper (r = 2), has passed a piece in which it has no
+//                           block; nothing else holds the producer for it there (e4m3 mixed batch 258 -> 261 us;
+//                           a barrier that every role arrives at in every piece: 267)
 //   q_full[t] / q_empty[t]: Q tile t landed / accumulator t's last QK MMA of the piece finished
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
 //   kv_full / kv_empty    : a slot of the K or V ring holds its block / the issuers that read it are done
@@ -356,14 +360,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   uint64_t* raw_empty = raw_full + 2 * NR;   // [2 NR]
   uint64_t* e_full = raw_empty + 2 * NR;    // [2 kExpRing]
   uint64_t* piece = e_full + 2 * kExpRing;  // [PIECES]
-  uint64_t* ml_full = piece + C::PIECES;  // [1]
+  uint64_t* passed = piece + C::PIECES;   // [3]
+  uint64_t* ml_full = passed + 3;         // [1]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ml_full + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int2* blk_exp = reinterpret_cast<int2*>(smem + C::OFF_EXP);
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
   PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::OFF_PIECE);
   float2* ml_x = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [128]
-  static_assert((21 + kFixRing + 2 * kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
+  static_assert((24 + kFixRing + 2 * kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -395,6 +400,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&raw_empty[s], 4);
     }
     for (int s = 0; s < C::PIECES; ++s) mbar_init(&piece[s], 1);
+    for (int r = 0; r < 3; ++r) mbar_init(&passed[r], r < 2 ? 128 : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -450,9 +456,19 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     int qn[2] = {0, 0};     // pieces of each accumulator
     int nl[2][2] = {};      // blocks of K and of V issued (16-bit pages: per reader)
     int nr = 0;             // ragged V blocks among them
+    int np[3] = {0, 0, 0};  // pieces without a block for softmax 0, softmax 1, the helper
     bool ok = true;
     while (ok) {
       const PagedPiece w = walk.template next<ONE>(p);
+      if (w.n_blocks > 0) {
+#pragma unroll
+        for (int r = 0; r < (QUANT ? 2 : 3); ++r) {
+          if (r < 2 ? w.n_s[r] > 0 : (w.jb0 + w.n_blocks) * kBlockK > w.sk) continue;
+          if (np[r] > 0) ok = ok && mbar_wait_warp(&passed[r], (np[r] - 1) & 1, abort_flag, p.status);
+          ++np[r];
+        }
+        if (!ok) break;
+      }
       if (lane == 0) {
         pieces[n_piece % C::PIECES] = w;
         mbar_arrive(&piece[n_piece % C::PIECES]);
@@ -707,6 +723,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           }
           nv[0] += ONE ? w.n_s[0] : w.n_blocks;
           nv[1] += ONE ? w.n_s[1] : 0;
+          if (live >= kBlockK) warp_arrive(&passed[2], lane);
         }
       }
     }
@@ -958,6 +975,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       if (ONE || n > 0) ++qn;
       if (n == 0) {
         if (n_other > 0) ++on[1 - t];
+        mbar_arrive(&passed[t]);
         continue;
       }
       const int tok = w.tok0 + qt * p.tok_tile + row_tok;
