@@ -31,7 +31,8 @@
 //   * K' = code * (k_scale / 2^ek), 2^(ek + 6) the power of two of the block's largest scale: the
 //     largest row lies just below fp16's largest value, rows of power-of-two scales stay exact down
 //     to 2^-21 of the largest scale and lose a bit for each one below (K' is read as 0 under
-//     2^-30).  The block's scores are multiplied by 2^ek;
+//     2^-30).  Other scales cost two roundings, of the factor and of the product (2^-11 each; a single one would
+//     need the products in fp32, and the conversions to it and back).  The block's scores are multiplied by 2^ek;
 //   * V' likewise with ev, and 2^ev joins the exponent: with y = s + ev the running maximum is taken
 //     over y, P = 2^(y - m) meets V', and the row sum takes 2^-ev of the block's sum.  P stays in
 //     fp16's best range whatever the scales are;

@@ -449,8 +449,9 @@ int sdpa_fwd_paged(const void* q, const void* k_pool, const void* v_pool, const 
  * v_scale; pool strides multiples of 16).  The codes are brought to fp16 on chip and both products
  * run in fp16 with fp32 accumulation, a bf16 query scaled into fp16 by a power of two per row; P is
  * rounded to fp16.  Scales enter relative to the largest of their 128-key block: rows of power-of-two
- * scales are exact down to 2^-21 of it, then lose a bit for each power of two and vanish under 2^-30;
- * other scales are rounded to fp16 (2^-11).
+ * scales are exact down to 2^-21 of it, then lose a bit for each power of two and vanish under 2^-30.
+ * Other scales are rounded to fp16 and their products with the codes once more: such a value of K or V
+ * is off by up to 2^-10 of itself.
  */
 int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, const float* k_scale,
                        const float* v_scale, const int32_t* page_table, const int32_t* kv_len,

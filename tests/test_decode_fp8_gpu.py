@@ -186,3 +186,16 @@ def test_cuts_anywhere(seed):
     x, pools, table = make(w, lens.tolist(), 64, seed=seed)
     o, lse = run(x, pools, table, w.scale)
     check(x, pools, table, w.scale, o, lse)
+
+
+@pytest.mark.parametrize("Hq,D", [(8, 128), (32, 192)])
+def test_scales_that_are_no_powers_of_two(Hq, D):
+    # the decode keeps the scales in fp32, so the bound at the top holds for any of them
+    lens = [700, 65, 1]
+    w = W.with_shape(B=3, Hq=Hq, Hkv=2, Sk=1024, D=D)
+    x, pools, table = make(w, lens, 32)
+    g = torch.Generator().manual_seed(53)
+    for i in (1, 3):
+        pools[i] = pools[i] * (0.5 + torch.rand(pools[i].shape, generator=g))
+    o, lse = run(x, pools, table, w.scale)
+    check(x, pools, table, w.scale, o, lse)

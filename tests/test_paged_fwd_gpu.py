@@ -460,3 +460,37 @@ def test_rows_of_a_tile_without_a_token_change_nothing(quant, dtype, new):
     same = [torch.equal(o, got[0][0]) and torch.equal(lse, got[0][1]) for o, lse in got]
     assert all(same), same
     check(*x, *got[0], 0.09, True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new,Hq,D", [([1, 3, 8, 2], 8, 128), ([1, 40, 300, 5], 8, 128), ([7, 1, 130, 9], 4, 192)])
+def test_scales_that_are_no_powers_of_two(dtype, new, Hq, D):
+    # A K or V value takes two fp16 roundings, (1 + 2^-11)^2 - 1 <= r = 2^-10 + 2^-22 of itself (the factors lie in
+    # [16, 128) here, so nothing is subnormal).  A score moves by at most d = r * scale * sum |q_i K_i|, so a weight by
+    # e^(2 d), the output by (e^(2 d) - 1 + r) vmax beside the bound at the top, and the log-sum-exp by d.
+    lens = [1, 700, 350, 90]
+    q, pools, table, kv, cu = make(new, lens, Hq, 2, D, 128, 32, dtype, True, seed=51)
+    g = torch.Generator().manual_seed(52)
+    for i in (1, 3):  # power-of-two scales of randn rows: 2^-7 and 2^-6, now within a factor of 4 of one another
+        pools[i] = torch.where(torch.isnan(pools[i]), pools[i], 2.0 ** -7 * (0.5 + 1.5 * torch.rand(pools[i].shape, generator=g)))
+    o, lse = run(q, pools, table, kv, cu, max(new), scale=0.03, causal=True)
+    k, v = values(pools)
+    ref, ref_lse = oracle.sdpa_fwd_paged(q, k, v, table, lens, cu, scale=0.03, causal=True)
+    got, got_lse = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    kg, vg = oracle.gather_pages(k, table, lens), oracle.gather_pages(v, table, lens)
+    r, u = 2.0 ** -10 + 2.0 ** -22, torch.finfo(o.dtype).eps / 2
+    for b, L in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        vmax = float(vg[b, :L].abs().max())
+        kh = kg[b, :L].abs().repeat_interleave(Hq // 2, 1)  # [L, Hq, D]
+        d = r * 0.03 * torch.einsum("nhd,lhd->nhl", q[rows].double().abs(), kh.double()).amax(-1).numpy()  # [n, Hq]
+        tol = u * np.abs(ref[rows]) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -16 + r + np.expm1(2 * d)[..., None]) * vmax
+        assert (np.abs(got[rows] - ref[rows]) <= tol).all(), b
+        seen = np.isfinite(ref_lse[:, rows])
+        assert np.array_equal(np.isfinite(got_lse[:, rows]), seen)
+        e = np.abs(np.where(seen, got_lse[:, rows], 0) - np.where(seen, ref_lse[:, rows], 0))
+        assert (e <= TOL_LSE + d.T).all(), b
+    # one visible key: the output is its V row, off by the two roundings and its own
+    if new[0] == 1 and o.dtype == torch.float16:
+        want = vg[0, 0].repeat_interleave(Hq // 2, 0).numpy()
+        assert (np.abs(got[0] - want) <= (r + 2.0 ** -11 * (1 + r)) * np.abs(want) + 2.0 ** -25).all()
