@@ -8,7 +8,9 @@
 // 2^-4 relative).  A scale of amax / 448 would round twice and gain nothing: a floating-point code
 // has the same relative step wherever in its range a value lies.  k >= -80 (rows of zeros take it):
 // the attention kernels hold 1 / scale in fp32.  NaN stays NaN and does not move the scale; a row
-// with an infinity gets 2^120, from which the infinity reads back as one and the rest as zeros.
+// with an infinity gets 2^120, from which the infinity reads back as one (448 * 2^120 is none of fp32's
+// values), entries of at most 2^110 as zeros and larger ones as they are rounded.  From 1.9375 * 2^127 on, where
+// the rounding reaches 2^128, finite values read back as infinities too.
 //
 // Both kernels are bound by memory: 3 (D + Dv) + 8 bytes move per row of K and V against some 40
 // instructions per 8 values.  66,000 tokens of 8 heads of 128 are written in 72 us (5.7 TB/s: 271 MB read,

@@ -341,8 +341,9 @@ int sdpa_decode_paged(const void* q, const void* k_pool, const void* v_pool, con
  * The scale of a row is the least power of two 2^k, k >= -80, with amax <= 448 * 2^k, and a code is
  * x * 2^-k rounded to nearest even: the scaling is exact, so a value is off by at most 2^-4 of
  * itself (or 2^-10 * scale, where the code is subnormal).  A row of zeros takes 2^-80.  NaN stays NaN and does
- * not move the scale; a row that holds an infinity takes 2^120, reads back as that infinity there
- * and as zeros elsewhere.
+ * not move the scale.  A row that holds an infinity takes 2^120 and reads back as that infinity there; its finite
+ * values of at most 2^110 read back as zeros, larger ones are rounded as above.  At 2^120 the code of a bf16
+ * magnitude of 1.9375 * 2^127 or more stands for 2^128, which reads back as an infinity.
  *
  * A row whose slot lies outside the page table or the pool (a negative position, a page index not in
  * [0, n_pages)) is not written, and the call raises a status that sdpa_check_device_status()

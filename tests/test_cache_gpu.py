@@ -177,3 +177,25 @@ def test_many_sequences_and_one_token_each():
     got = _write(k, v, codes, scales, table, kv_len, cu)
     want, ws = _expect(k, codes[0], scales[0], table, lens, [1] * B, page)
     assert torch.equal(got[0], want) and torch.equal(got[2], ws)
+
+
+def test_large_values_beside_an_infinity_and_at_the_end_of_the_range():
+    k, v, codes, scales, table, kv_len, cu = _cache([2], [2], 1, 64, 64, 16, "bf16")
+    k[:], v[:] = 0.0, 0.0
+    row = torch.tensor([float("-inf"), 3e38, -(2.0 ** 127), 2.0 ** 111, 1.5 * 2.0 ** 110, 2.0 ** 110, -1.0],
+                       dtype=torch.float64).to(torch.bfloat16)
+    k[0, 0, :7] = row
+    # codes at 2^120: 225.7 -> 224, 128, the smallest (2^-9), 1.5 * 2^-10 -> 2^-9, the tie 2^-10 -> 0, 0
+    want = [float("-inf"), 224 * 2.0 ** 120, -(2.0 ** 127), 2.0 ** 111, 2.0 ** 111, 0.0, 0.0]
+    top = torch.tensor([247 * 2.0 ** 120, -248 * 2.0 ** 120, 255 * 2.0 ** 120], dtype=torch.float64).to(torch.bfloat16)
+    assert top.double().tolist() == [247 * 2.0 ** 120, -248 * 2.0 ** 120, 255 * 2.0 ** 120]
+    k[1, 0, :3] = top
+    d = [c.to(DEV).view(torch.float8_e4m3fn) for c in codes] + [s.to(DEV) for s in scales]
+    fa.sdpa_cache_write_fp8(k.to(DEV), v.to(DEV), *d, table.to(DEV), kv_len.to(DEV), cu.to(DEV))
+    got, _ = fa.sdpa_cache_read_fp8(*d, table.to(DEV), cu.to(DEV), 2, dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    assert d[2][int(table[0, 0]), 0, :2].tolist() == [2.0 ** 120] * 2
+    assert got[0, 0, :7].double().cpu().tolist() == want
+    assert got[1, 0, :3].double().cpu().tolist() == [240 * 2.0 ** 120, float("-inf"), float("inf")]
+    assert (got[0, 0, 7:] == 0).all() and (got[1, 0, 3:] == 0).all()
