@@ -36,7 +36,9 @@ constexpr int kF8Chunk = 64;                   // keys per ring stage
 constexpr int kF8Box = kF8Chunk * 128;         // one box of 128 codes a row: 8 KB
 constexpr int kF8Threads = (kDecodeWarps + 1) * 32;
 // A zero scale (the filling of pages outside the pool) counts as 2^-100, so that the maximum stays
-// finite and the sum stays below fp32's largest value.
+// finite and the sum stays below fp32's largest value.  For V's scales in [2^-80, 2^80], as the header asks, the terms
+// 2^(s_j - m) of the sum lie between 2^88 and 2^-80 where their weight is the row's largest, and vanish (2^-126)
+// only under 2^-46 of it.
 constexpr float kMinLog2Scale = -100.f;
 constexpr int kF8MinSplit = 256;
 

@@ -199,3 +199,27 @@ def test_scales_that_are_no_powers_of_two(Hq, D):
         pools[i] = pools[i] * (0.5 + torch.rand(pools[i].shape, generator=g))
     o, lse = run(x, pools, table, w.scale)
     check(x, pools, table, w.scale, o, lse)
+
+
+@pytest.mark.parametrize("exps", [(80,), (-80,), (-80, 0, 80)])
+def test_scales_at_the_ends_of_their_range(exps):
+    # V's scales at 2^-80, 2^80 or a mixture, K's 2^60 with the softmax scale taking it back.  Beside the bounds at the
+    # top: s - m and s + log2(scale) are rounded where they are below 2^7 (2^-18, three times), and the sum's logarithm,
+    # up to 90 now, carries 2^-22 of itself (2^-15.5); times ln 2 all that is below 2^-15.
+    lens = [700, 65, 1]
+    w = W.with_shape(B=3, Hq=8, Hkv=2, Sk=1024)
+    x, pools, table = make(w, lens, 32)
+    g = torch.Generator().manual_seed(54)
+    pools[1] = pools[1] * 2.0 ** 60
+    e = torch.tensor(exps, dtype=torch.float64)[torch.randint(len(exps), pools[3].shape, generator=g)]
+    pools[3] = torch.where(torch.isnan(pools[3]), pools[3], torch.exp2(e).float())
+    scale = w.scale * 2.0 ** -60
+    o, lse = run(x, pools, table, scale)
+    k, v = oracle.dequantise_pool(*pools[:2]), oracle.dequantise_pool(*pools[2:])
+    ref, ref_lse = oracle.sdpa_decode_paged(x["q"], k, v, table, x["kv_len"], scale=scale)
+    vg = oracle.gather_pages(v, table, x["kv_len"])
+    for b, L in enumerate(lens):
+        vmax = float(vg[b, :L].abs().max())
+        err = np.abs(o[b].double().cpu().numpy() - ref[b])
+        assert (err <= 2.0 ** -8 * np.abs(ref[b]) + (TOL_P + 2.0 ** -15) * vmax).all(), b
+        assert np.abs(lse[b].double().cpu().numpy() - ref_lse[b]).max() <= TOL_LSE + 2.0 ** -15, b

@@ -494,3 +494,29 @@ def test_scales_that_are_no_powers_of_two(dtype, new, Hq, D):
     if new[0] == 1 and o.dtype == torch.float16:
         want = vg[0, 0].repeat_interleave(Hq // 2, 0).numpy()
         assert (np.abs(got[0] - want) <= (r + 2.0 ** -11 * (1 + r)) * np.abs(want) + 2.0 ** -25).all()
+
+
+@pytest.mark.parametrize("new", [[3, 8, 1], [90, 200, 1]])
+@pytest.mark.parametrize("exps", [(80,), (-80,), (-80, 0, 80)])
+def test_scales_at_the_ends_of_their_range(new, exps):
+    # V's scales at 2^-80, 2^80 or a mixture, K's 2^60 with the softmax scale taking it back.  Beside the bounds at the
+    # top: y - m is rounded where it is below 2^7 (2^-18, twice), and the sum's logarithm, up to 100 now, carries 2^-22
+    # of itself (2^-15.4); times ln 2 all that is below 2^-15.  A row under 2^-30 of its block's largest scale reads as
+    # zero, far inside the 2^-16 of vmax.
+    lens = [700, 1300, 77]
+    q, pools, table, kv, cu = make(new, lens, 8, 2, 128, 128, 32, "bf16", True, seed=55)
+    g = torch.Generator().manual_seed(56)
+    pools[1] = pools[1] * 2.0 ** 60
+    e = torch.tensor(exps, dtype=torch.float64)[torch.randint(len(exps), pools[3].shape, generator=g)]
+    pools[3] = torch.where(torch.isnan(pools[3]), pools[3], torch.exp2(e).float())
+    scale = 0.09 * 2.0 ** -60
+    o, lse = run(q, pools, table, kv, cu, max(new), scale=scale, causal=True)
+    k, v = values(pools)
+    ref, ref_lse = oracle.sdpa_fwd_paged(q, k, v, table, lens, cu, scale=scale, causal=True)
+    vg = oracle.gather_pages(v, table, lens)
+    for b, L in enumerate(lens):
+        rows = slice(int(cu[b]), int(cu[b + 1]))
+        vmax = float(vg[b, :L].abs().max())
+        err = np.abs(o.double().cpu().numpy()[rows] - ref[rows])
+        assert (err <= 2.0 ** -8 * np.abs(ref[rows]) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -15) * vmax).all(), (b, err.max() / vmax)
+        assert np.abs(lse.double().cpu().numpy()[:, rows] - ref_lse[:, rows]).max() <= TOL_LSE + 2.0 ** -15, b
