@@ -662,7 +662,8 @@ def _paged_outputs(q, Dv, lse_shape, out, lse, return_lse, stream):
 def sdpa_decode_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, *, scale: float | None = None,
                           out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
     """sdpa_decode_paged over a quantised cache: q [B,Hq,D] fp16/bf16, e4m3 pools [n_pages,page_size,Hkv,D|Dv],
-    scales [n_pages,Hkv,page_size] fp32.  Returns (o [B,Hq,Dv] in q's type, lse [B,Hq] fp32 or None)."""
+    scales [n_pages,Hkv,page_size] fp32.  Returns (o [B,Hq,Dv] in q's type, lse [B,Hq] fp32 or None).  The keys are
+    split for page_table's width: of a table much wider than the sequences need, pass the first columns."""
     n_pages, page_size, Hkv, D, Dv = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
     if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("q must be an fp16 or bf16 [B, Hq, D] tensor")

@@ -13,8 +13,8 @@
 // the rounding reaches 2^128, finite values read back as infinities too.
 //
 // Both kernels are bound by memory: 3 (D + Dv) + 8 bytes move per row of K and V against some 40
-// instructions per 8 values.  66,000 tokens of 8 heads of 128 are written in 72 us (5.7 TB/s: 271 MB read,
-// 135 MB of codes and 4 MB of scales written), 139,000 read back in 135 (6.4 TB/s).
+// instructions per 8 values.  66,000 tokens of 8 heads of 128 are written in 68 us (6.1 TB/s: 271 MB read,
+// 135 MB of codes and 4 MB of scales written), 139,000 read back in 131 (6.6 TB/s), both in a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,7 +30,7 @@ constexpr int kCacheThreads = 128;
 
 // The rows of K and V ((token, KV head), token major) are taken kLanes threads at a time, eight
 // values a thread; a block takes REPS passes of kCacheThreads / LANES rows.  4 x 128 threads wrote the
-// tokens above in 76 us, 2 x 256 in 82, 8 x 128 in 81; the scales' joint stores took 4 us off it.
+// tokens above in 76 us, 2 x 256 in 82, 8 x 128 in 81, all before the scales' joint stores, which took 4 us off.
 template <int D, int DV>
 struct CacheCfg {
   static constexpr int LANES = D > 128 ? 32 : D / 8;  // a power of two; 8 of the 32 idle for D = 192

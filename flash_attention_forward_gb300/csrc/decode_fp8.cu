@@ -14,8 +14,8 @@
 //     l = sum 2^(s_j - m) is the matching denominator.  P then stays in fp16's best range whatever
 //     the scales are, where a product P * v_scale could leave it.
 // Bound by memory: D + Dv + 8 bytes per row against 2 (D + Dv) flops per query head.  64 sequences of
-// 1024-16384 rows, 32 / 8 heads of 128, pages of 64: 196 us with the combine, 6.0 TB/s of codes and
-// scales; the same loads without the arithmetic take 194.  The products with keys and value dims in
+// 1024-16384 rows, 32 / 8 heads of 128, pages of 64: 193 us with the combine in a graph, 6.1 TB/s of codes
+// and scales; the same loads without the arithmetic took 194 when the whole took 196.  The products with keys and value dims in
 // the 16 rows of an MMA (below) brought it from 225: with heads there, half of each MMA, of the
 // accumulators and of the softmax's shuffles were for empty rows.
 #include <cuda_bf16.h>
@@ -417,7 +417,10 @@ cudaError_t launch_f8(int D, const DecodeParams& p, const CUtensorMap (&tm)[4], 
 
 // Keys per split: the largest of 2048 .. 256 that gives every SM of the card two CTAs (304), or
 // 256.  Longer splits write fewer partials and start fewer CTAs (the batch above: 4096 cost
-// 4 us more, 1024 14, 512 44); a few short sequences need more CTAs than that gives.
+// 4 us more, 1024 14, 512 44); a few short sequences need more CTAs than that gives.  The lengths are on the
+// device, so max_kv stands for them: a page table wider than they need gives longer splits than they would take, and
+// CTAs without keys (3 sequences of 3000 rows, 32 / 4 heads: 9 us with a tight table, 10 with one 8 times as wide,
+// 21 with one for 131072 rows; 64 sequences of 4000 rows, 32 / 8 heads: 101, 116, 145).
 int f8_log2_split(int B, int Hkv, int max_kv) {
   int log2 = 11;  // 2048
   while ((1 << log2) > kF8MinSplit &&

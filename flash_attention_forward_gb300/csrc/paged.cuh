@@ -16,9 +16,9 @@
 //     A unit whose keys a cut divides writes partials (unnormalised O, max, sum) that a second
 //     kernel merges.  The cuts are planned on the device, where the lengths are (paged_plan_kernel).
 // Bound by the tensor cores for long chunks and by memory for short ones.  32 / 8 heads of 128, pages of 64, bf16:
-// 8192 tokens over 32768 rows 2400 us in a short run (1.6 PFLOP/s) and 2700 under the power cap, drafts of 3-8
-// tokens of 16 sequences of 1024-16384 rows 103 us (5.5 TB/s); over e4m3 pages 4 x 2048 tokens of 16384 rows
-// 1530 us (1.35 PFLOP/s), the drafts 89 us (3.3 TB/s).
+// 8192 tokens over 32768 rows 2375-2490 us in a short run (1.55-1.6 PFLOP/s) and 2670-2730 under the power cap, drafts
+// of 3-8 tokens of 16 sequences of 1024-16384 rows 102 us (5.6 TB/s); over e4m3 pages 4 x 2048 tokens of 16384 rows
+// 1526 us (1.35 PFLOP/s), the drafts 88 us (3.4 TB/s).
 // K and V blocks have a ring each and are loaded in the order of their use: K(0), then K(j) and V(j-1)
 // for each j, then the last V.  A slot is so held for little longer than its MMAs take, and the rest of
 // the rings is loads in flight.
@@ -55,8 +55,11 @@ constexpr float kMinBlkScale2 = 1.1754944e-38f;  // a factor of 0 would turn mas
 constexpr int kFixRing = 8;         // v_ragged barriers: more than the ring holds blocks
 constexpr int kExpRing = 8;         // blocks whose exponents are kept: more than the ring can run ahead
 
-// ONE: no sequence has more tokens than one query tile holds (drafts of 16 sequences: 109 us over 16-bit pages and
-// 94 over e4m3 ones, 114 and 118 by the other form).  Shared memory then keeps one query tile,
+// ONE: no sequence has more tokens than one query tile holds.  In a graph, by this form and by the other, us over
+// 16-bit and over e4m3 pages (32 / 8 heads of 128): drafts of 16 sequences of 1024-16384 rows 102 / 107 and 88 / 111, full
+// tiles there (32 tokens) 107 / 110 and 97 / 119, full tiles of one head (8 / 8 heads, 128 tokens of 16384 rows)
+// 184 / 188 and 155 / 202, 64 sequences of one key block 21.0 / 21.4 and 26 / 27, of two 23 / 26 and 30 / 35, 200 of 512-1024
+// rows 121 / 130 and 173 / 190.  Shared memory then keeps one query tile,
 // the two accumulators take the even and the odd key blocks ("readers" 0 and 1, each with half of the
 // rings), so that one's softmax runs beside the other's MMAs, and slot 0's warps merge the two at the
 // end of a piece.  Otherwise accumulator t serves query tile t and both read every block.
@@ -241,7 +244,9 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 
 // The plan where every sequence has one query tile, by each CTA for itself: a scan over the sequences'
 // lengths on the line, then this CTA's two cuts; CTA 0 stores all of them and the cut units for the merge.
-// Spares the launch of a planning kernel and the wait for it (112 -> 108 us for the drafts of 16 sequences).
+// Spares the launch of a planning kernel and the wait for it (in a graph, 16-bit and e4m3 pages: drafts of 16 sequences
+// 104.5 -> 101.7 us and 89.1 -> 87.9, 64 sequences of one key block 22.7 -> 21.0 and 28.0 -> 26.3, 200 of 512-1024 rows
+// 123 -> 122 and 174 -> 173).
 // scratch: 8 KB of shared memory that nobody uses yet.  All threads; returns the cuts in `mine`.
 template <int THREADS>
 __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine) {

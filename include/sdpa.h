@@ -376,7 +376,9 @@ int sdpa_cache_read_fp8(const void* k_pool, const void* v_pool, const float* k_s
 /*
  * sdpa_decode_paged_fp8_workspace_size -- bytes of device scratch sdpa_decode_paged_fp8 needs
  * (per-split partial results; max_kv = max_pages * page_size).  Splits hold 2048 keys, or fewer
- * (down to 256) where B * Hkv * splits would leave SMs idle.  0 for bad sizes.
+ * (down to 256) where B * Hkv * splits would leave SMs idle, splits being counted for max_kv.  A page table
+ * much wider than the sequences need makes the call slower: pass its first columns (max_pages of them, the
+ * row stride as it is).  0 for bad sizes.
  */
 size_t sdpa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int max_kv, int Dv);
 
