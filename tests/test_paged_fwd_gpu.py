@@ -520,3 +520,53 @@ def test_scales_at_the_ends_of_their_range(new, exps):
         err = np.abs(o.double().cpu().numpy()[rows] - ref[rows])
         assert (err <= 2.0 ** -8 * np.abs(ref[rows]) + (2.0 ** -11 + 2.0 ** -14 + 2.0 ** -15) * vmax).all(), (b, err.max() / vmax)
         assert np.abs(lse.double().cpu().numpy()[:, rows] - ref_lse[:, rows]).max() <= TOL_LSE + 2.0 ** -15, b
+
+
+def test_pages_behind_two_to_the_32_bytes():
+    # the same rows in pages at the front of a small cache and at the end of pools of 4.4 GB: the same results, bit for bit
+    g = torch.Generator().manual_seed(61)
+    Hq, Hkv, D, page, dt = 8, 8, 128, 64, torch.bfloat16
+    new, lens = [5, 70, 1], [300, 450, 64]
+    n_small, n_big = 20, (1 << 32) // (page * Hkv * D) + 2000
+    total = sum(lens)
+    k, v = (torch.randn((total, Hkv, D), generator=g).to(dt).to(DEV) for _ in range(2))
+    q = torch.randn((sum(new), Hq, D), generator=g).to(dt).to(DEV)
+    kv = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    cu_k, cu_q = (torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32, device=DEV) for x in (lens, new))
+    ids = torch.randperm(n_small, generator=g)[:18].to(torch.int32)
+    got = []
+    for n, off in ((n_small, 0), (n_big, n_big - n_small)):
+        assert off == 0 or (off * page * Hkv * D) >= 1 << 32
+        kp, vp = (torch.empty((n, page, Hkv, D), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2))
+        ks, vs = (torch.empty((n, Hkv, page), device=DEV) for _ in range(2))
+        table = torch.full((3, 8), -1, dtype=torch.int32)
+        at = 0
+        for b, L in enumerate(lens):
+            m = (L + page - 1) // page
+            table[b, :m] = ids[at:at + m] + off
+            at += m
+        table = table.to(DEV)
+        fa.sdpa_cache_write_fp8(k, v, kp, vp, ks, vs, table, kv, cu_k)
+        out = [*fa.sdpa_cache_read_fp8(kp, vp, ks, vs, table, cu_k, total),
+               *fa.sdpa_decode_paged_fp8(q[:3], kp, vp, ks, vs, table, kv),
+               *fa.sdpa_fwd_paged_fp8(q, kp, vp, ks, vs, table, kv, cu_q, 70, causal=True)]
+        del kp, vp, ks, vs
+        # 16-bit pools of half as many pages: as many bytes
+        n16, off16 = (n, 0) if off == 0 else (n // 2, n // 2 - n_small)
+        pools = [torch.empty((n16, page, Hkv, D), dtype=dt, device=DEV) for _ in range(2)]
+        table = torch.where(table >= 0, table - off + off16, table)
+        for pool, x in zip(pools, (k, v)):
+            at = 0
+            for b, L in enumerate(lens):
+                for i in range(0, L, page):
+                    m = min(page, L - i)
+                    pool[table[b, i // page].long(), :m] = x[at + i:at + i + m]
+                at += L
+        out += fa.sdpa_fwd_paged(q, *pools, table, kv, cu_q, 70, causal=True)
+        torch.cuda.synchronize()
+        assert fa.sdpa_check_device_status() == fa.SDPA_OK
+        got.append(out)
+        del pools
+        torch.cuda.empty_cache()
+    for a, b in zip(*got):
+        assert torch.isfinite(a).all() and torch.equal(a, b)
