@@ -15,9 +15,9 @@
 //     the scales are, where a product P * v_scale could leave it.
 // Bound by memory: D + Dv + 8 bytes per row against 2 (D + Dv) flops per query head.  64 sequences of
 // 1024-16384 rows, 32 / 8 heads of 128, pages of 64: 193 us with the combine in a graph, 6.1 TB/s of codes
-// and scales; the same loads without the arithmetic took 194 when the whole took 196.  The products with keys and value dims in
-// the 16 rows of an MMA (below) brought it from 225: with heads there, half of each MMA, of the
-// accumulators and of the softmax's shuffles were for empty rows.
+// and scales; the same loads without the arithmetic took 194 when the whole took 196.  The products with
+// keys and value dims in the 16 rows of an MMA (below) brought it from 225: with heads there, half of each
+// MMA, of the accumulators and of the softmax's shuffles were for empty rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <algorithm>

@@ -324,8 +324,8 @@ int sdpa_decode_paged(const void* q, const void* k_pool, const void* v_pool, con
  * kernel reads those of a block of keys as one run.  The readers take any scales that are positive
  * and finite; the attention calls take V's from 2^-80 to 2^80, which are those that sdpa_cache_write_fp8
  * writes for |V| <= 448 * 2^80 (their row sums are held relative to the largest probability times V's
- * scale, and further out they would leave fp32).  page_size: a power of two >= 16.  Pool strides: multiples of 16 elements; pools and
- * scales 16-byte aligned.  Head dims: (D, Dv) in {(64, 64), (128, 128), (192, 128)} unless said otherwise.
+ * scale, and further out they would leave fp32).  page_size: a power of two >= 16.  Pool strides:
+ * multiples of 16 elements; pools and scales 16-byte aligned.  Head dims: (D, Dv) in {(64, 64), (128, 128), (192, 128)} unless said otherwise.
  */
 
 /*
