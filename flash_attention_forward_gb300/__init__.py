@@ -25,9 +25,17 @@ Entry points (same names as the C ABI):
                                                 a chunk of new tokens per sequence over a paged cache
     sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens_q,
                        max_seqlen_q, ...)       the same over a quantised cache
+    sdpa_cache_resize(page_table, kv_len, change, free_pages, n_free, page_size, total, ...)
+                                                pages given back and taken, positions and slots of new tokens
+    sdpa_rope(q, k, positions, inv_freq, ...)   rotary positions (frequencies: sdpa_rope_frequencies)
+    sdpa_latent_write(c, k_rope, pool, slots, positions, inv_freq, ...)   new tokens' rows into a latent cache
+    sdpa_fwd_latent_paged(q, pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q, ...)
+                                                latent attention, absorbed: over a latent cache's pages
+    sdpa_fwd_latent(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, ...)
+                                                latent attention, expanded: packed keys with one shared rotary part
     sdpa_fwd_workspace_size, sdpa_fwd_varlen_workspace_size, sdpa_fwd_int8_workspace_size,
-    sdpa_fwd_host_workspace_size,
-    sdpa_decode_workspace_size, sdpa_decode_paged_fp8_workspace_size, sdpa_fwd_paged_workspace_size,
+    sdpa_fwd_host_workspace_size, sdpa_cache_resize_workspace_size, sdpa_fwd_latent_paged_workspace_size,
+    sdpa_fwd_latent_workspace_size, sdpa_decode_workspace_size, sdpa_decode_paged_fp8_workspace_size, sdpa_fwd_paged_workspace_size,
     sdpa_check_device_status,
     sdpa_status_string, sdpa_version
 """
@@ -111,6 +119,22 @@ def _load():
         lib.sdpa_fwd_paged.restype = i
         lib.sdpa_fwd_paged_fp8.argtypes = [p] * 10 + [i] * 10 + [p, f, i, p, sz, i, p]
         lib.sdpa_fwd_paged_fp8.restype = i
+        lib.sdpa_cache_resize_workspace_size.argtypes = [i]
+        lib.sdpa_cache_resize_workspace_size.restype = sz
+        lib.sdpa_cache_resize.argtypes = [p] * 10 + [i] * 5 + [i64, p, sz, p]
+        lib.sdpa_cache_resize.restype = i
+        lib.sdpa_rope.argtypes = [p] * 6 + [i] * 6 + [f, p, i, p]
+        lib.sdpa_rope.restype = i
+        lib.sdpa_latent_write.argtypes = [p] * 6 + [i] * 6 + [f, p, i, p]
+        lib.sdpa_latent_write.restype = i
+        lib.sdpa_fwd_latent_paged_workspace_size.argtypes = [i] * 5
+        lib.sdpa_fwd_latent_paged_workspace_size.restype = sz
+        lib.sdpa_fwd_latent_paged.argtypes = [p] * 7 + [i] * 9 + [p, f, i, p, sz, i, p]
+        lib.sdpa_fwd_latent_paged.restype = i
+        lib.sdpa_fwd_latent_workspace_size.argtypes = [i] * 6
+        lib.sdpa_fwd_latent_workspace_size.restype = sz
+        lib.sdpa_fwd_latent.argtypes = [p] * 8 + [i] * 9 + [p, f, i, p, sz, i, p]
+        lib.sdpa_fwd_latent.restype = i
         lib.sdpa_check_device_status.argtypes = [p]
         lib.sdpa_check_device_status.restype = i
         lib.sdpa_status_string.argtypes = [i]
@@ -761,3 +785,266 @@ def sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, 
     sizes = _check_fp8_pools(k_pool, v_pool, k_scale, v_scale)
     return _fwd_paged("sdpa_fwd_paged_fp8", q, (k_pool, v_pool, k_scale, v_scale), sizes, page_table, kv_len,
                       cu_seqlens_q, max_seqlen_q, scale, causal, out, lse, return_lse, workspace, stream)
+
+
+def sdpa_cache_resize_workspace_size(B: int) -> int:
+    """Bytes of workspace for sdpa_cache_resize."""
+    return _load().sdpa_cache_resize_workspace_size(B)
+
+
+def sdpa_cache_resize(page_table, kv_len, change, free_pages, n_free, page_size: int, total: int, *, kv_len_out=None,
+                      n_free_out=None, cu_seqlens=None, positions=None, slots=None, workspace=None, stream=None):
+    """Change every sequence's length: kv_len int32 [B] by change int32 [B] (new tokens, or rows dropped from the
+    end).  Pages come from and go to the stack free_pages int32 [n_pages], n_free int32 [1]; page_table int32
+    [B, max_pages] is updated in place.  Returns (kv_len_out [B], n_free_out [1], cu_seqlens [B+1], positions [total] int32,
+    slots [total] int64) of the new tokens, at most ``total``; pass kv_len_out=kv_len and n_free_out=n_free to update
+    those in place.  A change that cannot be made whole changes nothing (see sdpa_check_device_status)."""
+    _int32_vector("kv_len", kv_len)
+    B, total = kv_len.shape[0], int(total)
+    _int32_vector("change", change, B)
+    _int32_vector("free_pages", free_pages)
+    _int32_vector("n_free", n_free, 1)
+    _check_page_table(B, page_table)
+    device = kv_len.device
+    if kv_len_out is None:
+        kv_len_out = _empty((B,), torch.int32, device, stream)
+    if n_free_out is None:
+        n_free_out = _empty((1,), torch.int32, device, stream)
+    if cu_seqlens is None:
+        cu_seqlens = _empty((B + 1,), torch.int32, device, stream)
+    if positions is None:
+        positions = _empty((total,), torch.int32, device, stream)
+    if slots is None:
+        slots = _empty((total,), torch.int64, device, stream)
+    elif slots.dtype != torch.int64 or slots.shape != (total,):
+        raise ValueError(f"slots must be an int64 vector of {total} entries")
+    _int32_vector("kv_len_out", kv_len_out, B)
+    _int32_vector("n_free_out", n_free_out, 1)
+    _int32_vector("cu_seqlens", cu_seqlens, B + 1)
+    _int32_vector("positions", positions, total)
+    lib = _load()
+    if workspace is None:
+        workspace = _empty((lib.sdpa_cache_resize_workspace_size(B),), torch.uint8, device, stream)
+    names = ("page_table", "kv_len", "change", "free_pages", "n_free", "kv_len_out", "n_free_out", "cu_seqlens", "positions",
+             "slots", "workspace")
+    tensors = (page_table, kv_len, change, free_pages, n_free, kv_len_out, n_free_out, cu_seqlens, positions, slots, workspace)
+    dev = _current_device(names, tensors)
+    _unit_vectors(names[1:], tensors[1:])
+    if not page_table.is_contiguous():
+        _on_device(page_table=page_table)
+    rc = lib.sdpa_cache_resize(*(t.data_ptr() for t in tensors[:-1]), B, total, int(page_size), page_table.shape[1],
+                               free_pages.shape[0], page_table.stride(0), workspace.data_ptr(), workspace.nbytes,
+                               _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_cache_resize", rc)
+    return kv_len_out, n_free_out, cu_seqlens, positions, slots
+
+
+def sdpa_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                          original_length: int = 0, fast_turns: float = 32.0, slow_turns: float = 1.0):
+    """(inv_freq fp32 [rotary_dim / 2] on the CPU, factor for sdpa_rope): base^(-2 i / rotary_dim) radians a position,
+    for a context ``factor`` times longer changed by
+
+    "linear"    all divided by factor: positions are interpolated;
+    "base"      the base raised to base * factor^(rotary_dim / (rotary_dim - 2)), so that the first pair keeps its
+                frequency and the last one is divided by factor;
+    "by_parts"  pairs that turn fast_turns times or more within original_length positions keep their frequency, those
+                that turn slow_turns times or fewer are divided by factor, those between are blended linearly in the
+                index of the pair; the turned dims are multiplied by 0.1 ln(factor) + 1."""
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 1.0 or not factor >= 1.0:
+        raise ValueError("rotary_dim must be even and positive, base above 1, factor at least 1")
+    half = torch.arange(rotary_dim // 2, dtype=torch.float64)
+    if scaling not in (None, "linear", "base", "by_parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling by the base needs two pairs or more")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    inv_freq = base ** (-2.0 * half / rotary_dim)
+    attention = 1.0
+    if scaling == "linear":
+        inv_freq = inv_freq / factor
+    elif scaling == "by_parts":
+        if original_length < 1 or not fast_turns > slow_turns > 0:
+            raise ValueError("by_parts needs original_length and fast_turns > slow_turns > 0")
+
+        def pair(turns):  # index of the pair that turns so often
+            return rotary_dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
+
+        lo, hi = max(math.floor(pair(fast_turns)), 0), min(math.ceil(pair(slow_turns)), rotary_dim - 1)
+        stretch = ((half - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        inv_freq = inv_freq * (1 - stretch + stretch / factor)
+        attention = 0.1 * math.log(factor) + 1.0
+    return inv_freq.float(), attention
+
+
+def _check_rope(name, inv_freq, positions, total):
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be an fp32 vector, one entry a pair")
+    _int32_vector("positions", positions, total)
+
+
+def sdpa_rope(q, k, positions, inv_freq, *, interleaved: bool = False, factor: float = 1.0, q_out=None, k_out=None,
+              stream=None):
+    """Rotary positions on q [total,Hq,D] and k [total,Hk,D] (fp16/bf16; k may be None): the first 2 * len(inv_freq)
+    dims of every head are turned by positions int32 [total] * inv_freq fp32, the others copied.  Pair i is dims i and
+    i + len(inv_freq), or with ``interleaved`` 2 i and 2 i + 1.  To turn another part of the head pass views of it.
+    Returns (q_out, k_out), in place where q_out is q.  The gradient is the same call with -positions."""
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be an fp16 or bf16 [total, Hq, D] tensor")
+    total, Hq, D = q.shape
+    if k is not None and (k.dim() != 3 or k.dtype != q.dtype or k.shape[0] != total or k.shape[2] != D):
+        raise ValueError("k must be [total, Hk, D] of q's type, tokens and head dim")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    _check_rope("sdpa_rope", inv_freq, positions, total)
+    for t, o, name in ((q, q_out, "q_out"), (k, k_out, "k_out")):
+        if o is not None and (o.shape != t.shape or o.dtype != t.dtype):
+            raise ValueError(f"{name} must have the shape and type of its input")
+    if q_out is None:
+        q_out = _empty(q.shape, q.dtype, q.device, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(k.shape, k.dtype, k.device, stream)
+    names, tensors = ("q", "q_out", "positions", "inv_freq", "k", "k_out"), (q, q_out, positions, inv_freq, k, k_out)
+    dev = _current_device(names, tensors)
+    _unit_vectors(names[2:4], tensors[2:4])
+    if k is None:
+        strides = _strides(("q", "q_out"), (q, q_out), (2, 2))
+        if strides is not None:
+            strides = _stride_array((*q.stride()[:2], 0, 0, *q_out.stride()[:2], 0, 0))
+    else:
+        strides = _strides(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), (2, 2, 2, 2))
+    rc = _load().sdpa_rope(q.data_ptr(), None if k is None else k.data_ptr(), q_out.data_ptr(),
+                           None if k is None else k_out.data_ptr(), positions.data_ptr(), inv_freq.data_ptr(), total, Hq,
+                           0 if k is None else k.shape[1], D, 2 * inv_freq.shape[0], int(bool(interleaved)), float(factor),
+                           strides, _DT[q.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_rope", rc)
+    return q_out, k_out
+
+
+def _check_latent_pool(pool):
+    if pool.dim() != 3 or pool.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("pool must be an fp16 or bf16 [n_pages, page_size, latent_dim + rotary_dim] tensor")
+    return pool.shape
+
+
+def sdpa_latent_write(c, k_rope, pool, slots, positions=None, inv_freq=None, *, interleaved: bool = False,
+                      factor: float = 1.0, stream=None):
+    """Store new tokens' rows into a latent cache: row slots[t] (int64 [total], page * page_size + row; negative:
+    skipped) of pool [n_pages,page_size,512+64] becomes c[t] [total,512] and behind it k_rope[t] [total,64] turned as
+    in sdpa_rope, or as it is without positions and inv_freq.  Writes in place."""
+    n_pages, page_size, width = _check_latent_pool(pool)
+    if c.dim() != 2 or k_rope.dim() != 2 or c.shape[0] != k_rope.shape[0]:
+        raise ValueError("c and k_rope must be [total, latent_dim] and [total, rotary_dim]")
+    if c.dtype != pool.dtype or k_rope.dtype != pool.dtype or c.shape[1] + k_rope.shape[1] != width:
+        raise ValueError("c, k_rope and the pool must share one dtype, and a row be as wide as c and k_rope together")
+    total = c.shape[0]
+    if slots.dtype != torch.int64 or slots.shape != (total,):
+        raise ValueError(f"slots must be an int64 vector of {total} entries")
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    if inv_freq is not None:
+        _check_rope("sdpa_latent_write", inv_freq, positions, total)
+        if 2 * inv_freq.shape[0] != k_rope.shape[1]:
+            raise ValueError("inv_freq must have one entry for each pair of k_rope")
+    names = ("c", "k_rope", "pool", "slots", "positions", "inv_freq")
+    tensors = (c, k_rope, pool, slots, positions, inv_freq)
+    dev = _current_device(names, tensors)
+    _unit_vectors(names[3:], [t for t in tensors[3:] if t is not None])
+    strides = _strides(names[:3], tensors[:3], (1, 1, 2))
+    rc = _load().sdpa_latent_write(*(None if t is None else t.data_ptr() for t in tensors), total, page_size, n_pages,
+                                   c.shape[1], k_rope.shape[1], int(bool(interleaved)), float(factor), strides,
+                                   _DT[c.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_latent_write", rc)
+
+
+def sdpa_fwd_latent_workspace_size(B: int, Hq: int, Hkv: int, total_q: int, max_seqlen_q: int, total_k: int) -> int:
+    """Bytes of workspace for sdpa_fwd_latent: the work plan (required), then partial results of cut key ranges
+    (optional)."""
+    return _load().sdpa_fwd_latent_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, total_k)
+
+
+def sdpa_fwd_latent(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, *, scale: float | None = None,
+                    causal: bool = False, out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """Latent attention, expanded form, over packed sequences: q [total_q,Hq,128+64], k_nope [total_k,Hkv,128], the
+    rotary part of the keys k_rope [total_k,64] one for all heads, v [total_k,Hkv,128] (fp16/bf16; k_nope and v may be
+    views of one expanded tensor), offsets int32 [B+1], at most max_seqlen_q queries each.  The queries of a sequence are
+    the last of its positions; causal masking is bottom-right.  Returns (o [total_q,Hq,128], lse [Hq,total_q] fp32 or
+    None)."""
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be a packed fp16 or bf16 [total_q, Hq, D] tensor")
+    if k_nope.dim() != 3 or v.dim() != 3 or k_rope.dim() != 2 or not k_nope.shape[0] == v.shape[0] == k_rope.shape[0]:
+        raise ValueError("k_nope, v and k_rope must be packed [total_k, Hkv, nope], [total_k, Hkv, Dv] and [total_k, rotary_dim]")
+    if k_nope.dtype != q.dtype or k_rope.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k_nope, k_rope and v must share one dtype")
+    total_q, Hq, D = q.shape
+    total_k, Hkv, nope = k_nope.shape
+    rot, Dv = k_rope.shape[1], v.shape[2]
+    if nope + rot != D or v.shape[1] != Hkv:
+        raise ValueError("q's head dim must be that of k_nope and k_rope together, and v have k_nope's heads")
+    _int32_vector("cu_seqlens_q", cu_seqlens_q)
+    B = cu_seqlens_q.shape[0] - 1
+    _int32_vector("cu_seqlens_k", cu_seqlens_k, B + 1)
+    max_seqlen_q = int(max_seqlen_q)
+    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
+    out, lse = _paged_outputs(q, Dv, (Hq, total_q), out, lse, return_lse, stream)
+    lib = _load()
+    if workspace is None:
+        need = lib.sdpa_fwd_latent_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, total_k)
+        workspace = _empty(max(16, need), torch.uint8, q.device, stream)
+    names = ("q", "k_nope", "k_rope", "v", "out", "cu_seqlens_q", "cu_seqlens_k", "workspace", "lse")
+    tensors = (q, k_nope, k_rope, v, out, cu_seqlens_q, cu_seqlens_k, workspace, lse)
+    dev = _current_device(names, tensors)
+    _unit_vectors(names[5:8], tensors[5:8])
+    strides = _strides(names[:5], tensors[:5], (2, 2, 1, 2, 2))
+    rc = lib.sdpa_fwd_latent(
+        q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+        out.data_ptr(), None if lse is None else lse.data_ptr(), B, Hq, Hkv, total_q, total_k, max_seqlen_q, nope, rot, Dv,
+        strides, scale, int(bool(causal)), workspace.data_ptr(), workspace.nbytes, _DT[q.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_fwd_latent", rc)
+    return out, lse
+
+
+def sdpa_fwd_latent_paged_workspace_size(B: int, Hq: int, total_q: int, max_seqlen_q: int, max_kv: int) -> int:
+    """Bytes of workspace for sdpa_fwd_latent_paged (max_kv = max_pages * page_size): the work plan (required), then
+    partial results of cut key ranges (optional)."""
+    return _load().sdpa_fwd_latent_paged_workspace_size(B, Hq, total_q, max_seqlen_q, max_kv)
+
+
+def sdpa_fwd_latent_paged(q, pool, page_table, kv_len, cu_seqlens_q, max_seqlen_q: int, *, scale: float,
+                          causal: bool = False, out=None, lse=None, return_lse: bool = True, workspace=None, stream=None):
+    """Latent attention, absorbed form, over a latent cache that holds the new tokens: q [total_q,Hq,512+64] (fp16/bf16,
+    packed, offsets cu_seqlens_q int32 [B+1], at most max_seqlen_q tokens each; one each is a decode step), pool
+    [n_pages,page_size,512+64], page_table int32 [B,max_pages], kv_len int32 [B] counting the new tokens.  A row is key of
+    every head and its first 512 values are their value.  ``scale`` is that of the heads before the absorption
+    (customarily 1 / sqrt(nope + 64)).  Causal masking is bottom-right.  Returns (o [total_q,Hq,512], lse [Hq,total_q] fp32
+    or None)."""
+    n_pages, page_size, width = _check_latent_pool(pool)
+    if q.dim() != 3 or q.dtype != pool.dtype or q.shape[2] != width:
+        raise ValueError("q must be a packed [total_q, Hq, latent_dim + rotary_dim] tensor of the pool's type and width")
+    total_q, Hq = q.shape[:2]
+    _int32_vector("kv_len", kv_len)
+    B = kv_len.shape[0]
+    _int32_vector("cu_seqlens_q", cu_seqlens_q, B + 1)
+    _check_page_table(B, page_table)
+    max_pages, max_seqlen_q, scale = page_table.shape[1], int(max_seqlen_q), float(scale)
+    out, lse = _paged_outputs(q, width - 64, (Hq, total_q), out, lse, return_lse, stream)
+    lib = _load()
+    if workspace is None:
+        need = lib.sdpa_fwd_latent_paged_workspace_size(B, Hq, total_q, max_seqlen_q, max_pages * page_size)
+        workspace = _empty(max(16, need), torch.uint8, q.device, stream)
+    names = ("q", "pool", "out", "page_table", "kv_len", "cu_seqlens_q", "workspace", "lse")
+    tensors = (q, pool, out, page_table, kv_len, cu_seqlens_q, workspace, lse)
+    dev = _current_device(names, tensors)
+    _unit_vectors(names[4:7], tensors[4:7])
+    strides = _strides(names[:4], tensors[:4], (2, 2, 2, 1))
+    rc = lib.sdpa_fwd_latent_paged(
+        q.data_ptr(), pool.data_ptr(), page_table.data_ptr(), kv_len.data_ptr(), cu_seqlens_q.data_ptr(), out.data_ptr(),
+        None if lse is None else lse.data_ptr(), B, Hq, total_q, max_seqlen_q, page_size, max_pages, n_pages, width - 64, 64,
+        strides, scale, int(bool(causal)), workspace.data_ptr(), workspace.nbytes, _DT[q.dtype], _raw_stream(stream, dev))
+    if rc:
+        raise SdpaError("sdpa_fwd_latent_paged", rc)
+    return out, lse

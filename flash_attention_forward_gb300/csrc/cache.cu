@@ -15,12 +15,10 @@
 // Both kernels are bound by memory: 3 (D + Dv) + 8 bytes move per row of K and V against some 40
 // instructions per 8 values.  66,000 tokens of 8 heads of 128 are written in 68 us (6.1 TB/s: 271 MB read,
 // 135 MB of codes and 4 MB of scales written), 139,000 read back in 131 (6.6 TB/s), both in a graph.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "sdpa.h"
 #include "internal.h"
 #include "ptx.cuh"
+#include "rows16.cuh"
 
 namespace sdpa {
 
@@ -82,20 +80,6 @@ __device__ __forceinline__ void block_slots(const CacheParams& p, int row0, int 
     slots[i] = s;
   }
   __syncthreads();
-}
-
-template <bool BF16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if constexpr (BF16) {
-      x[2 * i] = bf16lo_f32(w[i]), x[2 * i + 1] = bf16hi_f32(w[i]);
-    } else {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      x[2 * i] = f.x, x[2 * i + 1] = f.y;
-    }
-  }
 }
 
 // Exponent k of the row's scale from its largest magnitude m * 2^e (1 <= m < 2): 448 = 1.75 * 2^8.

@@ -188,6 +188,11 @@ struct CacheParams {
   FastDiv div_h;           // by Hkv
 };
 
+// Latent caches: a row is a token's latent vector, key and value of every head, and the rotary part of its keys.
+constexpr int kLatentDim = 512;
+constexpr int kLatentRot = 64;
+constexpr int kLatentRow = kLatentDim + kLatentRot;
+
 struct MaskConvertParams {
   const uint16_t* mask;
   int64_t mask_b, mask_i;

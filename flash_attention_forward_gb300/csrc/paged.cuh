@@ -125,18 +125,12 @@ struct PagedPiece {
   int n_s[2];              // blocks that each accumulator takes: those its tile sees, or the even and the odd ones
   int slot;                // partial slot, or -1: the whole unit, which stores O itself
   int q_off, n, len, sk;
-  int pad[4];
+  int k_off;               // packed keys: the sequence's first row
+  int pad[3];
 };
 static_assert(sizeof(PagedPiece) == 64, "the producer announces a piece in 64 bytes");
 
-// Loads of the walk; the host, where tests replay it, has neither form.
-__host__ __device__ __forceinline__ int walk_ld(const int32_t* p) {
-#ifdef __CUDA_ARCH__
-  return __ldg(p);
-#else
-  return *p;
-#endif
-}
+// The tiles of the plan; the host, where tests replay the walk, reads them plainly.
 __host__ __device__ __forceinline__ int2 walk_ld(const int2* p) {
 #ifdef __CUDA_ARCH__
   return ld_dep(p);
@@ -158,14 +152,15 @@ struct PagedWalk {
     PagedPiece w{};
     // planned by this kernel, tiles are sequences, and those without tokens are passed over
     if (ONE && p.inline_plan)
-      while (tile < end.x && walk_ld(p.cu_q + tile) == walk_ld(p.cu_q + tile + 1)) ++tile;
+      while (tile < end.x && plan_ld(p.cu_q + tile) == plan_ld(p.cu_q + tile + 1)) ++tile;
     if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
     const int2 at = ONE && p.inline_plan ? make_int2(tile, 0) : walk_ld(p.plan.tiles + tile);
     w.b = at.x;
     w.kvh = kvh;
-    w.q_off = walk_ld(p.cu_q + w.b);
-    w.n = walk_ld(p.cu_q + w.b + 1) - w.q_off;
-    w.len = walk_ld(p.kv_len + w.b);
+    w.q_off = plan_ld(p.cu_q + w.b);
+    w.n = plan_ld(p.cu_q + w.b + 1) - w.q_off;
+    w.len = paged_len(p, w.b);
+    w.k_off = p.cu_k != nullptr ? plan_ld(p.cu_k + w.b) : 0;
     w.sk = min(max(w.len, 0), p.max_kv);
     w.tok0 = at.y * kTilesPerCta * p.tok_tile;
     w.jb0 = off;
@@ -243,13 +238,14 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 // The plan where every sequence has one query tile, by each CTA for itself: a scan over the sequences'
-// lengths on the line, then this CTA's two cuts; CTA 0 stores all of them and the cut units for the merge.
+// lengths on the line, then this CTA's two cuts; one CTA stores all of them and the cut units for the merge.
 // Spares the launch of a planning kernel and the wait for it (in a graph, 16-bit and e4m3 pages: drafts of 16 sequences
 // 104.5 -> 101.7 us and 89.1 -> 87.9, 64 sequences of one key block 22.7 -> 21.0 and 28.0 -> 26.3, 200 of 512-1024 rows
 // 123 -> 122 and 174 -> 173).
 // scratch: 8 KB of shared memory that nobody uses yet.  All threads; returns the cuts in `mine`.
+// cta: the stretch that this block takes; store: it stores the plan.
 template <int THREADS>
-__device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine) {
+__device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine, int cta, bool store) {
   static_assert(THREADS >= kInlinePlanSeqs && THREADS > kPagedMaxCtas, "one thread per sequence and per cut");
   long long* pos = reinterpret_cast<long long*>(scratch);               // [kInlinePlanSeqs + 1]
   long long* warp_sum = pos + kInlinePlanSeqs + 1;                       // [THREADS / 32]
@@ -260,8 +256,8 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   long long v = 0;
   if (tid < p.B) {
     const int q0 = __ldg(p.cu_q + tid), q1 = __ldg(p.cu_q + tid + 1);
-    len = __ldg(p.kv_len + tid);
-    bad = q0 < 0 || q1 < q0 || q1 > p.total_q || static_cast<long long>(q1) - q0 > p.max_seqlen_q;
+    len = paged_len(p, tid);
+    bad = paged_bad(p, tid, q0, q1);
     n = q1 - q0;
     if (!bad && n > 0)
       v = static_cast<long long>(paged_tile_blocks(n, len, min(max(len, 0), p.max_kv), p.tok_tile, p.causal, 0) + kUnitCost) *
@@ -283,7 +279,6 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   __syncthreads();
   const long long total = pos[p.B];
   const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / kMinWork)));
-  const int cta = blockIdx.x;
   auto cut_at = [&](int c) { return bad ? make_int4(0, 0, 0, 0) : paged_inline_cut(p, pos, c, n_ctas); };
   if (cta < n_ctas) {
     if (tid == 0) mine[0] = cut_at(cta);
@@ -291,13 +286,13 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   } else if (tid == 0) {
     mine[0] = mine[1] = make_int4(0, 0, 0, 0);
   }
-  if (cta == 0) {  // for the merge
+  if (store) {  // for the merge
     if (tid <= n_ctas) p.plan.cuts[tid] = cuts[tid] = cut_at(tid);
     __syncthreads();
     if (tid < n_ctas && cuts[tid].z != 0) {
       const int b = cuts[tid].x, q0 = __ldg(p.cu_q + b);
       PagedGroup g;
-      if (paged_group(cuts, tid, n_ctas, make_int2(b, 0), q0, __ldg(p.cu_q + b + 1) - q0, __ldg(p.kv_len + b), g))
+      if (paged_group(cuts, tid, n_ctas, make_int2(b, 0), q0, __ldg(p.cu_q + b + 1) - q0, paged_len(p, b), g))
         p.plan.groups[atomicAdd(n_groups, 1)] = g;
     }
     __syncthreads();
@@ -327,10 +322,14 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
 //                           then zeroes those rows and completes kv_full in the copy's place
 //   s_full[t], p_half[t], p_full[t], o_full[t], o_empty[t]: as in the prefill kernels, per accumulator
 //   ml_full               : ONE: accumulator 1's max and sum are there
-template <bool BF16, bool QUANT, int D, int DV, bool ONE>
+//
+// PACKED: keys and values are packed rows instead of pages, and the last 64 columns of the keys come from a tensor of
+// their own without heads (tm_r; unused otherwise).  Only the loads differ: a block is one box of 128 rows a column chunk.
+template <bool BF16, bool QUANT, int D, int DV, bool ONE, bool PACKED>
 __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const PagedParams p) {
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r, const PagedParams p) {
+  static_assert(!(PACKED && QUANT), "packed keys are 16 bits wide");
   using C = PagedCfg<QUANT, D, DV, ONE>;
   constexpr int KS = C::KS, VS = C::VS, KR = C::KR, VR = C::VR;
   constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
@@ -421,7 +420,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   int4 cuts[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (ONE && p.inline_plan) {
     int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // not announced before the producer has read it
-    paged_inline_plan<C::THREADS>(p, sQ, mine);
+    paged_inline_plan<C::THREADS>(p, sQ, mine, blockIdx.x, blockIdx.x == 0);
     if (warp == 0) cuts[0] = mine[0], cuts[1] = mine[1];
   } else {
     pdl_wait();  // the plan comes from the kernel launched before
@@ -446,8 +445,9 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
+      if (PACKED) tma_prefetch_desc(&tm_r);
     }
-    const int rows = min(kBlockK, p.page_size);  // rows per box
+    const int rows = PACKED ? kBlockK : min(kBlockK, p.page_size);  // rows per box
     const int nsub = kBlockK / rows;             // boxes per column chunk: 1 .. 8
     constexpr int KPARTS = QUANT ? D / C::KW : C::NCH_D, VPARTS = QUANT ? DV / C::VW : C::NCH_V;
     constexpr int KCOLS = QUANT ? C::KW : 64, VCOLS = QUANT ? C::VW : 64;    // columns per box
@@ -498,7 +498,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         ++qn[t];
         if (ONE) ++qn[1];
       }
-      const int32_t* table = p.page_table + w.b * p.pt_b;
+      const int32_t* table = PACKED ? nullptr : p.page_table + w.b * p.pt_b;
       const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
       const int sub = lane & 7;                                  // page of the block: lane % 8 < nsub
       int phys_k = p.n_pages, row_k = 0;  // page and row of this lane's box; outside the pool: zeros
@@ -506,10 +506,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         const int phys_v = phys_k, row_v = row_k;
         if (j < w.n_blocks) {
           const int key = (w.jb0 + j) * kBlockK + sub * rows;
-          const int lp = key >> p.log2_page;
-          row_k = key & (p.page_size - 1);
-          phys_k = p.n_pages;
-          if (sub < nsub && lp < used) phys_k = __ldg(table + lp);
+          if constexpr (PACKED) {  // rows of the next sequence or past the last one: masked, as V's are zeroed
+            row_k = w.k_off + key, phys_k = 0;
+          } else {
+            const int lp = key >> p.log2_page;
+            row_k = key & (p.page_size - 1);
+            phys_k = p.n_pages;
+            if (sub < nsub && lp < used) phys_k = __ldg(table + lp);
+          }
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
@@ -535,9 +539,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                                  : (QUANT ? smem + C::OFF_VRAW + at * C::VRAW : sV + at * C::V_BYTES);
           const int parts = kv == 0 ? KPARTS : VPARTS, row_b = kv == 0 ? KROW : VROW;
           const int part = lane >> 3;  // column chunk
+          const bool shared = PACKED && kv == 0 && part == parts - 1;
           if (sub < nsub && part < parts)
-            tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, kv == 0 ? &tm_k : &tm_v, bar,
-                        part * (kv == 0 ? KCOLS : VCOLS), w.kvh, kv == 0 ? row_k : row_v, kv == 0 ? phys_k : phys_v);
+            tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, shared ? &tm_r : kv == 0 ? &tm_k : &tm_v, bar,
+                        shared ? 0 : part * (kv == 0 ? KCOLS : VCOLS), shared ? 0 : w.kvh, kv == 0 ? row_k : row_v,
+                        kv == 0 ? phys_k : phys_v);
         }
       }
     }
@@ -1251,11 +1257,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
 }
 
 // Launches the kernel, one CTA per SM: as a programmatic dependent of the plan kernel, if there is one.
-template <bool BF16, bool QUANT, int D, int DV, bool ONE>
-cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PagedParams& p,
-                             cudaStream_t st) {
+template <bool BF16, bool QUANT, int D, int DV, bool ONE, bool PACKED>
+cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tr,
+                             const PagedParams& p, cudaStream_t st) {
   using C = PagedCfg<QUANT, D, DV, ONE>;
-  auto kern = paged_kernel<BF16, QUANT, D, DV, ONE>;
+  auto kern = paged_kernel<BF16, QUANT, D, DV, ONE, PACKED>;
   int dev = 0, sms = 0;
   cudaError_t e = current_device_sms(&dev, &sms);
   if (e != cudaSuccess) return e;
@@ -1271,7 +1277,7 @@ cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = p.inline_plan ? 0 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, p);
+  return cudaLaunchKernelEx(&cfg, kern, tq, tk, tv, tr, p);
 }
 
 template <bool BF16, bool QUANT, int D, int DV>
@@ -1279,8 +1285,8 @@ cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, 
                                   const PagedParams& p, cudaStream_t st) {
   // three-block operands leave no room for two readers' rings beside the raw codes
   if constexpr (!(QUANT && D == 192))
-    if (p.max_seqlen_q <= p.tok_tile) return launch_paged_one<BF16, QUANT, D, DV, true>(tq, tk, tv, p, st);
-  return launch_paged_one<BF16, QUANT, D, DV, false>(tq, tk, tv, p, st);
+    if (p.max_seqlen_q <= p.tok_tile) return launch_paged_one<BF16, QUANT, D, DV, true, false>(tq, tk, tv, tv, p, st);
+  return launch_paged_one<BF16, QUANT, D, DV, false, false>(tq, tk, tv, tv, p, st);
 }
 
 }  // namespace sdpa

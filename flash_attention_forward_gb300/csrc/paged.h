@@ -6,7 +6,7 @@
 
 namespace sdpa {
 
-// The work, as one line.  A work unit is two query tiles (2 * tok_tile tokens of one sequence) and one
+// The work, as one line.  A work unit is unit_tiles query tiles (of tok_tile tokens of one sequence each) and one
 // KV head against all the key blocks the tiles see; units lie in the order (sequence, tile, KV
 // head), each as long as its key blocks plus kUnitCost for its prologue and epilogue.  CTA c takes the
 // stretch from cut c to cut c + 1, all of one length, so every SM has the same to do whatever the
@@ -62,7 +62,8 @@ struct PagedParams {
   float* lse;              // [Hq, total_q] or null
   int64_t o_s, o_h;        // element strides of o
   const int32_t* cu_q;     // [B + 1]
-  const int32_t* kv_len;   // [B]
+  const int32_t* kv_len;   // [B], or null: packed keys
+  const int32_t* cu_k;     // packed keys: [B + 1], sequence b's are rows cu_k[b] .. of [total_k, Hkv, .]
   const int32_t* page_table;
   int64_t pt_b;
   const float* k_scale;    // quantised caches: [n_pages, Hkv, page_size]
@@ -74,7 +75,8 @@ struct PagedParams {
   int B, Hq, Hkv, total_q, max_seqlen_q, group, causal;
   int tok_tile;            // tokens per 128-row query tile: 128 / group
   int page_size, log2_page, max_pages, n_pages;
-  int max_kv;              // max_pages * page_size
+  int max_kv;              // max_pages * page_size, or total_k
+  int unit_tiles;          // query tiles of a work unit
   int slot_rows, cut, sms; // cut: the workspace holds partials, units may be cut
   int max_tiles;           // tiles the plan has room for
   int inline_plan;         // the attention kernel plans for itself
@@ -100,6 +102,27 @@ __host__ __device__ __forceinline__ int paged_tile_blocks(int n, int len, int sk
 #endif
 
 #ifdef __CUDACC__
+// Loads of what the plan is made from; the host, where tests replay it, has no read-only form.
+__host__ __device__ __forceinline__ int plan_ld(const int32_t* p) {
+#ifdef __CUDA_ARCH__
+  return __ldg(p);
+#else
+  return *p;
+#endif
+}
+// Keys of sequence b.
+__host__ __device__ __forceinline__ int paged_len(const PagedParams& p, int b) {
+  return p.cu_k != nullptr ? plan_ld(p.cu_k + b + 1) - plan_ld(p.cu_k + b) : plan_ld(p.kv_len + b);
+}
+// Whether sequence b's offsets break the rules (q0, q1: its query rows).
+__host__ __device__ __forceinline__ bool paged_bad(const PagedParams& p, int b, int q0, int q1) {
+  bool bad = q0 < 0 || q1 < q0 || q1 > p.total_q || static_cast<long long>(q1) - q0 > p.max_seqlen_q;
+  if (p.cu_k != nullptr) {
+    const int k0 = plan_ld(p.cu_k + b), k1 = plan_ld(p.cu_k + b + 1);
+    bad = bad || k0 < 0 || k1 < k0 || k1 > p.max_kv;
+  }
+  return bad;
+}
 // Where cut c of n_ctas lies: position x of the line falls into a unit of `blocks` key blocks that starts
 // at `start` for KV head 0 (the tile's units follow one another).  {tile, KV head, block}.
 __host__ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, long long x, long long start, int tile, int blocks) {
@@ -153,6 +176,9 @@ cudaError_t launch_paged_bf16(int D, const CUtensorMap& tq, const CUtensorMap& t
                               const PagedParams& p, cudaStream_t st);
 cudaError_t launch_paged_fp8(bool bf16, int D, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                              const PagedParams& p, cudaStream_t st);
+// Packed keys [total_k, Hkv, 128] and their shared part [total_k, 64] (tr), D = 192.
+cudaError_t launch_paged_packed(bool bf16, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tr, const PagedParams& p, cudaStream_t st);
 cudaError_t launch_paged_combine(bool bf16, int Dv, const PagedParams& p, cudaStream_t st);
 
 }  // namespace sdpa

@@ -7,6 +7,7 @@
 #include "sdpa.h"
 #include "paged.h"
 #include "ptx.cuh"
+#include "scan.cuh"
 
 namespace sdpa {
 
@@ -14,33 +15,10 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// Inclusive sum of v over the block's threads so far (before: the sum of earlier calls); total: the
-// sum of all of them.  Two barriers.
-__device__ __forceinline__ long long block_scan(long long v, long long before, long long (&warp_sum)[33], long long& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sum[warp] = v;
-  __syncthreads();
-  long long s = warp_sum[lane];  // every warp scans the 32 sums itself
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, s, d);
-    if (lane >= d) s += y;
-  }
-  total = before + __shfl_sync(0xffffffffu, s, 31);
-  const long long prev = __shfl_sync(0xffffffffu, s, warp > 0 ? warp - 1 : 0);
-  return before + v + (warp > 0 ? prev : 0);
-}
-
 __device__ __forceinline__ int unit_blocks(const PagedParams& p, int n, int len, int i) {
   const int sk = min(max(len, 0), p.max_kv);
-  return max(paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta),
-             paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * kTilesPerCta + 1));
+  if (p.unit_tiles == 1) return paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i);
+  return max(paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * 2), paged_tile_blocks(n, len, sk, p.tok_tile, p.causal, i * 2 + 1));
 }
 
 // One block lays out the tiles, measures the line and places the cuts.  Offsets that are not sorted
@@ -58,7 +36,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   const int tid = threadIdx.x;
   pdl_launch_dependents();  // the attention kernel may set itself up meanwhile
   if (tid == 0) s_groups = 0;
-  const int tok_unit = kTilesPerCta * p.tok_tile;
+  const int tok_unit = p.unit_tiles * p.tok_tile;
   int bad = 0;
   long long n_tiles = 0;
   for (int base = 0; base < p.B; base += kPlanThreads) {
@@ -66,7 +44,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     int v = 0;
     if (b < p.B) {
       const int q0 = __ldg(p.cu_q + b), q1 = __ldg(p.cu_q + b + 1);
-      if (q0 < 0 || q1 < q0 || q1 > p.total_q || static_cast<long long>(q1) - q0 > p.max_seqlen_q)
+      if (paged_bad(p, b, q0, q1))
         bad = 1;
       else
         v = (q1 - q0 + tok_unit - 1) / tok_unit;
@@ -104,7 +82,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
       p.plan.tiles[tile] = at;
       if (small) s_tile[tile] = at;
       const int n = __ldg(p.cu_q + lo + 1) - __ldg(p.cu_q + lo);
-      v = static_cast<long long>(unit_blocks(p, n, __ldg(p.kv_len + lo), at.y) + kUnitCost) * p.Hkv;
+      v = static_cast<long long>(unit_blocks(p, n, paged_len(p, lo), at.y) + kUnitCost) * p.Hkv;
     }
     const long long before = total;
     const long long incl = block_scan(v, before, warp_sum, total);
@@ -131,7 +109,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
       }
       const int2 at = tiles[lo];
       const int n = __ldg(p.cu_q + at.x + 1) - __ldg(p.cu_q + at.x);
-      cut = paged_cut(p, x, pos[lo], lo, unit_blocks(p, n, __ldg(p.kv_len + at.x), at.y));
+      cut = paged_cut(p, x, pos[lo], lo, unit_blocks(p, n, paged_len(p, at.x), at.y));
     }
     s_cuts[c] = cut;
     p.plan.cuts[c] = cut;
@@ -142,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
     const int2 at = tiles[s_cuts[c].x];
     const int q0 = __ldg(p.cu_q + at.x);
     PagedGroup g;
-    if (paged_group(s_cuts, c, n_ctas, at, q0, __ldg(p.cu_q + at.x + 1) - q0, __ldg(p.kv_len + at.x), g))
+    if (paged_group(s_cuts, c, n_ctas, at, q0, __ldg(p.cu_q + at.x + 1) - q0, paged_len(p, at.x), g))
       p.plan.groups[atomicAdd(&s_groups, 1)] = g;
   }
   __syncthreads();
@@ -171,7 +149,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
   const int prow = blockIdx.y * kMergeRows + threadIdx.x / LANES, col = 8 * (threadIdx.x % LANES);
   const int t = prow / kBlockQ, row = prow - t * kBlockQ;
   const int row_tok = static_cast<int>(fast_div(row, p.div_group));
-  const int tile = tile_u * kTilesPerCta + t;
+  const int tile = tile_u * p.unit_tiles + t;
   const int tok = tile * p.tok_tile + row_tok;
   if (prow >= p.slot_rows || row_tok >= p.tok_tile || tok >= n) return;
   const int head = kvh * p.group + (row - row_tok * p.group);
@@ -205,8 +183,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
 }
 
 // Work tiles that calls of these sizes can have.
-long long tiles_bound(int B, int total_q, int max_seqlen_q, int group) {
-  const long long tok_unit = kTilesPerCta * (kBlockQ / group);
+long long tiles_bound(int B, int total_q, int max_seqlen_q, long long tok_unit) {
   return std::min(static_cast<long long>(B) * ((max_seqlen_q + tok_unit - 1) / tok_unit),
                   (static_cast<long long>(total_q) + (tok_unit - 1) * B) / tok_unit);
 }
@@ -218,9 +195,9 @@ int slot_rows(int group, int max_seqlen_q) {
 }
 
 // Bytes of partial results: two slots per CTA; none where no unit is long enough to be cut.
-size_t partial_bytes(int group, int max_seqlen_q, int max_kv, int Dv) {
+size_t partial_bytes(int slot_rows, int max_kv, int Dv) {
   if ((max_kv + kBlockK - 1) / kBlockK < 2 * kMinPiece) return 0;
-  return 2ull * kPagedMaxCtas * slot_rows(group, max_seqlen_q) * (Dv + 2) * sizeof(float);
+  return 2ull * kPagedMaxCtas * slot_rows * (Dv + 2) * sizeof(float);
 }
 
 bool encode_q(CUtensorMap* map, const void* q, bool bf16, int total_q, int Hq, int D, int64_t q_s, int64_t q_h, int group) {
@@ -260,9 +237,9 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
        reinterpret_cast<uintptr_t>(lse)) & 3u)
     return SDPA_ERR_INVALID;
   const int max_kv = max_pages * page_size;
-  const long long tiles = tiles_bound(B, total_q, max_seqlen_q, group);
+  const long long tiles = tiles_bound(B, total_q, max_seqlen_q, kTilesPerCta * (kBlockQ / group));
   if (tiles * Hkv >= (1ll << 30)) return SDPA_ERR_UNSUPPORTED;
-  const size_t plan = paged_plan_bytes(B, tiles), partials = partial_bytes(group, max_seqlen_q, max_kv, Dv);
+  const size_t plan = paged_plan_bytes(B, tiles), partials = partial_bytes(slot_rows(group, max_seqlen_q), max_kv, Dv);
   if (!workspace || !aligned16(workspace) || workspace_bytes < plan) return SDPA_ERR_INVALID;
 
   PagedParams p{};
@@ -272,6 +249,7 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = kBlockQ / group;
+  p.unit_tiles = kTilesPerCta;
   p.page_size = page_size, p.log2_page = __builtin_ctz((unsigned)page_size);
   p.max_pages = max_pages, p.n_pages = n_pages, p.max_kv = max_kv;
   p.scale2 = (float)((double)scale * 1.4426950408889634);
@@ -316,6 +294,71 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 
+// The expanded form of latent attention: the same kernels over packed keys.
+int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_q, const int32_t* cu_k,
+               void* o, float* lse, int B, int Hq, int Hkv, int total_q, int total_k, int max_seqlen_q, int nope, int rot,
+               int Dv, const int64_t* strides, float scale, int causal, void* workspace, size_t workspace_bytes, int dtype,
+               void* stream) {
+  // ---- validation (no CUDA call before this block passes)
+  if (!q || !k_nope || !k_rope || !v || !cu_q || !cu_k || !o) return SDPA_ERR_INVALID;
+  if (B < 1 || Hq < 1 || Hkv < 1 || total_q < 1 || total_k < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q || nope < 1 || rot < 1 || Dv < 1)
+    return SDPA_ERR_INVALID;
+  if (Hq % Hkv != 0) return SDPA_ERR_INVALID;
+  if (!(std::isfinite(scale) && scale > 0.f)) return SDPA_ERR_INVALID;
+  if (dtype != SDPA_F16 && dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
+  if (nope != 128 || rot != 64 || Dv != 128) return SDPA_ERR_UNSUPPORTED;
+  const int group = Hq / Hkv, D = nope + rot;
+  if (group > kBlockQ || total_k > (1 << 30)) return SDPA_ERR_UNSUPPORTED;
+  int64_t st[SDPA_FWD_LATENT_NSTRIDES] = {(int64_t)Hq * D, D, (int64_t)Hkv * nope, nope, rot, (int64_t)Hkv * Dv, Dv, (int64_t)Hq * Dv, Dv};
+  if (strides) std::memcpy(st, strides, sizeof(st));
+  for (int i = 0; i < SDPA_FWD_LATENT_NSTRIDES; ++i)
+    if (!stride_ok(st[i], 8)) return SDPA_ERR_UNSUPPORTED;
+  if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v) || !aligned16(o)) return SDPA_ERR_UNSUPPORTED;
+  if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
+    return SDPA_ERR_INVALID;
+  const long long tiles = tiles_bound(B, total_q, max_seqlen_q, kTilesPerCta * (kBlockQ / group));
+  if (tiles * Hkv >= (1ll << 30)) return SDPA_ERR_UNSUPPORTED;
+  const size_t plan = paged_plan_bytes(B, tiles), partials = partial_bytes(slot_rows(group, max_seqlen_q), total_k, Dv);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < plan) return SDPA_ERR_INVALID;
+
+  PagedParams p{};
+  p.o = o, p.lse = lse, p.o_s = st[7], p.o_h = st[8];
+  p.cu_q = cu_q, p.cu_k = cu_k;
+  p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
+  p.causal = causal ? 1 : 0;
+  p.tok_tile = kBlockQ / group;
+  p.unit_tiles = kTilesPerCta;
+  p.page_size = kBlockK, p.log2_page = 7, p.max_kv = total_k;
+  p.scale2 = (float)((double)scale * 1.4426950408889634);
+  p.div_group = make_fastdiv((uint32_t)group);
+  p.slot_rows = slot_rows(group, max_seqlen_q);
+  p.cut = partials > 0 && workspace_bytes >= plan + partials;
+  p.max_tiles = (int)tiles;
+  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= p.tok_tile;
+  p.plan = paged_plan_at(workspace, tiles);
+  p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
+  p.part_ml = p.part_o + 2ull * kPagedMaxCtas * p.slot_rows * Dv;
+  int dev = 0;
+  if (current_device_sms(&dev, &p.sms) != cudaSuccess || device_status_ptr(&p.status) != cudaSuccess) return SDPA_ERR_CUDA;
+  p.sms = std::min(p.sms, kPagedMaxCtas);
+
+  alignas(64) CUtensorMap tq, tk, tv, tr;
+  const bool bf16 = dtype == SDPA_BF16;
+  const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  auto rows = [&](CUtensorMap* map, const void* x, int H, int dim, int64_t s, int64_t h) {
+    return encode_bshd(map, x, dt, 2, 1, total_k, H, dim, (int64_t)total_k * s, s, h, 64, kBlockK, CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  if (!encode_q(&tq, q, bf16, total_q, Hq, D, st[0], st[1], group) || !rows(&tk, k_nope, Hkv, nope, st[2], st[3]) ||
+      !rows(&tv, v, Hkv, Dv, st[5], st[6]) || !rows(&tr, k_rope, 1, rot, st[4], rot))
+    return SDPA_ERR_CUDA;
+  p.stall_first_stage = take_stall_flag();
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = p.inline_plan ? cudaSuccess : launch_paged_plan(p, s);
+  if (e == cudaSuccess) e = launch_paged_packed(bf16, tq, tk, tv, tr, p, s);
+  if (e == cudaSuccess && p.cut) e = launch_paged_combine(bf16, Dv, p, s);
+  return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
+}
+
 }  // namespace
 
 cudaError_t launch_paged_plan(const PagedParams& p, cudaStream_t st) {
@@ -334,6 +377,9 @@ cudaError_t launch_paged_combine(bool bf16, int Dv, const PagedParams& p, cudaSt
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
+  if (Dv == kLatentDim)
+    return bf16 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<true, kLatentDim>, p)
+                : cudaLaunchKernelEx(&cfg, paged_combine_kernel<false, kLatentDim>, p);
   if (Dv == 64)
     return bf16 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<true, 64>, p)
                 : cudaLaunchKernelEx(&cfg, paged_combine_kernel<false, 64>, p);
@@ -352,7 +398,7 @@ size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int ma
       max_seqlen_q > total_q || max_kv < 1 || max_kv > (1 << 30) || Dv < 1)
     return 0;
   const int group = Hq / Hkv;
-  return paged_plan_bytes(B, tiles_bound(B, total_q, max_seqlen_q, group)) + partial_bytes(group, max_seqlen_q, max_kv, Dv);
+  return paged_plan_bytes(B, tiles_bound(B, total_q, max_seqlen_q, kTilesPerCta * (kBlockQ / group))) + partial_bytes(slot_rows(group, max_seqlen_q), max_kv, Dv);
 }
 
 int sdpa_fwd_paged(const void* q, const void* k_pool, const void* v_pool, const int32_t* page_table,
@@ -374,6 +420,18 @@ int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, co
   return fwd_paged(true, q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, cu_seqlens_q, o, lse, B, Hq, Hkv,
                    total_q, max_seqlen_q, page_size, max_pages, n_pages, D, Dv, strides, scale, causal, workspace,
                    workspace_bytes, dtype, stream);
+}
+
+size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int total_k) {
+  return sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, total_k, 128);
+}
+
+int sdpa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, void* o, float* lse, int B, int Hq, int Hkv, int total_q, int total_k,
+                    int max_seqlen_q, int nope, int rotary_dim, int Dv, const int64_t* strides, float scale, int causal,
+                    void* workspace, size_t workspace_bytes, sdpa_dtype dtype, void* stream) {
+  return fwd_latent(q, k_nope, k_rope, v, cu_seqlens_q, cu_seqlens_k, o, lse, B, Hq, Hkv, total_q, total_k, max_seqlen_q,
+                    nope, rotary_dim, Dv, strides, scale, causal, workspace, workspace_bytes, dtype, stream);
 }
 
 }  // extern "C"

@@ -30,9 +30,9 @@
  *  - Validation happens before any CUDA call; an invalid call launches nothing.
  *  - The library allocates no device memory in these entry points.  Decode and masked
  *    prefill take a caller workspace sized by the *_workspace_size functions.
- *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_paged*, sdpa_fwd_int8, sdpa_decode, sdpa_decode_paged*
- *    and sdpa_cache_* may be recorded into a CUDA graph (stream capture) once a first call on
- *    the device has run outside the capture; sdpa_fwd_host may not.
+ *  - sdpa_fwd, sdpa_fwd_fp8, sdpa_fwd_varlen*, sdpa_fwd_paged*, sdpa_fwd_latent*, sdpa_fwd_int8, sdpa_decode,
+ *    sdpa_decode_paged*, sdpa_cache_*, sdpa_rope and sdpa_latent_write may be recorded into a CUDA graph (stream
+ *    capture) once a first call on the device has run outside the capture; sdpa_fwd_host may not.
  */
 #ifndef SDPA_GB300_H
 #define SDPA_GB300_H
@@ -464,6 +464,171 @@ int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, co
                        int max_seqlen_q, int page_size, int max_pages, int n_pages, int D, int Dv,
                        const int64_t* strides, float scale, int causal, void* workspace, size_t workspace_bytes,
                        sdpa_dtype dtype, void* stream);
+
+/*
+ * sdpa_cache_resize_workspace_size -- bytes of device scratch sdpa_cache_resize needs for B sequences.  0 for B < 1.
+ */
+size_t sdpa_cache_resize_workspace_size(int B);
+
+/*
+ * sdpa_cache_resize -- page allocation: every sequence's length changes by change[b], pages are given back and taken,
+ * and the new tokens' positions and cache slots are laid out, all on the device and once for all layers of a step.
+ *
+ *   page_table [B, max_pages] DEVICE int32, row stride table_stride >= max_pages, updated in place: entries of pages
+ *           that are taken are written, all others (those of pages given back too) are left as they are
+ *   kv_len  [B] DEVICE int32: rows of each sequence before the call
+ *   change  [B] DEVICE int32: rows to add (> 0: new tokens) or to drop from the end (< 0; -kv_len[b] ends a sequence)
+ *   free_pages [n_pages] DEVICE int32, n_free [1] DEVICE int32: the stack of free pages, entries 0 .. n_free - 1.
+ *           The pages that sequences no longer need (of kv_len rows a sequence holds ceil(kv_len / page_size) pages)
+ *           are pushed, in the order of sequences and of pages, then new pages are popped in that order.  Entries
+ *           below n_free are never written, of those from n_free on only the ones that stay on the stack.
+ *   kv_len_out [B], n_free_out [1] DEVICE int32, written: the values after the call.  They may be kv_len and n_free
+ *           themselves; otherwise a second call with the same inputs does the same.
+ *   cu_seqlens [B + 1] DEVICE int32, written: offsets of each sequence's max(change, 0) new tokens, for
+ *           sdpa_cache_write_fp8, sdpa_fwd_paged* and sdpa_fwd_latent_paged (with kv_len_out)
+ *   positions [total] DEVICE int32, slots [total] DEVICE int64, written: position of each new token in its sequence,
+ *           and its cache row page * page_size + position % page_size, for sdpa_rope and sdpa_latent_write.
+ *           total >= the sum of the new tokens; entries behind it are position 0, slot -1 (no row)
+ *   workspace: sdpa_cache_resize_workspace_size(B) bytes, 16-byte aligned; calls that overlap on the GPU need
+ *           separate ones
+ *
+ * A page belongs to one sequence.  If the free pages do not suffice, a length would be negative or past
+ * max_pages * page_size, the new tokens are more than total, or the stack would leave [0, n_pages], the whole call
+ * changes nothing: kv_len_out = kv_len, n_free_out = n_free, cu_seqlens = 0, slots = -1, and
+ * sdpa_check_device_status() reports SDPA_ERR_INVALID.  page_size: a power of two >= 16.  One or two kernels.
+ */
+int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t* change, int32_t* free_pages,
+                      const int32_t* n_free, int32_t* kv_len_out, int32_t* n_free_out, int32_t* cu_seqlens,
+                      int32_t* positions, int64_t* slots, int B, int total, int page_size, int max_pages, int n_pages,
+                      int64_t table_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Number of int64 entries in the stride array of sdpa_rope. */
+#define SDPA_ROPE_NSTRIDES 8
+
+/*
+ * sdpa_rope -- rotary positions on queries and keys: pair i of the first rotary_dim dims of every head is turned by
+ * the angle positions[t] * inv_freq[i],
+ *     (a, b) -> factor * (a cos - b sin, b cos + a sin),
+ * in fp32, rounded once; dims rotary_dim .. D - 1 are copied.  The angle is reduced to a fraction of a turn before it is
+ * rounded to fp32, which loses 2^-64 of the angle and 2^-64 turns a position.
+ *
+ *   q, q_out [total, Hq, D], k, k_out [total, Hk, D]  dtype (SDPA_F16 or SDPA_BF16); Hk = 0: no k (NULL).  q_out = q and
+ *           k_out = k (with the same strides) turn in place; otherwise outputs must not overlap inputs
+ *   positions [total] DEVICE int32 (negative ones turn back, which is the gradient's rotation)
+ *   inv_freq [rotary_dim / 2] DEVICE fp32, radians a position, below 2^25 in magnitude (else NaN)
+ *   rotary_dim <= D, a multiple of 16 (interleaved: of 8).  interleaved = 0: pair i is dims i and
+ *           i + rotary_dim / 2; else dims 2 i and 2 i + 1
+ *   factor: finite; multiplies the turned dims (the attention factor of stretched contexts, else 1)
+ *   strides: NULL for the contiguous layouts, else 8 element strides {q_s, q_h,  k_s, k_h,  q_out_s, q_out_h,  k_out_s,
+ *           k_out_h}, multiples of 8; pointers 16-byte aligned.  D a multiple of 8.
+ * One kernel.
+ */
+int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,
+              int total, int Hq, int Hk, int D, int rotary_dim, int interleaved, float factor, const int64_t* strides,
+              sdpa_dtype dtype, void* stream);
+
+/* Number of int64 entries in the stride array of sdpa_latent_write. */
+#define SDPA_LATENT_WRITE_NSTRIDES 4
+
+/*
+ * Latent caches.  A cache is one page pool [n_pages, page_size, latent_dim + rotary_dim], f16 or bf16, and a page table as in
+ * sdpa_decode_paged.  A row is a token's latent vector, which is key and value of every head, and
+ * behind it the rotary part of its key, which all heads share.  latent_dim = 512, rotary_dim = 64.
+ */
+
+/*
+ * sdpa_latent_write -- stores new tokens' rows: pool row slots[t] = [c[t] | rope(k_rope[t], positions[t])].
+ *
+ *   c [total, latent_dim], k_rope [total, rotary_dim]  dtype (SDPA_F16 or SDPA_BF16)
+ *   slots [total] DEVICE int64, 8-byte aligned: page * page_size + row (those of sdpa_cache_resize).  A negative slot is
+ *           skipped; one of n_pages * page_size or more is skipped and sdpa_check_device_status() reports
+ *           SDPA_ERR_INVALID.  No two tokens of a call may share a slot.
+ *   positions [total] DEVICE int32, inv_freq [rotary_dim / 2], interleaved, factor: as in sdpa_rope; both pointers NULL: the
+ *           rotary part is stored as it is
+ *   strides: NULL for the contiguous layouts, else 4 element strides {c_s, k_rope_s, pool page, row}, multiples
+ *           of 8; c, k_rope and pool 16-byte aligned.  page_size: a power of two >= 16.
+ * One kernel.
+ */
+int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64_t* slots, const int32_t* positions,
+                      const float* inv_freq, int total, int page_size, int n_pages, int latent_dim, int rotary_dim,
+                      int interleaved, float factor, const int64_t* strides, sdpa_dtype dtype, void* stream);
+
+/* Number of int64 entries in the stride array of sdpa_fwd_latent_paged. */
+#define SDPA_FWD_LATENT_PAGED_NSTRIDES 7
+
+/*
+ * sdpa_fwd_latent_paged_workspace_size -- bytes of device scratch for sdpa_fwd_latent_paged (max_kv = max_pages *
+ * page_size): the work plan, which the call needs, and partial results of query tiles whose keys are divided over several
+ * SMs.  With room for the plan (the value for max_kv = 1) but less than the full size the call divides no tile's
+ * keys; results agree within rounding.  0 for bad sizes.
+ */
+size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_seqlen_q, int max_kv);
+
+/*
+ * sdpa_fwd_latent_paged -- latent attention in its absorbed form: every head's query, taken through the expansion of the
+ * keys, meets the cached rows themselves,
+ *     s[j] = scale * dot(q[t, h, :], row_j),   o[t, h, :] = sum_j softmax(s)[j] * row_j[0 .. latent_dim - 1],
+ * and o goes through the expansion of the values outside.  Sequences, positions and masking are those of
+ * sdpa_fwd_paged: sequence b's n_b new tokens are packed rows cu_seqlens_q[b] .., token i of them is position
+ * kv_len[b] - n_b + i and sees the keys j < kv_len[b], with causal != 0 only those up to its position.  One token a sequence
+ * is a decode step.  A token without visible keys gets O = 0, LSE = -inf.
+ *
+ *   q [total_q, Hq, latent_dim + rotary_dim], o [total_q, Hq, latent_dim]  dtype (SDPA_F16 or SDPA_BF16; o written for the
+ *           rows some sequence owns, the others are left as they are)
+ *   pool [n_pages, page_size, latent_dim + rotary_dim]  dtype: a latent cache
+ *   lse, page_table, kv_len, cu_seqlens_q, max_seqlen_q, bad offsets: as in sdpa_fwd_paged
+ *   strides: NULL for the contiguous layouts, else 7 element strides {q_s, q_h,  pool page, row,  o_s, o_h,  page_table row},
+ *           the first six multiples of 8
+ *   workspace: see sdpa_fwd_latent_paged_workspace_size; 16-byte aligned, contents on entry irrelevant.  Calls that
+ *           overlap on the GPU need separate workspaces.
+ *
+ * P is rounded to dtype for the product with the values, row sums take the fp32 probabilities.  Rows of a page at or past
+ * kv_len never contribute and may hold anything; the visible rows must be finite.  Hq <= 128; latent_dim = 512, rotary_dim = 64;
+ * page_size a power of two >= 16; pointers 16-byte aligned.  The kernels in `stream`: the plan (which the attention makes
+ * itself for up to 256 sequences of one query tile), the attention, and the merge of divided tiles where the workspace
+ * allows any.
+ */
+int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_table, const int32_t* kv_len,
+                          const int32_t* cu_seqlens_q, void* o, float* lse, int B, int Hq, int total_q, int max_seqlen_q,
+                          int page_size, int max_pages, int n_pages, int latent_dim, int rotary_dim, const int64_t* strides,
+                          float scale, int causal, void* workspace, size_t workspace_bytes, sdpa_dtype dtype, void* stream);
+
+/* Number of int64 entries in the stride array of sdpa_fwd_latent. */
+#define SDPA_FWD_LATENT_NSTRIDES 9
+
+/*
+ * sdpa_fwd_latent_workspace_size -- bytes of device scratch for sdpa_fwd_latent, as for sdpa_fwd_paged: the work plan
+ * (required; the value for total_k = 1), then partial results of cut key ranges (optional).  0 for bad sizes.
+ */
+size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int total_k);
+
+/*
+ * sdpa_fwd_latent -- latent attention in its expanded form, over packed sequences: a head's keys are its own part k_nope,
+ * expanded from the latent vectors, and behind it the rotary part k_rope that all heads share and that is not
+ * repeated in memory,
+ *     s[j] = scale * (dot(q[t, h, 0 .. nope - 1], k_nope[j, kvh, :]) + dot(q[t, h, nope ..], k_rope[j, :])).
+ * Sequence b owns query rows cu_seqlens_q[b] .. and key rows cu_seqlens_k[b] ..; its n_b queries are the last of its L_b
+ * positions: query i is position L_b - n_b + i, and with causal != 0 sees the keys up to it (bottom-right aligned, as in
+ * sdpa_fwd_paged).  A query without visible keys gets O = 0, LSE = -inf.
+ *
+ *   q [total_q, Hq, nope + rotary_dim], o [total_q, Hq, Dv]  dtype (SDPA_F16 or SDPA_BF16; o written for the rows some
+ *           sequence owns)
+ *   k_nope [total_k, Hkv, nope], k_rope [total_k, rotary_dim], v [total_k, Hkv, Dv]  dtype
+ *   lse [Hq, total_q] fp32 contiguous, natural log; may be NULL
+ *   cu_seqlens_q, cu_seqlens_k [B + 1] DEVICE int32, non-decreasing within [0, total_q] and [0, total_k]; max_seqlen_q >= every
+ *           n_b and <= total_q.  Offsets that break this make the call store nothing and raise a status that
+ *           sdpa_check_device_status() reports as SDPA_ERR_INVALID.
+ *   strides: NULL for the contiguous layouts, else 9 element strides {q_s, q_h,  k_nope_s, k_nope_h,  k_rope_s,  v_s, v_h,
+ *           o_s, o_h}, multiples of 8 (k_nope and v may be views of one expanded tensor)
+ *   workspace: see sdpa_fwd_latent_workspace_size; 16-byte aligned.  Calls that overlap on the GPU need separate ones.
+ *
+ * nope = 128, rotary_dim = 64, Dv = 128; Hq / Hkv <= 128; pointers 16-byte aligned.  Keys and values some sequence owns must be
+ * finite.  The kernels are those of sdpa_fwd_paged.
+ */
+int sdpa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, void* o, float* lse, int B, int Hq, int Hkv, int total_q, int total_k,
+                    int max_seqlen_q, int nope, int rotary_dim, int Dv, const int64_t* strides, float scale, int causal,
+                    void* workspace, size_t workspace_bytes, sdpa_dtype dtype, void* stream);
 
 /*
  * sdpa_decode_noalloc -- sdpa_decode for callers that cannot allocate device memory: runtimes
