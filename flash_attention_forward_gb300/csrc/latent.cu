@@ -38,6 +38,10 @@ constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr int kPairs = kLatentDim / 128;       // of a key block
 constexpr int kLatentCols = 16;                // columns of a softmax warpgroup
 constexpr int kLatentMaxRows = 64;
+constexpr int kLatentMinPiece = 1;             // blocks; see paged.h
+constexpr int kLatentMinWork = 2;
+constexpr float kNoMax = 1e38f;                // minus the running maximum before the first visible key: finite, so that
+                                               // a hidden key's -inf stays -inf
 
 template <int R>
 struct LatentCfg {
@@ -59,7 +63,8 @@ struct LatentCfg {
   static constexpr int N_BARS = 2 * (PAIRS + ROPES) + 7 + PIECES;
   static constexpr int OFF_PIECE = OFF_BAR + 256;
   static constexpr int OFF_RED = OFF_PIECE + PIECES * 64;          // float [2][WGS][4][16]: maxima, sums
-  static constexpr int SMEM = OFF_RED + 2 * WGS * 4 * kLatentCols * 4;
+  static constexpr int OFF_ROW = OFF_RED + 2 * WGS * 4 * kLatentCols * 4;  // int64 [R], float [R]: rows of O and factors
+  static constexpr int SMEM = OFF_ROW + R * 12;
   static constexpr int S_COL = 0, O_COL = R;                       // tensor memory columns
   static constexpr uint32_t TMEM = R == 64 ? 512 : R == 32 ? 256 : 128;
   static_assert(N_BARS * 8 + 8 <= 256, "barriers fit their area");
@@ -126,6 +131,18 @@ __device__ __forceinline__ bool barrier_any(uint32_t id, uint32_t count, bool x)
       : "r"(static_cast<uint32_t>(x)), "r"(id), "r"(count)
       : "memory");
   return r != 0;
+}
+
+// (x0, x1) = (a0, a1) * b + (c0, c1)
+__device__ __forceinline__ void ffma2_pair(float& x0, float& x1, float a0, float a1, float b, float c0, float c1) {
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\t"
+      "mov.b64 rb, {%4, %4};\n\t"
+      "mov.b64 rc, {%5, %6};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\t"
+      "mov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(x0), "=f"(x1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c0), "f"(c1));
 }
 
 // Barriers (phases continue from piece to piece):
@@ -361,6 +378,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     const uint32_t bar_id = 1 + wg;
     float* red_max = reinterpret_cast<float*>(smem + C::OFF_RED) + wg * 4 * NC;  // [4][16]
     float* red_sum = red_max + C::WGS * 4 * NC;
+    int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::OFF_ROW) + wg * NC;
+    float* row_inv = reinterpret_cast<float*>(smem + C::OFF_ROW + C::WGS * NC * 8) + wg * NC;
     // P^T row of this key: 32 bytes of this warpgroup's columns
     uint8_t* p_row[2];
 #pragma unroll
@@ -383,19 +402,20 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       const int tokens = min(p.tok_tile, w.n - tok0);
       const int base = p.causal ? w.len - w.n + tok0 + 1 : sk;  // keys that the tile's first token sees, but for sk
       const int lim_all = min(sk, base);
-      float m[NC], l[NC];
+      // minus the running maximum, in powers of two, and the sum.  A column without a (token, head), whose scores may be
+      // anything, has P = 0 and no say in the votes.
+      float nm[NC], l[NC];
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
-        // columns without a (token, head): their scores may be anything, P = 0 keeps them out of the votes
         const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + c), lp.div_heads));
         const bool valid = t < tokens && col0 + c - t * lp.group_heads < heads;
-        m[c] = valid ? -INFINITY : INFINITY;
+        nm[c] = valid ? kNoMax : -INFINITY;
         l[c] = 0.f;
       }
       for (int j = 0; j < nb; ++j, ++sn) {
         ok = mbar_wait_warp(s_full, sn & 1, abort_flag, p.status);
         const int k0 = (jb0 + j) * kBlockK;
-        float s[NC];
+        float s[NC], x[NC];  // scores; their distance from the running maximum
         bool need = !ok;
         if (ok) {
           tc_fence_after();
@@ -423,7 +443,11 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             }
           }
 #pragma unroll
-          for (int c = 0; c < NC; ++c) need = need || s[c] * p.scale2 > m[c] + kPagedRescaleLog2;
+          for (int c = 0; c < NC; c += 2) ffma2_pair(x[c], x[c + 1], s[c], s[c + 1], p.scale2, nm[c], nm[c + 1]);
+          float top = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int c = 2; c < NC; c += 2) top = fmax3(top, x[c], x[c + 1]);
+          need = top > kPagedRescaleLog2;
         }
         if (barrier_any(bar_id, 128, need)) {
           // the columns' maxima over the block's keys, new running maxima, O and l rescaled
@@ -449,9 +473,9 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
             const float mb = fmaxf(fmaxf(red_max[c], red_max[NC + c]), fmaxf(red_max[2 * NC + c], red_max[3 * NC + c]));
-            const float top = fmaxf(m[c], mb * p.scale2);
-            alpha[c] = top == m[c] ? 1.f : ex2(m[c] - top);
-            m[c] = top;
+            const float neg = fminf(nm[c], -(mb * p.scale2));
+            alpha[c] = neg == nm[c] ? 1.f : ex2(neg - nm[c]);
+            nm[c] = neg;
             l[c] *= alpha[c];
           }
           if (j > 0) {
@@ -467,14 +491,14 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             }
             tmem_st_wait();
           }
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) ffma2_pair(x[c], x[c + 1], s[c], s[c + 1], p.scale2, nm[c], nm[c + 1]);
         }
         uint32_t pk[NC / 2];
 #pragma unroll
         for (int c = 0; c < NC; c += 2) {
-          const float p0 = ex2(fmaf(s[c], p.scale2, m[c] == -INFINITY ? 0.f : -m[c]));
-          const float p1 = ex2(fmaf(s[c + 1], p.scale2, m[c + 1] == -INFINITY ? 0.f : -m[c + 1]));
-          l[c] += p0;
-          l[c + 1] += p1;
+          const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
+          fadd2(l[c], l[c + 1], p0, p1);
           pk[c / 2] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
         }
         *reinterpret_cast<uint4*>(p_row[0]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
@@ -489,54 +513,70 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
         for (int c = 0; c < NC; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
-      if (lane == 0)
+      if (lane == 0) {
 #pragma unroll
-        for (int c = 0; c < NC; c += 4)
+        for (int c = 0; c < NC; c += 4) {
           *reinterpret_cast<float4*>(red_sum + wq * NC + c) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
-      __syncwarp();
-      named_barrier_sync(bar_id, 128);
-      ok = mbar_wait_warp(o_full, on & 1, abort_flag, p.status);
-      ++on;
-      if (!ok) continue;  // to the barrier at which the warps leave together
-      tc_fence_after();
-      const bool partial = slot >= 0;
-      int64_t at[NC];  // of the column's row in O or among the partials; < 0: no row
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + c), lp.div_heads));
-        const int h = hg * lp.group_heads + col0 + c - t * lp.group_heads;
-        l[c] = (red_sum[c] + red_sum[NC + c]) + (red_sum[2 * NC + c] + red_sum[3 * NC + c]);
-        at[c] = -1;
-        if (m[c] == INFINITY) continue;
-        if (partial) {
-          const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.Hq + h;
-          at[c] = prow * kLatentDim;
-          if (row == c) *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m[c], l[c]);
-          l[c] = 1.f;
-        } else {
-          const int q_row = q_off + tok0 + t;
-          at[c] = q_row * p.o_s + h * p.o_h;
-          if (row == c && p.lse != nullptr)
-            p.lse[static_cast<int64_t>(h) * p.total_q + q_row] = l[c] > 0.f ? (m[c] + lg2(l[c])) * kPagedLn2 : -INFINITY;
-          l[c] = l[c] > 0.f ? 1.f / l[c] : 0.f;
+          if (wq == 0) *reinterpret_cast<float4*>(row_inv + c) = make_float4(nm[c], nm[c + 1], nm[c + 2], nm[c + 3]);
         }
       }
       __syncwarp();
+      named_barrier_sync(bar_id, 128);
+      const bool partial = slot >= 0;
+      if (row < NC) {
+        // this thread's column: where its row of O goes (among the partials or to O; < 0: nowhere), its factor
+        const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + row), lp.div_heads));
+        const int h = hg * lp.group_heads + col0 + row - t * lp.group_heads;
+        const float neg = row_inv[row];
+        const float sum = (red_sum[row] + red_sum[NC + row]) + (red_sum[2 * NC + row] + red_sum[3 * NC + row]);
+        int64_t at = -1;
+        if (neg != -INFINITY) {
+          if (partial) {
+            const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.Hq + h;
+            at = prow * kLatentDim;
+            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(-neg, sum);
+          } else {
+            const int q_row = q_off + tok0 + t;
+            at = q_row * p.o_s + h * p.o_h;
+            if (p.lse != nullptr)
+              p.lse[static_cast<int64_t>(h) * p.total_q + q_row] = sum > 0.f ? (lg2(sum) - neg) * kPagedLn2 : -INFINITY;
+          }
+        }
+        row_at[row] = at;
+        row_inv[row] = partial ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+      }
+      ok = mbar_wait_warp(o_full, on & 1, abort_flag, p.status);
+      ++on;
+      if (barrier_any(bar_id, 128, !ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
 #pragma unroll 1
       for (int c = 0; c < kPairs; ++c) {
         uint32_t o[NC];
         tmem_ld16(tO + c * R, o);
         tmem_ld_wait();
         reg_fence(o);
+        if (partial) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          if (at[i] < 0) continue;
-          const float x = __uint_as_float(o[i]) * l[i];
-          const int64_t to = at[i] + c * 128 + row;
-          if (partial)
-            p.part_o[to] = x;
-          else
-            static_cast<uint16_t*>(p.o)[to] = static_cast<uint16_t>(BF16 ? pack_bf16x2(x, 0.f) : pack_f16x2(x, 0.f));
+          for (int i = 0; i < NC; ++i) {
+            const int64_t at = row_at[i];
+            if (at >= 0) p.part_o[at + c * 128 + row] = __uint_as_float(o[i]);
+          }
+        } else {
+          // neighbouring lanes hold neighbouring dims: an even lane takes both of column i, an odd one of column i + 1
+#pragma unroll
+          for (int i = 0; i < NC; i += 2) {
+            const int mine = i + (lane & 1);
+            const float a = __uint_as_float(o[i]) * row_inv[i], b = __uint_as_float(o[i + 1]) * row_inv[i + 1];
+            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+            const float lo = lane & 1 ? other : a, hi = lane & 1 ? b : other;
+            const int64_t at = row_at[mine];
+            if (at >= 0)
+              *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(p.o) + at + c * 128 + (row & ~1)) =
+                  BF16 ? pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
+          }
         }
         __syncwarp();
       }
@@ -597,7 +637,7 @@ long long latent_tiles(int B, int total_q, int max_seqlen_q, int tok_tile) {
 }
 // Two slots per team of CTAs; none where no unit is long enough to be cut.
 size_t latent_partial_bytes(const LatentTile& t, int Hq, int max_kv) {
-  if ((max_kv + kBlockK - 1) / kBlockK < 2 * kMinPiece) return 0;
+  if ((max_kv + kBlockK - 1) / kBlockK < 2 * kLatentMinPiece) return 0;
   return 2ull * (kPagedMaxCtas / t.groups) * t.tok_tile * Hq * (kLatentDim + 2) * sizeof(float);
 }
 
@@ -654,7 +694,7 @@ int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_t
   p.B = B, p.Hq = Hq, p.Hkv = 1, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = Hq;
   p.causal = causal ? 1 : 0;
   p.tok_tile = t.tok_tile;
-  p.unit_tiles = 1;
+  p.unit_tiles = 1, p.min_piece = kLatentMinPiece, p.min_work = kLatentMinWork;
   p.page_size = page_size, p.log2_page = __builtin_ctz((unsigned)page_size);
   p.max_pages = max_pages, p.n_pages = n_pages, p.max_kv = max_kv;
   p.scale2 = (float)((double)scale * 1.4426950408889634);

@@ -278,7 +278,7 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   if (tid == 0) pos[0] = 0;
   __syncthreads();
   const long long total = pos[p.B];
-  const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / kMinWork)));
+  const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / p.min_work)));
   auto cut_at = [&](int c) { return bad ? make_int4(0, 0, 0, 0) : paged_inline_cut(p, pos, c, n_ctas); };
   if (cta < n_ctas) {
     if (tid == 0) mine[0] = cut_at(cta);

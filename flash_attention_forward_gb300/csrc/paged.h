@@ -11,10 +11,10 @@ namespace sdpa {
 // head), each as long as its key blocks plus kUnitCost for its prologue and epilogue.  CTA c takes the
 // stretch from cut c to cut c + 1, all of one length, so every SM has the same to do whatever the
 // lengths are.  A cut inside a unit divides its keys; the two or more pieces write partials that a
-// second kernel merges.  Cuts that would leave fewer than kMinPiece blocks on a side move to the
+// second kernel merges.  Cuts that would leave fewer than min_piece blocks on a side move to the
 // unit's edge.
 constexpr int kUnitCost = 2;         // blocks' time of a unit's prologue and epilogue
-constexpr int kMinPiece = 3;         // blocks
+constexpr int kMinPiece = 3;         // blocks (of the chunk attention; its min_piece and min_work)
 constexpr int kMinWork = 6;          // blocks per CTA below which more CTAs do not pay (unless units are left)
 constexpr int kPagedMaxCtas = 160;
 
@@ -76,7 +76,8 @@ struct PagedParams {
   int tok_tile;            // tokens per 128-row query tile: 128 / group
   int page_size, log2_page, max_pages, n_pages;
   int max_kv;              // max_pages * page_size, or total_k
-  int unit_tiles;          // query tiles of a work unit
+  int unit_tiles = kTilesPerCta;  // query tiles of a work unit
+  int min_piece = kMinPiece, min_work = kMinWork;
   int slot_rows, cut, sms; // cut: the workspace holds partials, units may be cut
   int max_tiles;           // tiles the plan has room for
   int inline_plan;         // the attention kernel plans for itself
@@ -129,9 +130,9 @@ __host__ __device__ __forceinline__ int4 paged_cut(const PagedParams& p, long lo
   const long long unit = blocks + kUnitCost, r = x - start;  // many KV heads of a long sequence: past 32 bits
   int kvh = static_cast<int>(r / unit);
   int off = static_cast<int>(r - kvh * unit) - kUnitCost;
-  if (p.cut ? off < kMinPiece : 2 * off < blocks) {
+  if (p.cut ? off < p.min_piece : 2 * off < blocks) {
     off = 0;
-  } else if (!p.cut || blocks - off < kMinPiece) {
+  } else if (!p.cut || blocks - off < p.min_piece) {
     off = 0;
     if (++kvh == p.Hkv) kvh = 0, ++tile;
   }

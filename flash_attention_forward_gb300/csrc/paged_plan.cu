@@ -96,8 +96,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   __syncthreads();
   const long long* pos = small ? s_pos : p.plan.tile_pos;
   const int2* tiles = small ? s_tile : p.plan.tiles;
-  // as many CTAs as have kMinWork each, and at least one for every unit
-  const int n_ctas = static_cast<int>(min(static_cast<long long>(p.sms), max(n_tiles * p.Hkv, total / kMinWork)));
+  // as many CTAs as have min_work each, and at least one for every unit
+  const int n_ctas = static_cast<int>(min(static_cast<long long>(p.sms), max(n_tiles * p.Hkv, total / p.min_work)));
   for (int c = tid; c <= n_ctas; c += kPlanThreads) {
     int4 cut = make_int4(static_cast<int>(n_tiles), 0, 0, 0);
     if (c < n_ctas) {
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int i = 0; i < pieces; ++i) {
-    if (i > 0 && ld_dep(&p.plan.cuts[first + i].z) >= blocks) break;  // this tile ends before
+    if (i > 0 && p.unit_tiles > 1 && ld_dep(&p.plan.cuts[first + i].z) >= blocks) break;  // this tile ends before
     const int64_t r = static_cast<int64_t>(i == 0 ? slot0 : 2 * (first + i)) * p.slot_rows + prow;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + r * 2);
     const float4 a = *reinterpret_cast<const float4*>(p.part_o + r * DV + col);
@@ -249,7 +249,6 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = kBlockQ / group;
-  p.unit_tiles = kTilesPerCta;
   p.page_size = page_size, p.log2_page = __builtin_ctz((unsigned)page_size);
   p.max_pages = max_pages, p.n_pages = n_pages, p.max_kv = max_kv;
   p.scale2 = (float)((double)scale * 1.4426950408889634);
@@ -327,7 +326,6 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = kBlockQ / group;
-  p.unit_tiles = kTilesPerCta;
   p.page_size = kBlockK, p.log2_page = 7, p.max_kv = total_k;
   p.scale2 = (float)((double)scale * 1.4426950408889634);
   p.div_group = make_fastdiv((uint32_t)group);
