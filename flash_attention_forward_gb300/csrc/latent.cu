@@ -45,7 +45,8 @@ constexpr float kNoMax = 1e38f;                // minus the running maximum befo
 
 template <int R>
 struct LatentCfg {
-  static constexpr int WGS = R / kLatentCols;
+  static constexpr int NC = kLatentCols;
+  static constexpr int WGS = R / NC;
   static constexpr int THREADS = 128 + 128 * WGS;
   static constexpr int Q_CHUNK = R * 128;
   static constexpr int Q_BYTES = (kLatentRow / 64) * Q_CHUNK;
@@ -62,9 +63,9 @@ struct LatentCfg {
   static constexpr int PIECES = 8;  // announced pieces: more than the producer can run ahead of the softmax
   static constexpr int N_BARS = 2 * (PAIRS + ROPES) + 7 + PIECES;
   static constexpr int OFF_PIECE = OFF_BAR + 256;
-  static constexpr int OFF_RED = OFF_PIECE + PIECES * 64;          // float [2][WGS][4][16]: maxima, sums
-  static constexpr int OFF_ROW = OFF_RED + 2 * WGS * 4 * kLatentCols * 4;  // int64 [R], float [R]: rows of O and factors
-  static constexpr int SMEM = OFF_ROW + R * 12;
+  static constexpr int OFF_RED = OFF_PIECE + PIECES * 64;          // float [2][WGS][4][NC]: maxima, sums
+  static constexpr int OFF_ROW = OFF_RED + 2 * WGS * 4 * NC * 4;  // int64 [R], float [2][R]: rows of O, factors, maxima
+  static constexpr int SMEM = OFF_ROW + R * 16;
   static constexpr int S_COL = 0, O_COL = R;                       // tensor memory columns
   static constexpr uint32_t TMEM = R == 64 ? 512 : R == 32 ? 256 : 128;
   static_assert(N_BARS * 8 + 8 <= 256, "barriers fit their area");
@@ -368,8 +369,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       mbar_drain(mma_done, 0);
     }
   } else if (warp >= 4) {
-    // ------------------------------------------------------------ softmax: a warpgroup for 16 columns
-    constexpr int NC = kLatentCols;
+    // ------------------------------------------------------------ softmax: a warpgroup for NC columns
+    constexpr int NC = C::NC;
     const int wg = (warp - 4) >> 2, wq = warp & 3;
     const int row = wq * 32 + lane;   // key of the block; dim of 128
     const int col0 = wg * NC;
@@ -380,10 +381,11 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     float* red_sum = red_max + C::WGS * 4 * NC;
     int64_t* row_at = reinterpret_cast<int64_t*>(smem + C::OFF_ROW) + wg * NC;
     float* row_inv = reinterpret_cast<float*>(smem + C::OFF_ROW + C::WGS * NC * 8) + wg * NC;
-    // P^T row of this key: 32 bytes of this warpgroup's columns
-    uint8_t* p_row[2];
+    float* neg_max = row_inv + C::WGS * NC;
+    // P^T row of this key: this warpgroup's columns
+    uint8_t* p_row[NC / 8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NC / 8; ++i) {
       const int off = row * C::P_ROW + col0 * 2 + i * 16;
       p_row[i] = smem + C::OFF_P + (off ^ (((off >> 7) & C::P_XOR) << 4));
     }
@@ -402,25 +404,55 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       const int tokens = min(p.tok_tile, w.n - tok0);
       const int base = p.causal ? w.len - w.n + tok0 + 1 : sk;  // keys that the tile's first token sees, but for sk
       const int lim_all = min(sk, base);
-      // minus the running maximum, in powers of two, and the sum.  A column without a (token, head), whose scores may be
-      // anything, has P = 0 and no say in the votes.
-      float nm[NC], l[NC];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + c), lp.div_heads));
-        const bool valid = t < tokens && col0 + c - t * lp.group_heads < heads;
-        nm[c] = valid ? kNoMax : -INFINITY;
-        l[c] = 0.f;
+      // Minus the columns' running maxima, in powers of two, lie in shared memory.  A column without a (token, head), whose
+      // scores may be anything, has P = 0 and no say in the votes.
+      if (row < NC) {
+        const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + row), lp.div_heads));
+        neg_max[row] = t < tokens && col0 + row - t * lp.group_heads < heads ? kNoMax : -INFINITY;
       }
+      named_barrier_sync(bar_id, 128);
+      float l[NC];  // this key's sums
+#pragma unroll
+      for (int c = 0; c < NC; ++c) l[c] = 0.f;
       for (int j = 0; j < nb; ++j, ++sn) {
         ok = mbar_wait_warp(s_full, sn & 1, abort_flag, p.status);
         const int k0 = (jb0 + j) * kBlockK;
-        float s[NC], x[NC];  // scores; their distance from the running maximum
+        auto scores = [&](uint32_t (&r)[NC]) {  // of this thread's key; hidden ones -inf
+          tmem_ld16(tS, r);
+          tmem_ld_wait();
+          reg_fence(r);
+          if (k0 + kBlockK > lim_all) {  // the diagonal and the last block hide keys
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+              const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + c), lp.div_heads));
+              if (k0 + row >= min(sk, p.causal ? base + t : sk)) r[c] = 0xFF800000u;
+            }
+          }
+        };
+        // P with the maxima as they are, which nearly always holds: the barrier that says so comes behind the work
+        uint32_t pk[NC / 2];
+        float sums[NC];
+        auto probabilities = [&](const uint32_t (&r)[NC]) {  // and the largest distance from a running maximum
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < NC; c += 2) {
+            const float2 nm = *reinterpret_cast<const float2*>(neg_max + c);
+            float x0, x1;
+            ffma2_pair(x0, x1, __uint_as_float(r[c]), __uint_as_float(r[c + 1]), p.scale2, nm.x, nm.y);
+            top = fmax3(top, x0, x1);
+            const float p0 = ex2(x0), p1 = ex2(x1);
+            sums[c] = l[c], sums[c + 1] = l[c + 1];
+            fadd2(sums[c], sums[c + 1], p0, p1);
+            pk[c / 2] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+          }
+          return top;
+        };
         bool need = !ok;
         if (ok) {
           tc_fence_after();
           uint32_t r[NC];
-          tmem_ld16(tS, r);
+          scores(r);
+          need = probabilities(r) > kPagedRescaleLog2;
           // rows of V past the cache: 0 * NaN would poison the product.  The block's pairs have all landed.
           if (k0 + kBlockK > sk && k0 + row >= sk) {
             for (int c = wg; c < kPairs; c += C::WGS) {
@@ -431,30 +463,15 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             }
           }
           __syncwarp();
-          tmem_ld_wait();
-          reg_fence(r);
-#pragma unroll
-          for (int c = 0; c < NC; ++c) s[c] = __uint_as_float(r[c]);
-          if (k0 + kBlockK > lim_all) {  // the diagonal and the last block hide keys
-#pragma unroll
-            for (int c = 0; c < NC; ++c) {
-              const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + c), lp.div_heads));
-              if (k0 + row >= min(sk, p.causal ? base + t : sk)) s[c] = -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int c = 0; c < NC; c += 2) ffma2_pair(x[c], x[c + 1], s[c], s[c + 1], p.scale2, nm[c], nm[c + 1]);
-          float top = fmaxf(x[0], x[1]);
-#pragma unroll
-          for (int c = 2; c < NC; c += 2) top = fmax3(top, x[c], x[c + 1]);
-          need = top > kPagedRescaleLog2;
         }
         if (barrier_any(bar_id, 128, need)) {
-          // the columns' maxima over the block's keys, new running maxima, O and l rescaled
+          // the columns' maxima over the block's keys, new running maxima, O and the sums rescaled
+          uint32_t r[NC];
           if (ok) {
+            scores(r);
             float mx[NC];
 #pragma unroll
-            for (int c = 0; c < NC; ++c) mx[c] = s[c];
+            for (int c = 0; c < NC; ++c) mx[c] = __uint_as_float(r[c]);
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
@@ -465,6 +482,9 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
                 *reinterpret_cast<float4*>(red_max + wq * NC + c) = make_float4(mx[c], mx[c + 1], mx[c + 2], mx[c + 3]);
             __syncwarp();
           }
+          float nm[NC];
+#pragma unroll
+          for (int c = 0; c < NC; ++c) nm[c] = neg_max[c];
           if (barrier_any(bar_id, 128, !ok)) {
             ok = false;
             break;
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             const float mb = fmaxf(fmaxf(red_max[c], red_max[NC + c]), fmaxf(red_max[2 * NC + c], red_max[3 * NC + c]));
             const float neg = fminf(nm[c], -(mb * p.scale2));
             alpha[c] = neg == nm[c] ? 1.f : ex2(neg - nm[c]);
-            nm[c] = neg;
+            if (row == c) neg_max[c] = neg;
             l[c] *= alpha[c];
           }
           if (j > 0) {
@@ -491,18 +511,14 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             }
             tmem_st_wait();
           }
-#pragma unroll
-          for (int c = 0; c < NC; c += 2) ffma2_pair(x[c], x[c + 1], s[c], s[c + 1], p.scale2, nm[c], nm[c + 1]);
+          named_barrier_sync(bar_id, 128);  // the new maxima are there
+          probabilities(r);
         }
-        uint32_t pk[NC / 2];
 #pragma unroll
-        for (int c = 0; c < NC; c += 2) {
-          const float p0 = ex2(x[c]), p1 = ex2(x[c + 1]);
-          fadd2(l[c], l[c + 1], p0, p1);
-          pk[c / 2] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-        }
-        *reinterpret_cast<uint4*>(p_row[0]) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4*>(p_row[1]) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        for (int c = 0; c < NC; ++c) l[c] = sums[c];
+#pragma unroll
+        for (int i = 0; i < NC / 8; ++i)
+          *reinterpret_cast<uint4*>(p_row[i]) = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         warp_arrive(p_full, lane);
@@ -515,10 +531,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
         for (int c = 0; c < NC; ++c) l[c] += __shfl_xor_sync(0xffffffffu, l[c], d);
       if (lane == 0) {
 #pragma unroll
-        for (int c = 0; c < NC; c += 4) {
+        for (int c = 0; c < NC; c += 4)
           *reinterpret_cast<float4*>(red_sum + wq * NC + c) = make_float4(l[c], l[c + 1], l[c + 2], l[c + 3]);
-          if (wq == 0) *reinterpret_cast<float4*>(row_inv + c) = make_float4(nm[c], nm[c + 1], nm[c + 2], nm[c + 3]);
-        }
       }
       __syncwarp();
       named_barrier_sync(bar_id, 128);
@@ -527,7 +541,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
         // this thread's column: where its row of O goes (among the partials or to O; < 0: nowhere), its factor
         const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + row), lp.div_heads));
         const int h = hg * lp.group_heads + col0 + row - t * lp.group_heads;
-        const float neg = row_inv[row];
+        const float neg = neg_max[row];
         const float sum = (red_sum[row] + red_sum[NC + row]) + (red_sum[2 * NC + row] + red_sum[3 * NC + row]);
         int64_t at = -1;
         if (neg != -INFINITY) {
