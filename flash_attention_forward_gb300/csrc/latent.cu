@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       for (int j = 0; ok && j < w.n_blocks; ++j) {
         const int page = next, row = ((w.jb0 + j) * kBlockK + sub * rows) & (p.page_size - 1);
         next = page_of(j + 1);
+        const int next_row = ((w.jb0 + j + 1) * kBlockK + sub * rows) & (p.page_size - 1);
 #pragma unroll 1
         for (int c = 0; c <= kPairs; ++c) {  // four pairs, then the rotary chunk
           const bool rope = c == kPairs;
@@ -283,7 +284,13 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
           if (lane == 0) mbar_arrive_expect_tx(full, rope ? kChunkBytes : kPairBytes);
           __syncwarp();
           uint8_t* dst = rope ? smem + C::OFF_ROPE + s * kChunkBytes : smem + C::OFF_PAIR + s * kPairBytes;
-          if (sub < nsub && part < (rope ? 1 : 2)) tma_load_3d(dst + box_at, &tm_c, full, c * 128 + part * 64, row, page);
+          if (sub < nsub && part < (rope ? 1 : 2)) {
+            tma_load_3d(dst + box_at, &tm_c, full, c * 128 + part * 64, row, page);
+            // The ring holds little more than a block, so the next one's boxes go to the L2 meanwhile (one sequence's 64
+            // heads: 177 -> 155 us; two and more blocks ahead lose it all again).  Not for small pages, whose many boxes keep
+            // the copy engine busy as it is.
+            if (nsub <= 2 && hg == 0 && j + 1 < w.n_blocks) tma_prefetch_3d(&tm_c, c * 128 + part * 64, next_row, next);
+          }
         }
       }
     }
