@@ -21,7 +21,7 @@
 // no maximum at all: one barrier with an OR over the warpgroup.  Sums stay per thread, in fp32, until the end of a piece.
 //
 // The work is divided over the SMs as in the chunk attention (paged.h): a unit is one tile of R pairs and one sequence's
-// keys, cuts inside it write partials, which paged_combine_kernel merges.
+// keys, cuts inside it write partials, which latent_combine_kernel merges.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -39,7 +39,7 @@ constexpr int kPairs = kLatentDim / 128;       // of a key block
 constexpr int kLatentCols = 16;                // columns of a softmax warpgroup
 constexpr int kLatentMaxRows = 64;
 constexpr int kLatentMinPiece = 1;             // blocks; see paged.h
-constexpr int kLatentMinWork = 2;
+constexpr int kLatentMinWork = 1;
 constexpr float kNoMax = 1e38f;                // minus the running maximum before the first visible key: finite, so that
                                                // a hidden key's -inf stays -inf
 
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   const int team = blockIdx.x / lp.groups, hg = blockIdx.x - team * lp.groups;
   pdl_launch_dependents();  // the combine may be scheduled early; it waits for this grid
 
-  if (tid == 0) {
+  if (tid == 64) {  // not in the warp that allocates
     for (int s = 0; s < C::PAIRS; ++s) mbar_init(&pair_full[s], 1), mbar_init(&pair_empty[s], 1);
     for (int s = 0; s < C::ROPES; ++s) mbar_init(&rope_full[s], 1), mbar_init(&rope_empty[s], 1);
     mbar_init(q_full, 1);
@@ -204,21 +204,22 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
   int4 cuts[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (p.inline_plan) {
-    int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // not announced before the producer has read it
-    paged_inline_plan<C::THREADS>(p, sQ, mine, team, blockIdx.x == 0);
-    if (warp == 0) cuts[0] = mine[0], cuts[1] = mine[1];
+    int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // free until eight pieces are announced
+    paged_inline_plan<C::THREADS>(p, sQ, mine, team, blockIdx.x == 0);  // barriers of the whole block
+    cuts[0] = mine[0], cuts[1] = mine[1];
+    __syncthreads();  // read before it is a piece's place
   } else {
+    __syncthreads();
     pdl_wait();  // the plan comes from the kernel launched before
-    if (warp == 0 && team < ld_dep(&p.plan.head->n_ctas)) {
+    if (team < ld_dep(&p.plan.head->n_ctas)) {
       cuts[0] = ld_dep(p.plan.cuts + team);
       cuts[1] = ld_dep(p.plan.cuts + team + 1);
     }
   }
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
   int n_piece = 0;
   auto next_piece = [&](bool& ok) -> const LatentPiece& {
     const LatentPiece& w = pieces[n_piece % C::PIECES];
@@ -227,78 +228,85 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     return w;
   };
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ TMA producer (one warp)
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ TMA producers (three warps)
+    // One announces the pieces and loads the query tile and the first chunk of every pair, one the second chunk, one the
+    // rotary chunk: pages of 16 rows take eight boxes a chunk, and a warp issues them one after the other.
+    const int part = warp == 0 ? 0 : warp - 1;
+    const bool rope = part == 2;
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_c);
     }
     const int rows = min(kBlockK, p.page_size);  // rows per box
-    const int nsub = kBlockK / rows;             // boxes per chunk: 1 .. 8
-    const int sub = lane & 7, part = lane >> 3;  // this lane's box of a pair: page and chunk
-    const uint32_t box_at = part * kChunkBytes + sub * rows * 128;
+    const int nsub = kBlockK / rows;             // boxes per chunk: 1 .. 8, one lane each
+    const uint32_t box_at = (part & 1) * kChunkBytes + lane * rows * 128;
+    const int ring = rope ? C::ROPES : C::PAIRS;
+    uint64_t* full = rope ? rope_full : pair_full;
+    uint64_t* empty = rope ? rope_empty : pair_empty;
+    uint8_t* base = smem + (rope ? C::OFF_ROPE : C::OFF_PAIR) + box_at;
+    const int slot_bytes = rope ? kChunkBytes : kPairBytes;
     const int q_tx = p.tok_tile * lp.group_heads * kLatentRow * 2;
     LatentWalk walk(team, cuts[0], cuts[1]);
-    int qn = 0, np = 0, nr = 0;  // pieces, pairs and rotary chunks so far
+    int qn = 0, nl = 0;  // pieces and slots so far
     bool ok = true;
     while (ok) {
       const LatentPiece w = walk.next(p);
-      if (lane == 0) {
-        pieces[n_piece % C::PIECES] = w;
-        mbar_arrive(&piece[n_piece % C::PIECES]);
+      if (part == 0) {
+        if (lane == 0) {
+          pieces[n_piece % C::PIECES] = w;
+          mbar_arrive(&piece[n_piece % C::PIECES]);
+        }
+        ++n_piece;
       }
-      ++n_piece;
       if (w.n_blocks == 0) break;
-      if (qn > 0 && !mbar_wait_warp(q_empty, (qn - 1) & 1, abort_flag, p.status)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full, q_tx);
-        for (int c = 0; c < kLatentRow / 64; ++c)
-          tma_load_3d(sQ + c * C::Q_CHUNK, &tm_q, q_full, c * 64, hg * lp.group_heads, w.q_off + w.tok0);
-      }
-      ++qn;
       const int32_t* table = p.page_table + w.b * p.pt_b;
       const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
       auto page_of = [&](int j) {  // of this lane's box in block j; outside the pool: zeros
-        const int page = ((w.jb0 + j) * kBlockK + sub * rows) >> p.log2_page;
-        return j < w.n_blocks && sub < nsub && page < used ? __ldg(table + page) : p.n_pages;
+        const int page = ((w.jb0 + j) * kBlockK + lane * rows) >> p.log2_page;
+        return j < w.n_blocks && lane < nsub && page < used ? __ldg(table + page) : p.n_pages;
       };
+      auto row_of = [&](int j) { return ((w.jb0 + j) * kBlockK + lane * rows) & (p.page_size - 1); };
       int next = page_of(0);
+      if (part == 0) {
+        if (qn > 0 && !mbar_wait_warp(q_empty, (qn - 1) & 1, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, q_tx);
+          for (int c = 0; c < kLatentRow / 64; ++c)
+            tma_load_3d(sQ + c * C::Q_CHUNK, &tm_q, q_full, c * 64, hg * lp.group_heads, w.q_off + w.tok0);
+        }
+        ++qn;
+      }
       for (int j = 0; ok && j < w.n_blocks; ++j) {
-        const int page = next, row = ((w.jb0 + j) * kBlockK + sub * rows) & (p.page_size - 1);
+        const int page = next, row = row_of(j);
         next = page_of(j + 1);
-        const int next_row = ((w.jb0 + j + 1) * kBlockK + sub * rows) & (p.page_size - 1);
 #pragma unroll 1
-        for (int c = 0; c <= kPairs; ++c) {  // four pairs, then the rotary chunk
-          const bool rope = c == kPairs;
-          const int ring = rope ? C::ROPES : C::PAIRS, i = rope ? nr++ : np++;
-          const int s = i % ring, r = i / ring;
-          uint64_t* full = rope ? &rope_full[s] : &pair_full[s];
-          if (r > 0 && !mbar_wait_warp(rope ? &rope_empty[s] : &pair_empty[s], (r - 1) & 1, abort_flag, p.status)) {
+        for (int c = rope ? kPairs : 0; c < (rope ? kPairs + 1 : kPairs); ++c, ++nl) {
+          const int s = nl % ring, r = nl / ring;
+          if (r > 0 && !mbar_wait_warp(&empty[s], (r - 1) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          if (p.stall_first_stage && i == 0) continue;  // test hook: the first slots never fill
-          if (lane == 0) mbar_arrive_expect_tx(full, rope ? kChunkBytes : kPairBytes);
+          if (p.stall_first_stage && nl == 0) continue;  // test hook: the first slots never fill
+          // one arrival announces the bytes of both chunks of a pair, which may have landed by then
+          if (lane == 0 && part != 1) mbar_arrive_expect_tx(&full[s], slot_bytes);
           __syncwarp();
-          uint8_t* dst = rope ? smem + C::OFF_ROPE + s * kChunkBytes : smem + C::OFF_PAIR + s * kPairBytes;
-          if (sub < nsub && part < (rope ? 1 : 2)) {
-            tma_load_3d(dst + box_at, &tm_c, full, c * 128 + part * 64, row, page);
-            // The ring holds little more than a block, so the next one's boxes go to the L2 meanwhile (one sequence's 64
-            // heads: 177 -> 155 us; two and more blocks ahead lose it all again).  Not for small pages, whose many boxes keep
-            // the copy engine busy as it is.
-            if (nsub <= 2 && hg == 0 && j + 1 < w.n_blocks) tma_prefetch_3d(&tm_c, c * 128 + part * 64, next_row, next);
-          }
+          if (lane < nsub) tma_load_3d(base + s * slot_bytes, &tm_c, &full[s], c * 128 + (part & 1) * 64, row, page);
         }
+        // With one block in the ring the next one's boxes go to the L2 meanwhile (64 / 128 heads of 64 sequences: 151 -> 144,
+        // 248 -> 244 us; with more in the ring, or further ahead, it loses: 16 heads 124 -> 152).  Not for small pages, whose
+        // many boxes keep the copy engine busy as it is.
+        if (C::P_OVER_ROPE && rope && nsub <= 2 && hg == 0 && j + 1 < w.n_blocks && lane < nsub)
+          for (int c = 0; c < kLatentRow / 64; ++c) tma_prefetch_3d(&tm_c, c * 64, row_of(j + 1), next);
       }
     }
     if (!ok && lane == 0) {
       // let every copy already in flight land before the CTA's shared memory goes away
       if (qn > 0) mbar_drain(q_full, (qn - 1) & 1);
-      for (int i = max(0, np - C::PAIRS); i < np; ++i) mbar_drain(&pair_full[i % C::PAIRS], (i / C::PAIRS) & 1);
-      for (int i = max(0, nr - C::ROPES); i < nr; ++i) mbar_drain(&rope_full[i % C::ROPES], (i / C::ROPES) & 1);
+      for (int i = max(0, nl - ring); i < nl; ++i) mbar_drain(&full[i % ring], (i / ring) & 1);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer (one thread)
@@ -371,9 +379,12 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
         if (!ok) break;
         ++qn;
       }
-      // every MMA issued so far has finished before tensor memory is released
-      mma_commit(mma_done);
-      mbar_drain(mma_done, 0);
+      // Every MMA issued so far has finished before tensor memory is released: the softmax has waited for the last ones
+      // (o_full), unless a wait gave up.
+      if (*abort_flag) {
+        mma_commit(mma_done);
+        mbar_drain(mma_done, 0);
+      }
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax: a warpgroup for NC columns
@@ -615,6 +626,83 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   }
 }
 
+// Merges the pieces of the cut units, as paged_combine_kernel, for rows of 512 values: O = sum w_i O_i / sum w_i l_i, w_i =
+// 2^(m_i - max m).  Two warps a row; a warp's lanes fetch the maxima and sums of up to 32 pieces side by side, so that the
+// loads of O depend on one load only and are in flight together.
+constexpr int kLatentMergeRows = 4;
+
+template <bool BF16>
+__global__ void __launch_bounds__(64 * kLatentMergeRows) latent_combine_kernel(const PagedParams p) {
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  // read at once, whether the group exists or not
+  const int n_groups = ld_dep(&p.plan.head->n_groups);
+  const int4* record = reinterpret_cast<const int4*>(p.plan.groups + blockIdx.x);
+  const int4 g0 = ld_dep(record), g1 = ld_dep(record + 1);
+  if (static_cast<int>(blockIdx.x) >= n_groups) return;
+  const int tile = g0.x, first = g0.z, pieces = g0.w, slot0 = g1.x, q_off = g1.y, n = g1.z;
+  const int row = blockIdx.y * kLatentMergeRows + threadIdx.x / 64, col = (threadIdx.x % 64) * 4;  // and col + 256
+  const int row_tok = static_cast<int>(fast_div(row, p.div_group));
+  const int tok = tile * p.tok_tile + row_tok;
+  if (row >= p.slot_rows || tok >= n) return;
+  auto row_of = [&](int i) { return static_cast<int64_t>(i == 0 ? slot0 : 2 * (first + i)) * p.slot_rows + row; };
+  float M = -INFINITY, L = 0.f;
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int base = 0; base < pieces; base += 32) {
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (base + lane < pieces) ml = *reinterpret_cast<const float2*>(p.part_ml + row_of(base + lane) * 2);
+    float top = fmaxf(M, ml.x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float old = M == -INFINITY ? 0.f : ex2(M - top);
+    M = top;
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    float sum = w * ml.y;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    L = L * old + sum;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] *= old;
+    const int count = min(32, pieces - base);
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const float* o = p.part_o + row_of(base + i) * kLatentDim + col;
+      const float4 a = *reinterpret_cast<const float4*>(o), b = *reinterpret_cast<const float4*>(o + 256);
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] += wi * v[c];
+    }
+  }
+  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const int head = row - row_tok * p.group;
+  uint16_t* o = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_off + tok) * p.o_s + static_cast<int64_t>(head) * p.o_h + col;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float* a = acc + 4 * h;
+    *reinterpret_cast<uint2*>(o + 256 * h) =
+        BF16 ? make_uint2(pack_bf16x2(a[0] * inv, a[1] * inv), pack_bf16x2(a[2] * inv, a[3] * inv))
+             : make_uint2(pack_f16x2(a[0] * inv, a[1] * inv), pack_f16x2(a[2] * inv, a[3] * inv));
+  }
+  if (p.lse != nullptr && col == 0)
+    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L > 0.f ? (M + lg2(L)) * kPagedLn2 : -INFINITY;
+}
+
+cudaError_t launch_latent_combine(bool bf16, const PagedParams& p, cudaStream_t st) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  // at most p.sms - 1 units are cut
+  cfg.gridDim = dim3(static_cast<unsigned>(std::max(p.sms - 1, 1)),
+                     static_cast<unsigned>((p.slot_rows + kLatentMergeRows - 1) / kLatentMergeRows));
+  cfg.blockDim = dim3(64 * kLatentMergeRows);
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, latent_combine_kernel<true>, p) : cudaLaunchKernelEx(&cfg, latent_combine_kernel<false>, p);
+}
+
 template <bool BF16, int R>
 cudaError_t launch_latent(const CUtensorMap& tq, const CUtensorMap& tc, const PagedParams& p, const LatentParams& lp,
                           cudaStream_t st) {
@@ -751,7 +839,7 @@ int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_t
     else
       e = bf16 ? launch_latent<true, 64>(tq, tc, p, lp, s) : launch_latent<false, 64>(tq, tc, p, lp, s);
   }
-  if (e == cudaSuccess && p.cut) e = launch_paged_combine(bf16, kLatentDim, p, s);
+  if (e == cudaSuccess && p.cut) e = launch_latent_combine(bf16, p, s);
   return e == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
 

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
   const int prow = blockIdx.y * kMergeRows + threadIdx.x / LANES, col = 8 * (threadIdx.x % LANES);
   const int t = prow / kBlockQ, row = prow - t * kBlockQ;
   const int row_tok = static_cast<int>(fast_div(row, p.div_group));
-  const int tile = tile_u * p.unit_tiles + t;
+  const int tile = tile_u * kTilesPerCta + t;
   const int tok = tile * p.tok_tile + row_tok;
   if (prow >= p.slot_rows || row_tok >= p.tok_tile || tok >= n) return;
   const int head = kvh * p.group + (row - row_tok * p.group);
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
   float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
   for (int i = 0; i < pieces; ++i) {
-    if (i > 0 && p.unit_tiles > 1 && ld_dep(&p.plan.cuts[first + i].z) >= blocks) break;  // this tile ends before
+    if (i > 0 && ld_dep(&p.plan.cuts[first + i].z) >= blocks) break;  // this tile ends before
     const int64_t r = static_cast<int64_t>(i == 0 ? slot0 : 2 * (first + i)) * p.slot_rows + prow;
     const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + r * 2);
     const float4 a = *reinterpret_cast<const float4*>(p.part_o + r * DV + col);
@@ -375,9 +375,6 @@ cudaError_t launch_paged_combine(bool bf16, int Dv, const PagedParams& p, cudaSt
   cfg.stream = st;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  if (Dv == kLatentDim)
-    return bf16 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<true, kLatentDim>, p)
-                : cudaLaunchKernelEx(&cfg, paged_combine_kernel<false, kLatentDim>, p);
   if (Dv == 64)
     return bf16 ? cudaLaunchKernelEx(&cfg, paged_combine_kernel<true, 64>, p)
                 : cudaLaunchKernelEx(&cfg, paged_combine_kernel<false, 64>, p);
