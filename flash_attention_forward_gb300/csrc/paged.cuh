@@ -331,7 +331,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_r, const PagedParams p) {
   static_assert(!(PACKED && QUANT), "packed keys are 16 bits wide");
   using C = PagedCfg<QUANT, D, DV, ONE>;
-  constexpr int KS = C::KS, VS = C::VS, KR = C::KR, VR = C::VR;
+  // Packed keys of D = 192: beside two query tiles there is room for K of two blocks and V of one, and a single slot of V
+  // leaves its load no more time than one tile's Q K^T.  So K and V share eight 16 KB slots: block g's three chunks of K
+  // are numbers 5 g .. 5 g + 2, its V's two halves (64 keys) 5 g + 3 and 5 g + 4, number i lies in slot i % 8.  V(g) then takes
+  // the place of K(g - 1), loaded two steps before its use, and K(g) those of K(g - 2) and V(g - 2), which are free before the
+  // second tile's last Q K^T: every load has at least three products' time (8192 tokens x 128 heads: 2529 -> TIME us).
+  constexpr bool SHARED = PACKED && !ONE;
+  constexpr int KS = C::KS, VS = SHARED ? 2 : C::VS, KR = C::KR, VR = SHARED ? 2 : C::VR;
+  constexpr int kSlot = 16 * 1024;
+  static_assert(!SHARED || (C::NCH_D == 3 && C::NCH_V == 2 && C::KS * C::K_BYTES + C::VS * C::V_BYTES == 8 * kSlot), "eight slots");
   constexpr int NR = C::RAWS > 0 ? C::RAWS : 1;
   constexpr int HELD = C::HELD;
   constexpr bool CONVERT_Q = QUANT && BF16;
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         }
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          if (kv == 0 ? j == w.n_blocks : j == 0) continue;  // K(j), then V(j-1)
+          if (kv == 0 || SHARED ? j == w.n_blocks : j == 0) continue;  // K(j), then V(j-1) (V(j) where they share slots)
           const int rd = ONE && !QUANT ? (j - kv) & 1 : 0;
           const int ring = kv == 0 ? LK : LV, base = (kv == 0 ? 0 : QUANT ? NR : KS) + rd * ring;
           const int c = rd ? nl[kv][1]++ : nl[kv][0]++;
@@ -526,9 +534,16 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             ok = false;
             break;
           }
+          if constexpr (SHARED) {  // whose slots these were besides: K(c): V(c - 2), V(c): K(c - 1)
+            if (kv == 0 ? c > 1 && !mbar_wait_warp(&ld_empty[KS + c % 2], ((c - 2) / 2) & 1, abort_flag, p.status)
+                        : c > 0 && !mbar_wait_warp(&ld_empty[(c - 1) % 2], ((c - 1) / 2) & 1, abort_flag, p.status)) {
+              ok = false;
+              break;
+            }
+          }
           if (p.stall_first_stage && c == 0) continue;  // test hook: the first slots never fill
           uint64_t* bar = &ld_full[base + s];
-          if (!QUANT && kv == 1 && (w.jb0 + j) * kBlockK > w.sk) {
+          if (!QUANT && kv == 1 && (w.jb0 + j + (SHARED ? 1 : 0)) * kBlockK > w.sk) {
             bar = &v_ragged[nr % kFixRing];
             ++nr;
           }
@@ -539,6 +554,15 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                                  : (QUANT ? smem + C::OFF_VRAW + at * C::VRAW : sV + at * C::V_BYTES);
           const int parts = kv == 0 ? KPARTS : VPARTS, row_b = kv == 0 ? KROW : VROW;
           const int part = lane >> 3;  // column chunk
+          if constexpr (SHARED) {
+            if (kv == 1) {  // V's halves of 64 keys, two boxes each
+              if (sub == 0 && part < 4)
+                tma_load_4d(sK + ((5 * c + 3 + (part >> 1)) & 7) * kSlot + (part & 1) * (kSlot / 2), &tm_v, bar, (part & 1) * 64,
+                            w.kvh, row_k + (part >> 1) * 64, 0);
+              continue;
+            }
+            dst = sK + ((5 * c + part) & 7) * kSlot - part * kBlockK * row_b;
+          }
           const bool shared = PACKED && kv == 0 && part == parts - 1;
           if (sub < nsub && part < parts)
             tma_load_4d(dst + part * kBlockK * row_b + sub * rows * row_b, shared ? &tm_r : kv == 0 ? &tm_k : &tm_v, bar,
@@ -574,11 +598,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       const int t = warp >> 1;
       const uint64_t dq0 = make_smem_desc(smem_u32(sQ), 16, 1024, kSwizzle128B);
       const uint64_t dk0 = make_smem_desc(smem_u32(sK), 16, 1024, kSwizzle128B);
-      const uint64_t dv0 = make_smem_desc(smem_u32(sV), kBlockK * 128, 1024, kSwizzle128B);
+      const uint64_t dv0 = make_smem_desc(smem_u32(SHARED ? sK : sV), SHARED ? kSlot / 2 : kBlockK * 128, 1024, kSwizzle128B);
       const uint32_t q_lo = static_cast<uint32_t>(dq0), q_hi = static_cast<uint32_t>(dq0 >> 32);
       const uint32_t k_lo = static_cast<uint32_t>(dk0), k_hi = static_cast<uint32_t>(dk0 >> 32);
       const uint32_t v_lo = static_cast<uint32_t>(dv0), v_hi = static_cast<uint32_t>(dv0 >> 32);
       const uint32_t tS = tmem_base + t * 128;
+      int gk = 0, gv = 0;         // shared slots: blocks of K and of V so far
       const uint32_t tO = tmem_base + 256 + t * 128;
       int qn = 0;                 // loads of this accumulator's query tile so far
       int on = 0, pn = 0;         // pieces and blocks of this slot so far
@@ -596,9 +621,10 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       };
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.status); };
       const uint32_t dq = q_lo + static_cast<uint32_t>(((ONE ? 0 : t) * C::Q_BYTES) >> 4);
-      // O (+)= P V for keys 0-63 or 64-127 of the V block in slot v, and S = Q K^T of the K block in slot k
+      // O (+)= P V for keys 0-63 or 64-127 of the V block in slot v, and S = Q K^T of the K block in slot k (with shared
+      // slots: of block v and k)
       auto pv_half = [&](int half, int v, uint32_t acc) {
-        const uint32_t dv = v_lo + static_cast<uint32_t>((v * C::V_BYTES) >> 4);
+        const uint32_t dv = v_lo + static_cast<uint32_t>((SHARED ? ((5 * v + 3 + half) & 7) * kSlot - half * 64 * 128 : v * C::V_BYTES) >> 4);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < C::PV_STEPS / 2; ++kk) {
@@ -612,7 +638,8 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
 #pragma unroll
         for (int kk = 0; kk < C::QK_STEPS; ++kk) {
           const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
-          mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+          const uint32_t b = SHARED ? k_lo + static_cast<uint32_t>((((5 * k + kk / 4) & 7) * kSlot + (kk % 4) * 32) >> 4) : dk + off;
+          mma_f16_ss(tS, dq + off, q_hi, b, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
         }
       };
       while (true) {
@@ -676,12 +703,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             if (!(ok = wait(&turn[t], turns))) break;
             turns ^= 1u;
             if (pv) {
-              pv_half(0, vu, j > 1 ? 1u : 0u);
-              pv_half(1, vu, 1u);
+              pv_half(0, SHARED ? gv : vu, j > 1 ? 1u : 0u);
+              pv_half(1, SHARED ? gv : vu, 1u);
               ++pn;
+              if (SHARED) mma_commit(&kv_empty[KS + vu]);  // its slots are K's after next: at once
             }
-            if (j < n) qk(ku);
+            if (j < n) qk(SHARED ? gk : ku);
             mbar_arrive(&turn[1 - t]);
+            gk += j < nb, gv += j > 0;
             if (j < n) {
               mma_commit(&s_full[t]);
               mma_commit(&kv_empty[ku]);
@@ -690,7 +719,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
               mbar_arrive(&kv_empty[ku]);
             }
             if (pv) {
-              mma_commit(&kv_empty[KS + vu]);
+              if (!SHARED) mma_commit(&kv_empty[KS + vu]);
               if (j == n) mma_commit(&o_full[t]);
             } else if (j > 0) {
               mbar_arrive(&kv_empty[KS + vu]);
@@ -725,10 +754,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             ++nr;
             uint8_t* v = sV + s * C::V_BYTES;
             // whole 128-byte rows of every column chunk: the swizzle stays inside a row
+            const int g = nv[0] + last;  // shared slots: the block
             for (int u = lane + max(live, 0) * 8; u < kBlockK * 8; u += 32)
 #pragma unroll
               for (int c = 0; c < C::NCH_V; ++c)
-                *reinterpret_cast<uint4*>(v + c * kBlockK * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(SHARED ? sK + ((5 * g + 3 + (u >> 9)) & 7) * kSlot + c * (kSlot / 2) + (u & 511) * 16
+                                                 : v + c * kBlockK * 128 + u * 16) = make_uint4(0u, 0u, 0u, 0u);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&kv_full[KS + s]);
