@@ -155,30 +155,47 @@ struct PagedWalk {
       while (tile < end.x && plan_ld(p.cu_q + tile) == plan_ld(p.cu_q + tile + 1)) ++tile;
     if (!(tile < end.x || (tile == end.x && (kvh < end.y || (kvh == end.y && off < end.z))))) return w;
     const int2 at = ONE && p.inline_plan ? make_int2(tile, 0) : walk_ld(p.plan.tiles + tile);
-    w.b = at.x;
+    const int all = unit<ONE>(p, at, w);
+    const int stop = (tile == end.x && kvh == end.y) ? end.z : all;
     w.kvh = kvh;
+    w.jb0 = off;
+    w.n_blocks = stop - off;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      w.n_s[t] = ONE ? (w.n_blocks + 1 - t) / 2 : min(max(w.n_s[t] - off, 0), w.n_blocks);
+    w.slot = (off > 0 || stop < all) ? 2 * cta + 1 - first : -1;
+    first = 0;
+    off = 0;
+    if (++kvh == p.Hkv) kvh = 0, ++tile;
+    return w;
+  }
+  // Item i of the list: a whole unit.
+  __device__ __forceinline__ static PagedPiece item(const PagedParams& p, int i, int n_items) {
+    const int tiles = n_items / p.Hkv, per = tiles * p.list_heads;
+    const int g = i / per, heads = min(p.list_heads, p.Hkv - g * p.list_heads);
+    const int r = i - g * per, rank = r / heads;
+    PagedPiece w{};
+    w.n_blocks = unit<false>(p, walk_ld(p.plan.tiles + rank), w);
+    w.kvh = g * p.list_heads + (r - rank * heads);
+    w.slot = -1;
+    return w;
+  }
+
+ private:
+  // Fills in the sequence of a unit, and in n_s the blocks that its tiles see; returns the longer one's.
+  template <bool ONE>
+  __host__ __device__ __forceinline__ static int unit(const PagedParams& p, int2 at, PagedPiece& w) {
+    w.b = at.x;
     w.q_off = plan_ld(p.cu_q + w.b);
     w.n = plan_ld(p.cu_q + w.b + 1) - w.q_off;
     w.len = paged_len(p, w.b);
     w.k_off = p.cu_k != nullptr ? plan_ld(p.cu_k + w.b) : 0;
     w.sk = min(max(w.len, 0), p.max_kv);
     w.tok0 = at.y * kTilesPerCta * p.tok_tile;
-    w.jb0 = off;
-    int blocks[kTilesPerCta];
 #pragma unroll
     for (int t = 0; t < kTilesPerCta; ++t)
-      blocks[t] = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, at.y * kTilesPerCta + t);
-    const int all = max(blocks[0], blocks[1]);
-    const int stop = (tile == end.x && kvh == end.y) ? end.z : all;
-    w.n_blocks = stop - off;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      w.n_s[t] = ONE ? (w.n_blocks + 1 - t) / 2 : min(max(blocks[t] - off, 0), w.n_blocks);
-    w.slot = (off > 0 || stop < all) ? 2 * cta + 1 - first : -1;
-    first = 0;
-    off = 0;
-    if (++kvh == p.Hkv) kvh = 0, ++tile;
-    return w;
+      w.n_s[t] = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, at.y * kTilesPerCta + t);
+    return max(w.n_s[0], w.n_s[1]);
   }
 };
 
@@ -335,7 +352,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   // leaves its load no more time than one tile's Q K^T.  So K and V share eight 16 KB slots: block g's three chunks of K
   // are numbers 5 g .. 5 g + 2, its V's two halves (64 keys) 5 g + 3 and 5 g + 4, number i lies in slot i % 8.  V(g) then takes
   // the place of K(g - 1), loaded two steps before its use, and K(g) those of K(g - 2) and V(g - 2), which are free before the
-  // second tile's last Q K^T: every load has at least three products' time (8192 tokens x 128 heads: 2529 -> TIME us).
+  // second tile's last Q K^T: every load has at least three products' time (8192 tokens x 128 heads: 2529 -> 2200 us).
   constexpr bool SHARED = PACKED && !ONE;
   constexpr int KS = C::KS, VS = SHARED ? 2 : C::VS, KR = C::KR, VR = SHARED ? 2 : C::VR;
   constexpr int kSlot = 16 * 1024;
@@ -467,13 +484,27 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
     uint64_t* ld_empty = QUANT ? raw_empty : kv_empty;
     const int q_tx = p.tok_tile * p.group * D * 2;
     PagedWalk walk(blockIdx.x, cuts[0], cuts[1]);
+    // from a list: the next item is asked for while this one is loaded
+    int n_items = 0, item = 0;
+    auto take = [&]() { return lane == 0 ? atomicAdd(&p.plan.head->next_item, 1) : 0; };
+    if constexpr (SHARED) {
+      n_items = ld_dep(&p.plan.head->n_items);
+      if (n_items > 0) item = take();
+    }
     int qn[2] = {0, 0};     // pieces of each accumulator
     int nl[2][2] = {};      // blocks of K and of V issued (16-bit pages: per reader)
     int nr = 0;             // ragged V blocks among them
     int np[3] = {0, 0, 0};  // pieces without a block for softmax 0, softmax 1, the helper
     bool ok = true;
     while (ok) {
-      const PagedPiece w = walk.template next<ONE>(p);
+      PagedPiece w;
+      if (SHARED && n_items > 0) {
+        const int i = __shfl_sync(0xffffffffu, item, 0);
+        w = i < n_items ? PagedWalk::item(p, i, n_items) : PagedPiece{};
+        if (i < n_items) item = take();
+      } else {
+        w = walk.template next<ONE>(p);
+      }
       if (w.n_blocks > 0) {
 #pragma unroll
         for (int r = 0; r < (QUANT ? 2 : 3); ++r) {

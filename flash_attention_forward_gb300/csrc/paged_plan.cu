@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   }
   if (__syncthreads_or(bad) || n_tiles > p.max_tiles) {
     if (tid == 0) {
-      p.plan.head->n_ctas = p.plan.head->n_groups = 0;
+      p.plan.head->n_ctas = p.plan.head->n_groups = p.plan.head->n_items = p.plan.head->next_item = 0;
       atomicOr(p.status, kStatusBadSeqlens);
     }
     return;
@@ -96,6 +96,27 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   __syncthreads();
   const long long* pos = small ? s_pos : p.plan.tile_pos;
   const int2* tiles = small ? s_tile : p.plan.tiles;
+  if (p.list_heads > 0 && n_tiles * p.Hkv >= static_cast<long long>(kListUnits) * p.sms) {
+    // a list: the tiles longest first (as they lie where shared memory does not hold them)
+    if (small) {
+      auto length = [&](int i) { return (i + 1 < n_tiles ? s_pos[i + 1] : total) - s_pos[i]; };
+      for (int tile = tid; tile < n_tiles; tile += kPlanThreads) {
+        const long long mine = length(tile);
+        int rank = 0;
+        for (int i = 0; i < n_tiles; ++i) {
+          const long long other = length(i);
+          rank += other > mine || (other == mine && i < tile);
+        }
+        p.plan.tiles[rank] = s_tile[tile];
+      }
+    }
+    if (tid == 0) {
+      p.plan.head->n_ctas = p.sms;
+      p.plan.head->n_groups = p.plan.head->next_item = 0;
+      p.plan.head->n_items = static_cast<int>(n_tiles) * p.Hkv;
+    }
+    return;
+  }
   // as many CTAs as have min_work each, and at least one for every unit
   const int n_ctas = static_cast<int>(min(static_cast<long long>(p.sms), max(n_tiles * p.Hkv, total / p.min_work)));
   for (int c = tid; c <= n_ctas; c += kPlanThreads) {
@@ -127,6 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   if (tid == 0) {
     p.plan.head->n_ctas = n_ctas;
     p.plan.head->n_groups = s_groups;
+    p.plan.head->n_items = p.plan.head->next_item = 0;
   }
 }
 
@@ -323,6 +345,7 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   PagedParams p{};
   p.o = o, p.lse = lse, p.o_s = st[7], p.o_h = st[8];
   p.cu_q = cu_q, p.cu_k = cu_k;
+  p.list_heads = (int)std::max<int64_t>(1, std::min<int64_t>(Hkv, kListBytes / ((int64_t)total_k * (nope + Dv) * 2)));
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = kBlockQ / group;

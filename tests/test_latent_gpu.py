@@ -95,6 +95,20 @@ def test_expanded_short_chunks_cuts_and_queries_without_keys(dtype, new, lens, H
     check_expanded(q, k, r, v, new, lens, o, lse, 192 ** -0.5, True)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("new,lens,H", [([600, 1, 130, 300, 0, 257, 900, 40], [700, 1, 130, 900, 9, 100, 900, 300], 80),
+                                        ([129] + [1, 3] * 600, [129] + [5, 3] * 600, 2)])
+def test_expanded_many_units(causal, new, lens, H):
+    # whole units from a list, some heads at a time; and more tiles than the plan sorts
+    q, k, r, v = packed(new, lens, H, H, "bf16", seed=H)
+    cu_q, cu_k = offsets(new).to(DEV), offsets(lens).to(DEV)
+    o, lse = fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, max(new), scale=0.07, causal=causal)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    check_expanded(q, k, r, v, new, lens, o, lse, 0.07, causal)
+    o2, lse2 = fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, max(new), scale=0.07, causal=causal)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_expanded_other_sequences_rows_and_the_rest_of_the_output():
     # rows no sequence owns, and the other sequences', may be NaN; the output's are left as they are
     new, lens = [3, 70, 2], [200, 70, 129]
