@@ -331,6 +331,7 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
 //   q_full[t] / q_empty[t]: Q tile t landed / accumulator t's last QK MMA of the piece finished
 //   q_ready[t]            : quantised pages and a bf16 query: tile t converted to fp16
 //   kv_full / kv_empty    : a slot of the K or V ring holds its block / the issuers that read it are done
+//   kc_full[3 s + c]      : shared slots: chunk c of K's block s (mod 2) landed, in kv_full's place
 //   raw_full / raw_empty  : quantised pages: codes of K (0) or V (1) landed / read by the converters
 //   e_full[i % 8 (+ 8)]   : quantised pages: each converter warp of K (of V, where those are others) has stored
 //                           the exponents of its 32 rows of block i (the block's are the largest of the four)
@@ -392,13 +393,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   uint64_t* piece = e_full + 2 * kExpRing;  // [PIECES]
   uint64_t* passed = piece + C::PIECES;   // [3]
   uint64_t* ml_full = passed + 3;         // [1]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ml_full + 1);
+  uint64_t* kc_full = ml_full + 1;        // [6], shared slots only: chunk c of the K block in ring slot s, 3 s + c
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(kc_full + (SHARED ? 6 : 0));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   int2* blk_exp = reinterpret_cast<int2*>(smem + C::OFF_EXP);
   int8_t* q_exp = reinterpret_cast<int8_t*>(smem + C::OFF_QEXP);
   PagedPiece* pieces = reinterpret_cast<PagedPiece*>(smem + C::OFF_PIECE);
   float2* ml_x = reinterpret_cast<float2*>(smem + C::OFF_ML);  // [128]
-  static_assert((24 + kFixRing + 2 * kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
+  static_assert(((SHARED ? 30 : 24) + kFixRing + 2 * kExpRing + 2 * (KS + VS) + 4 * NR + C::PIECES) * 8 + 8 <= C::BARS, "barriers fit their area");
 
   const int tid = threadIdx.x;
   const int warp = tid >> 5;
@@ -418,6 +420,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       mbar_init(&turn[t], 1);
     }
     mbar_init(ml_full, 4);
+    for (int s = 0; s < (SHARED ? 6 : 0); ++s) mbar_init(&kc_full[s], 1);
     for (int t = 0; t < 2; ++t) mbar_init(&q_empty[t], 1);
     for (int s = 0; s < kFixRing; ++s) mbar_init(&v_ragged[s], 1);
     for (int s = 0; s < KS + VS; ++s) {
@@ -565,12 +568,10 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             ok = false;
             break;
           }
-          if constexpr (SHARED) {  // whose slots these were besides: K(c): V(c - 2), V(c): K(c - 1)
-            if (kv == 0 ? c > 1 && !mbar_wait_warp(&ld_empty[KS + c % 2], ((c - 2) / 2) & 1, abort_flag, p.status)
-                        : c > 0 && !mbar_wait_warp(&ld_empty[(c - 1) % 2], ((c - 1) / 2) & 1, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
+          // shared slots: V(c) comes in the place of K(c - 1), too
+          if (SHARED && kv == 1 && c > 0 && !mbar_wait_warp(&ld_empty[(c - 1) % 2], ((c - 1) / 2) & 1, abort_flag, p.status)) {
+            ok = false;
+            break;
           }
           if (p.stall_first_stage && c == 0) continue;  // test hook: the first slots never fill
           uint64_t* bar = &ld_full[base + s];
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             bar = &v_ragged[nr % kFixRing];
             ++nr;
           }
-          if (lane == 0) mbar_arrive_expect_tx(bar, kv == 0 ? KTX : VTX);
+          if (lane == 0 && !(SHARED && kv == 0)) mbar_arrive_expect_tx(bar, kv == 0 ? KTX : VTX);
           __syncwarp();
           const int at = rd * ring + s;
           uint8_t* dst = kv == 0 ? (QUANT ? smem + C::OFF_KRAW + at * C::KRAW : sK + at * C::K_BYTES)
@@ -592,7 +593,22 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
                             w.kvh, row_k + (part >> 1) * 64, 0);
               continue;
             }
-            dst = sK + ((5 * c + part) & 7) * kSlot - part * kBlockK * row_b;
+            // K's first chunk in the place of K(c - 2)'s last, the others in those of V(c - 2)
+#pragma unroll 1
+            for (int ch = 0; ch < 3; ++ch) {
+              if (ch == 1 && c > 1 && !mbar_wait_warp(&ld_empty[KS + c % 2], ((c - 2) / 2) & 1, abort_flag, p.status)) {
+                ok = false;
+                break;
+              }
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&kc_full[3 * s + ch], kSlot);
+                tma_load_4d(sK + ((5 * c + ch) & 7) * kSlot, ch == 2 ? &tm_r : &tm_k, &kc_full[3 * s + ch], ch == 2 ? 0 : ch * 64,
+                            ch == 2 ? 0 : w.kvh, row_k, 0);
+              }
+            }
+            __syncwarp();
+            if (!ok) break;
+            continue;
           }
           const bool shared = PACKED && kv == 0 && part == parts - 1;
           if (sub < nsub && part < parts)
@@ -610,7 +626,12 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       for (int kv = 0; kv < 2; ++kv)
         for (int rd = 0; rd < 2; ++rd) {
           const int ring = kv == 0 ? LK : LV, base = (kv == 0 ? 0 : QUANT ? NR : KS) + rd * ring;
-          for (int j = max(0, nl[kv][rd] - ring); j < nl[kv][rd]; ++j) mbar_drain(&ld_full[base + j % ring], (j / ring) & 1);
+          for (int j = max(0, nl[kv][rd] - ring); j < nl[kv][rd]; ++j) {
+            if (SHARED && kv == 0)
+              for (int ch = 0; ch < 3; ++ch) mbar_drain(&kc_full[3 * (j % ring) + ch], (j / ring) & 1);
+            else
+              mbar_drain(&ld_full[base + j % ring], (j / ring) & 1);
+          }
         }
     }
   } else if (warp == 1 || warp == 3) {
@@ -663,14 +684,28 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           mma_f16_ts(tO, tS + q * 8, dv + static_cast<uint32_t>((q * 16 * 128) >> 4), v_hi, idesc_pv, kk > 0 ? 1u : acc);
         }
       };
+      // Shared slots: chunk by chunk, those that had not landed before this tile's turn (landed) as they do.
+      auto qk_chunks = [&](int k, int slot, uint32_t parity, const bool (&landed)[3]) {
+#pragma unroll
+        for (int c = 0; c < 3; ++c) {
+          if (!landed[c] && !wait(&kc_full[3 * slot + c], parity)) return false;
+          tc_fence_after();
+          const uint32_t b = k_lo + static_cast<uint32_t>((((5 * k + c) & 7) * kSlot) >> 4);
+          const uint32_t a = dq + static_cast<uint32_t>((c * kBlockQ * 128) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ss(tS, a + static_cast<uint32_t>((kk * 32) >> 4), q_hi, b + static_cast<uint32_t>((kk * 32) >> 4), k_hi, idesc_qk,
+                       c > 0 || kk > 0 ? 1u : 0u);
+        }
+        return true;
+      };
       auto qk = [&](int k) {
         const uint32_t dk = k_lo + static_cast<uint32_t>((k * C::K_BYTES) >> 4);
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < C::QK_STEPS; ++kk) {
           const uint32_t off = static_cast<uint32_t>(((kk / 4) * kBlockQ * 128 + (kk % 4) * 32) >> 4);
-          const uint32_t b = SHARED ? k_lo + static_cast<uint32_t>((((5 * k + kk / 4) & 7) * kSlot + (kk % 4) * 32) >> 4) : dk + off;
-          mma_f16_ss(tS, dq + off, q_hi, b, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
+          mma_f16_ss(tS, dq + off, q_hi, dk + off, k_hi, idesc_qk, kk > 0 ? 1u : 0u);
         }
       };
       while (true) {
@@ -721,8 +756,14 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
           // landing and passed on.
           for (int j = 0; j <= nb; ++j) {
             const int ku = ks, vu = vs;
+            const uint32_t kpar = kph;
+            bool landed[3] = {false, false, false};
             if (j < nb) {
-              if (!(ok = wait(&kv_full[ku], kph))) break;
+              if (SHARED) {  // P V does not wait for them; a block that this tile does not see has to have landed
+                if (j >= n && !(ok = wait(&kc_full[3 * ku], kpar) && wait(&kc_full[3 * ku + 1], kpar) && wait(&kc_full[3 * ku + 2], kpar))) break;
+              } else if (!(ok = wait(&kv_full[ku], kph))) {
+                break;
+              }
               next_k();
             }
             if (j > 0) {
@@ -731,6 +772,9 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
             }
             const bool pv = j > 0 && j <= n;
             if (pv && !(ok = (j > 1 || on == 0 || wait(&o_empty[t], (on - 1) & 1)) && wait(&p_full[t], pn & 1))) break;
+            if (SHARED && j < n)
+#pragma unroll
+              for (int c = 0; c < 3; ++c) landed[c] = mbar_test(&kc_full[3 * ku + c], kpar);
             if (!(ok = wait(&turn[t], turns))) break;
             turns ^= 1u;
             if (pv) {
@@ -739,7 +783,11 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
               ++pn;
               if (SHARED) mma_commit(&kv_empty[KS + vu]);  // its slots are K's after next: at once
             }
-            if (j < n) qk(SHARED ? gk : ku);
+            if (SHARED) {
+              if (j < n && !(ok = qk_chunks(gk, ku, kpar, landed))) break;
+            } else if (j < n) {
+              qk(ku);
+            }
             mbar_arrive(&turn[1 - t]);
             gk += j < nb, gv += j > 0;
             if (j < n) {
