@@ -37,7 +37,7 @@ struct PagedPlanHeader {
 // done.  The list takes some KV heads at a time, as many as have their keys and values in kListBytes, and their units
 // longest first: what runs at one time then shares K and V in the L2.  Equal stretches of the line have every CTA at heads
 // of its own (8192 tokens x 128 heads: 10.8 GB of reads that miss it, 2200 us against 1900).
-constexpr int kListUnits = 8;                 // per SM, from which on work is a list
+constexpr int kListUnits = 4;                 // per SM, from which on work is a list
 constexpr int64_t kListBytes = 32 << 20;
 struct PagedPlan {
   PagedPlanHeader* head;
