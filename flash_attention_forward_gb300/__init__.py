@@ -119,7 +119,7 @@ def _load():
         lib.sdpa_fwd_paged.restype = i
         lib.sdpa_fwd_paged_fp8.argtypes = [p] * 10 + [i] * 10 + [p, f, i, p, sz, i, p]
         lib.sdpa_fwd_paged_fp8.restype = i
-        lib.sdpa_cache_resize_workspace_size.argtypes = [i]
+        lib.sdpa_cache_resize_workspace_size.argtypes = [i] * 3
         lib.sdpa_cache_resize_workspace_size.restype = sz
         lib.sdpa_cache_resize.argtypes = [p] * 10 + [i] * 5 + [i64, p, sz, p]
         lib.sdpa_cache_resize.restype = i
@@ -787,9 +787,9 @@ def sdpa_fwd_paged_fp8(q, k_pool, v_pool, k_scale, v_scale, page_table, kv_len, 
                       cu_seqlens_q, max_seqlen_q, scale, causal, out, lse, return_lse, workspace, stream)
 
 
-def sdpa_cache_resize_workspace_size(B: int) -> int:
-    """Bytes of workspace for sdpa_cache_resize."""
-    return _load().sdpa_cache_resize_workspace_size(B)
+def sdpa_cache_resize_workspace_size(B: int, total: int, max_pages: int) -> int:
+    """Bytes of workspace for sdpa_cache_resize (0 for small calls)."""
+    return _load().sdpa_cache_resize_workspace_size(B, total, max_pages)
 
 
 def sdpa_cache_resize(page_table, kv_len, change, free_pages, n_free, page_size: int, total: int, *, kv_len_out=None,
@@ -800,41 +800,45 @@ def sdpa_cache_resize(page_table, kv_len, change, free_pages, n_free, page_size:
     slots [total] int64) of the new tokens, at most ``total``; pass kv_len_out=kv_len and n_free_out=n_free to update
     those in place.  A change that cannot be made whole changes nothing (see sdpa_check_device_status)."""
     _int32_vector("kv_len", kv_len)
-    B, total = kv_len.shape[0], int(total)
+    B, total, device, lib = kv_len.shape[0], int(total), kv_len.device, _load()
     _int32_vector("change", change, B)
     _int32_vector("free_pages", free_pages)
     _int32_vector("n_free", n_free, 1)
     _check_page_table(B, page_table)
-    device = kv_len.device
-    if kv_len_out is None:
-        kv_len_out = _empty((B,), torch.int32, device, stream)
-    if n_free_out is None:
-        n_free_out = _empty((1,), torch.int32, device, stream)
-    if cu_seqlens is None:
-        cu_seqlens = _empty((B + 1,), torch.int32, device, stream)
-    if positions is None:
-        positions = _empty((total,), torch.int32, device, stream)
-    if slots is None:
-        slots = _empty((total,), torch.int64, device, stream)
-    elif slots.dtype != torch.int64 or slots.shape != (total,):
-        raise ValueError(f"slots must be an int64 vector of {total} entries")
-    _int32_vector("kv_len_out", kv_len_out, B)
-    _int32_vector("n_free_out", n_free_out, 1)
-    _int32_vector("cu_seqlens", cu_seqlens, B + 1)
-    _int32_vector("positions", positions, total)
-    lib = _load()
-    if workspace is None:
-        workspace = _empty((lib.sdpa_cache_resize_workspace_size(B),), torch.uint8, device, stream)
-    names = ("page_table", "kv_len", "change", "free_pages", "n_free", "kv_len_out", "n_free_out", "cu_seqlens", "positions",
-             "slots", "workspace")
-    tensors = (page_table, kv_len, change, free_pages, n_free, kv_len_out, n_free_out, cu_seqlens, positions, slots, workspace)
-    dev = _current_device(names, tensors)
-    _unit_vectors(names[1:], tensors[1:])
+    max_pages = page_table.shape[1]
+    names, given = ["page_table", "kv_len", "change", "free_pages", "n_free"], [page_table, kv_len, change, free_pages, n_free]
+
+    def output(name, t, n, dtype=torch.int32):
+        if t is None:
+            return _empty((n,), dtype, device, stream)
+        if t.dtype != dtype or t.shape != (n,):
+            raise ValueError(f"{name} must be a vector of {n} entries of {dtype}")
+        names.append(name)
+        given.append(t)
+        return t
+
+    kv_len_out = output("kv_len_out", kv_len_out, B)
+    n_free_out = output("n_free_out", n_free_out, 1)
+    cu_seqlens = output("cu_seqlens", cu_seqlens, B + 1)
+    positions = output("positions", positions, total)
+    slots = output("slots", slots, total, torch.int64)
+    need = lib.sdpa_cache_resize_workspace_size(B, total, max_pages)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        names.append("workspace")
+        given.append(workspace)
+    elif need:
+        workspace = _empty((need,), torch.uint8, device, stream)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
+    dev = _current_device(names, given)
+    _unit_vectors(names[1:], given[1:])
     if not page_table.is_contiguous():
         _on_device(page_table=page_table)
-    rc = lib.sdpa_cache_resize(*(t.data_ptr() for t in tensors[:-1]), B, total, int(page_size), page_table.shape[1],
-                               free_pages.shape[0], page_table.stride(0), workspace.data_ptr(), workspace.nbytes,
-                               _raw_stream(stream, dev))
+    rc = lib.sdpa_cache_resize(
+        page_table.data_ptr(), kv_len.data_ptr(), change.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
+        kv_len_out.data_ptr(), n_free_out.data_ptr(), cu_seqlens.data_ptr(), positions.data_ptr(), slots.data_ptr(), B, total,
+        int(page_size), max_pages, free_pages.shape[0], page_table.stride(0), ws, ws_bytes, _raw_stream(stream, dev))
     if rc:
         raise SdpaError("sdpa_cache_resize", rc)
     return kv_len_out, n_free_out, cu_seqlens, positions, slots

@@ -22,6 +22,12 @@ namespace {
 
 constexpr int kResizeThreads = 1024;
 constexpr int kResizeTokens = 1024;  // tokens a block of the second kernel
+// One block does all of it where that is little: the sequences fit its shared memory, and the tokens and the pages that
+// could be given back are few.
+constexpr int kResizeSeqs = 1024;
+bool one_block(int B, int total, int max_pages) {
+  return B <= kResizeSeqs && total <= 4 * kResizeThreads && static_cast<long long>(B) * max_pages <= 64 * kResizeThreads;
+}
 
 struct ResizeHead {
   int32_t ok, n_free, freed, taken;
@@ -105,9 +111,11 @@ __device__ __forceinline__ void resize_token(const ResizeParams& p, const int4& 
 
 // One block: the sums.  ALL: the items too.
 template <bool ALL>
-__global__ void __launch_bounds__(kResizeThreads) resize_plan_kernel(const ResizeParams p) {
+__global__ void __launch_bounds__(kResizeThreads) resize_plan_kernel(ResizeParams p) {
   __shared__ long long warp_sum[33];
+  __shared__ int4 s_seqs[ALL ? kResizeSeqs : 1];
   const int tid = threadIdx.x;
+  if (ALL) p.seqs = s_seqs;
   if (!ALL) pdl_launch_dependents();
   long long tokens = 0, freed = 0, taken = 0;
   int bad = 0;
@@ -189,8 +197,8 @@ using namespace sdpa;
 
 extern "C" {
 
-size_t sdpa_cache_resize_workspace_size(int B) {
-  return B < 1 ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int4);
+size_t sdpa_cache_resize_workspace_size(int B, int total, int max_pages) {
+  return B < 1 || total < 1 || max_pages < 1 || one_block(B, total, max_pages) ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int4);
 }
 
 int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t* change, int32_t* free_pages,
@@ -208,18 +216,18 @@ int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t*
   for (const void* w : words)
     if (reinterpret_cast<uintptr_t>(w) & 3u) return SDPA_ERR_INVALID;
   if (reinterpret_cast<uintptr_t>(slots) & 7u) return SDPA_ERR_INVALID;
-  if (!workspace || !aligned16(workspace) || workspace_bytes < sdpa_cache_resize_workspace_size(B)) return SDPA_ERR_INVALID;
+  const size_t need = sdpa_cache_resize_workspace_size(B, total, max_pages);
+  if (need > 0 && (!workspace || !aligned16(workspace) || workspace_bytes < need)) return SDPA_ERR_INVALID;
 
   ResizeParams p{};
   p.table = page_table, p.kv_len = kv_len, p.change = change, p.n_free = n_free, p.free_pages = free_pages;
   p.kv_len_out = kv_len_out, p.n_free_out = n_free_out, p.cu = cu_seqlens, p.positions = positions, p.slots = slots;
-  p.head = static_cast<int4*>(workspace), p.seqs = p.head + 1;
+  if (need > 0) p.head = static_cast<int4*>(workspace), p.seqs = p.head + 1;
   p.pt_b = table_stride;
   p.B = B, p.total = total, p.log2_page = __builtin_ctz((unsigned)page_size), p.max_pages = max_pages, p.n_pages = n_pages;
   if (device_status_ptr(&p.status) != cudaSuccess) return SDPA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // One block does all of it where that is little: the tokens, and the pages that could be given back.
-  if (total <= 4 * kResizeThreads && static_cast<long long>(B) * max_pages <= 64 * kResizeThreads) {
+  if (one_block(B, total, max_pages)) {
     resize_plan_kernel<true><<<1, kResizeThreads, 0, st>>>(p);
     return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
   }

@@ -12,6 +12,7 @@
 // instructions at a rate of two a cycle and SM.
 //
 // Both kernels are bound by memory.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -24,7 +25,7 @@ namespace sdpa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // cos and sin of position * inv_freq, times factor.  inv_freq of 2^25 and above, infinite or NaN: NaN.
 struct Turn {
@@ -70,7 +71,8 @@ struct RopeParams {
   FastDiv div_units, div_lanes;
 };
 
-constexpr int kRopeBatch = 4;  // heads whose loads are in flight together
+constexpr int kRopeBatch = 2;  // heads whose loads are in flight together
+constexpr long long kRopeBusy = 152 * 1024, kRopeFull = 152 * 4096;  // threads
 
 // A thread keeps one unit of a head's row (half pairs: vectors i and i + half; interleaved: one vector;
 // behind the turned dims a vector that is copied) and the angles of its pairs for every lanes-th head.
@@ -90,8 +92,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
   const uint16_t* k = p.k + tok * p.k_s;
   uint16_t* qo = p.qo + tok * p.qo_s;
   uint16_t* ko = p.ko + tok * p.ko_s;
-  uint4 x[kRopeBatch][NV];
-  auto load = [&](int h) {
+  uint4 x[kRopeBatch][NV], next[kRopeBatch][NV];
+  auto load = [&](uint4 (&x)[kRopeBatch][NV], int h) {
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i, h += p.lanes) {
       if (h >= p.H || !(turns || (h < p.Hq ? p.copy_q : p.copy_k))) continue;
@@ -100,14 +102,15 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       if (!INTERLEAVED && turns) x[i][NV - 1] = *reinterpret_cast<const uint4*>(row + d1);
     }
   };
-  load(h0);
+  load(x, h0);
   Turn t[INTERLEAVED ? 4 : 8];
   if (turns) {
     const int pos = __ldg(p.positions + tok);
 #pragma unroll
     for (int i = 0; i < (INTERLEAVED ? 4 : 8); ++i) t[i] = turn_at(__ldg(p.inv_freq + (INTERLEAVED ? 4 : 8) * unit + i), pos, p.factor);
   }
-  for (int h = h0; h < p.H;) {
+  for (int h = h0; h < p.H; h += kRopeBatch * p.lanes) {
+    load(next, h + kRopeBatch * p.lanes);  // while this batch is turned
     int hs = h;
 #pragma unroll
     for (int i = 0; i < kRopeBatch; ++i, hs += p.lanes) {
@@ -130,8 +133,10 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
       }
       *reinterpret_cast<uint4*>(row + d0) = x[i][0];
     }
-    h += kRopeBatch * p.lanes;
-    load(h);
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) x[i][v] = next[i][v];
   }
 }
 
@@ -244,11 +249,11 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
   p.turn_units = rotary_dim / (interleaved ? 8 : 16);
   p.units = p.turn_units + (p.copy_q || p.copy_k ? (D - rotary_dim) / 8 : 0);
   p.factor = factor;
-  // Few tokens: more threads share a token's heads, so that the SMs are busy; many: one thread computes its angles
-  // once for all heads.
+  // A token's heads are shared by as many threads as keep the SMs busy, but a thread that has a batch of heads to itself
+  // computes its angles once for them.
   const long long rows = static_cast<long long>(total) * p.units;
-  constexpr long long kWant = 152 * 1024;
-  p.lanes = static_cast<int>(rows >= kWant ? 1 : (kWant + rows - 1) / rows < p.H ? (kWant + rows - 1) / rows : p.H);
+  const long long busy = (kRopeBusy + rows - 1) / rows, full = (kRopeFull + rows - 1) / rows, batches = (p.H + kRopeBatch - 1) / kRopeBatch;
+  p.lanes = static_cast<int>(std::min<long long>(p.H, std::max(busy, std::min(full, batches))));
   if (rows * p.lanes >= (1ll << 31)) return SDPA_ERR_UNSUPPORTED;
   p.div_units = make_fastdiv(static_cast<uint32_t>(p.units));
   p.div_lanes = make_fastdiv(static_cast<uint32_t>(p.lanes));

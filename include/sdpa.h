@@ -466,9 +466,10 @@ int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, co
                        sdpa_dtype dtype, void* stream);
 
 /*
- * sdpa_cache_resize_workspace_size -- bytes of device scratch sdpa_cache_resize needs for B sequences.  0 for B < 1.
+ * sdpa_cache_resize_workspace_size -- bytes of device scratch sdpa_cache_resize needs: 0 where one block does it all (up to
+ * 1024 sequences, 4096 tokens and B * max_pages of 65536) and for bad sizes.
  */
-size_t sdpa_cache_resize_workspace_size(int B);
+size_t sdpa_cache_resize_workspace_size(int B, int total, int max_pages);
 
 /*
  * sdpa_cache_resize -- page allocation: every sequence's length changes by change[b], pages are given back and taken,
@@ -489,8 +490,8 @@ size_t sdpa_cache_resize_workspace_size(int B);
  *   positions [total] DEVICE int32, slots [total] DEVICE int64, written: position of each new token in its sequence,
  *           and its cache row page * page_size + position % page_size, for sdpa_rope and sdpa_latent_write.
  *           total >= the sum of the new tokens; entries behind it are position 0, slot -1 (no row)
- *   workspace: sdpa_cache_resize_workspace_size(B) bytes, 16-byte aligned; calls that overlap on the GPU need
- *           separate ones
+ *   workspace: sdpa_cache_resize_workspace_size(B, total, max_pages) bytes, 16-byte aligned (NULL where that is 0);
+ *           calls that overlap on the GPU need separate ones
  *
  * A page belongs to one sequence.  If the free pages do not suffice, a length would be negative or past
  * max_pages * page_size, the new tokens are more than total, or the stack would leave [0, n_pages], the whole call
