@@ -51,7 +51,11 @@ struct LatentCfg {
   static constexpr int Q_CHUNK = R * 128;
   static constexpr int Q_BYTES = (kLatentRow / 64) * Q_CHUNK;
   static constexpr bool P_OVER_ROPE = R == 64;
-  static constexpr int PAIRS = R == 64 ? 4 : 5, ROPES = R == 16 ? 2 : 1;  // ring slots
+  static constexpr int PAIRS = R == 64 ? 4 : 5, ROPES = R == 16 ? 2 : 1;  // room for so many
+  // A slot of the ring, with a barrier for its arrival and one for its release, is a pair; with R = 64, where the single
+  // issuing thread sets the pace and every wait costs it some 110 cycles and every commit 55, half a block, the
+  // second one with the rotary chunk (64 / 128 heads of 64 sequences: TIME us).
+  static constexpr int SLOT_PAIRS = R == 64 ? 2 : 1, SLOTS = PAIRS / SLOT_PAIRS, BLOCK_SLOTS = kPairs / SLOT_PAIRS;
   static constexpr int P_ROW = 2 * R, P_BYTES = kBlockK * P_ROW;
   static constexpr uint32_t P_SWIZZLE = R == 64 ? kSwizzle128B : R == 32 ? kSwizzle64B : kSwizzle32B;
   static constexpr int P_XOR = R == 64 ? 7 : R == 32 ? 3 : 1;
@@ -61,7 +65,7 @@ struct LatentCfg {
   static constexpr int OFF_P = P_OVER_ROPE ? OFF_ROPE : OFF_ROPE + ROPES * kChunkBytes;
   static constexpr int OFF_BAR = OFF_ROPE + ROPES * kChunkBytes + (P_OVER_ROPE ? 0 : P_BYTES);
   static constexpr int PIECES = 8;  // announced pieces: more than the producer can run ahead of the softmax
-  static constexpr int N_BARS = 2 * (PAIRS + ROPES) + 7 + PIECES;
+  static constexpr int N_BARS = 2 * (SLOTS + ROPES) + 7 + PIECES;
   static constexpr int OFF_PIECE = OFF_BAR + 256;
   static constexpr int OFF_RED = OFF_PIECE + PIECES * 64;          // float [2][WGS][4][NC]: maxima, sums
   static constexpr int OFF_ROW = OFF_RED + 2 * WGS * 4 * NC * 4;  // int64 [R], float [2][R]: rows of O, factors, maxima
@@ -149,8 +153,8 @@ __device__ __forceinline__ void ffma2_pair(float& x0, float& x1, float a0, float
 // Barriers (phases continue from piece to piece):
 //   piece[i % PIECES]         : the producer announced piece i
 //   q_full / q_empty          : the query tile landed / its last Q K^T of the piece is done
-//   pair_full / pair_empty    : a ring slot holds 128 dims of 128 keys / their P V is done
-//   rope_full / rope_empty    : a rotary chunk landed / its K Q^T is done (R = 64: the block's P V, as P lies there)
+//   pair_full / pair_empty    : a ring slot holds its dims of 128 keys / their P V is done
+//   rope_full / rope_empty    : a rotary chunk landed / its K Q^T is done (R = 64: part of the second slot; P lies there, too)
 //   s_full, p_full            : the scores are there (and all P V before them done) / P is written, O rescaled
 //   o_full, o_empty           : the piece's last P V is done / O has been read
 template <bool BF16, int R>
@@ -165,9 +169,9 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     return;
   }
   uint8_t* sQ = smem + C::OFF_Q;
-  uint64_t* pair_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [PAIRS]
-  uint64_t* pair_empty = pair_full + C::PAIRS;
-  uint64_t* rope_full = pair_empty + C::PAIRS;                            // [ROPES]
+  uint64_t* pair_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [SLOTS]
+  uint64_t* pair_empty = pair_full + C::SLOTS;
+  uint64_t* rope_full = pair_empty + C::SLOTS;                            // [ROPES]
   uint64_t* rope_empty = rope_full + C::ROPES;
   uint64_t* q_full = rope_empty + C::ROPES;
   uint64_t* q_empty = q_full + 1;
@@ -186,7 +190,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   pdl_launch_dependents();  // the combine may be scheduled early; it waits for this grid
 
   if (tid == 64) {  // not in the warp that allocates
-    for (int s = 0; s < C::PAIRS; ++s) mbar_init(&pair_full[s], 1), mbar_init(&pair_empty[s], 1);
+    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&pair_full[s], 1), mbar_init(&pair_empty[s], 1);
     for (int s = 0; s < C::ROPES; ++s) mbar_init(&rope_full[s], 1), mbar_init(&rope_empty[s], 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -241,11 +245,11 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
     const int rows = min(kBlockK, p.page_size);  // rows per box
     const int nsub = kBlockK / rows;             // boxes per chunk: 1 .. 8, one lane each
     const uint32_t box_at = (part & 1) * kChunkBytes + lane * rows * 128;
-    const int ring = rope ? C::ROPES : C::PAIRS;
-    uint64_t* full = rope ? rope_full : pair_full;
-    uint64_t* empty = rope ? rope_empty : pair_empty;
+    const bool own_ring = rope && !C::P_OVER_ROPE;
+    const int ring = own_ring ? C::ROPES : C::SLOTS;
+    uint64_t* full = own_ring ? rope_full : pair_full;
+    uint64_t* empty = own_ring ? rope_empty : pair_empty;
     uint8_t* base = smem + (rope ? C::OFF_ROPE : C::OFF_PAIR) + box_at;
-    const int slot_bytes = rope ? kChunkBytes : kPairBytes;
     const int q_tx = p.tok_tile * lp.group_heads * kLatentRow * 2;
     LatentWalk walk(team, cuts[0], cuts[1]);
     int qn = 0, nl = 0;  // pieces and slots so far
@@ -284,17 +288,28 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
         const int page = next, row = row_of(j);
         next = page_of(j + 1);
 #pragma unroll 1
-        for (int c = rope ? kPairs : 0; c < (rope ? kPairs + 1 : kPairs); ++c, ++nl) {
+        for (int g = 0; g < (own_ring ? 1 : C::BLOCK_SLOTS); ++g, ++nl) {  // the block's slots
           const int s = nl % ring, r = nl / ring;
+          const bool last = g == C::BLOCK_SLOTS - 1;
+          if (C::P_OVER_ROPE && rope && !last) continue;
           if (r > 0 && !mbar_wait_warp(&empty[s], (r - 1) & 1, abort_flag, p.status)) {
             ok = false;
             break;
           }
           if (p.stall_first_stage && nl == 0) continue;  // test hook: the first slots never fill
-          // one arrival announces the bytes of both chunks of a pair, which may have landed by then
-          if (lane == 0 && part != 1) mbar_arrive_expect_tx(&full[s], slot_bytes);
+          // one arrival announces all bytes of a slot, which may have landed by then
+          if (lane == 0 && (part == 0 || own_ring))
+            mbar_arrive_expect_tx(&full[s], own_ring ? kChunkBytes
+                                                     : C::SLOT_PAIRS * kPairBytes + (C::P_OVER_ROPE && last ? kChunkBytes : 0));
           __syncwarp();
-          if (lane < nsub) tma_load_3d(base + s * slot_bytes, &tm_c, &full[s], c * 128 + (part & 1) * 64, row, page);
+          if (rope) {
+            if (lane < nsub) tma_load_3d(base + (own_ring ? s * kChunkBytes : 0), &tm_c, &full[s], kLatentDim, row, page);
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::SLOT_PAIRS; ++i)
+              if (lane < nsub)
+                tma_load_3d(base + (s * C::SLOT_PAIRS + i) * kPairBytes, &tm_c, &full[s], (g * C::SLOT_PAIRS + i) * 128 + part * 64, row, page);
+          }
         }
         // With one block in the ring the next one's boxes go to the L2 meanwhile (64 / 128 heads of 64 sequences: 151 -> 144,
         // 248 -> 244 us; with more in the ring, or further ahead, it loses: 16 heads 124 -> 152).  Not for small pages, whose
@@ -325,32 +340,33 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       const uint32_t v_lo = static_cast<uint32_t>(dv), v_hi = static_cast<uint32_t>(dv >> 32);
       const uint32_t p_lo = static_cast<uint32_t>(dp), p_hi = static_cast<uint32_t>(dp >> 32);
       const uint32_t tS = tmem_base + C::S_COL, tO = tmem_base + C::O_COL;
-      int qn = 0, np = 0, nr = 0, pn = 0;  // pieces, pairs, rotary chunks, blocks so far
+      int qn = 0, nl = 0, bn = 0;  // pieces, slots, blocks so far
       bool ok = true;
       auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag, p.status); };
+      // slot g of the block; a single block in the ring always lies in the same ones
+      auto slot_of = [&](int g) { return C::SLOTS == C::BLOCK_SLOTS ? g : (nl + g) % C::SLOTS; };
       while (true) {
         const LatentPiece& w = next_piece(ok);
         const int nb = ok ? w.n_blocks : 0;
         if (nb == 0 || !wait(q_full, qn & 1)) break;
         for (int j = 0; ok && j < nb; ++j) {
-          // S^T = K Q^T, chunk by chunk as they land
-#pragma unroll 1
-          for (int c = 0; c < kPairs; ++c) {
-            const int s = (np + c) % C::PAIRS;
-            if (!(ok = wait(&pair_full[s], ((np + c) / C::PAIRS) & 1))) break;
-            tc_fence_after();
-            const uint32_t a = k_lo + static_cast<uint32_t>((s * kPairBytes) >> 4);
-            const uint32_t b = q_lo + static_cast<uint32_t>((2 * c * C::Q_CHUNK) >> 4);
+          // S^T = K Q^T, slot by slot as they land
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
+          for (int g = 0; g < C::BLOCK_SLOTS; ++g) {
+            const int s = slot_of(g);
+            if (!(ok = wait(&pair_full[s], ((nl + g) / C::SLOTS) & 1))) break;
+            tc_fence_after();
+            const uint32_t a = k_lo + static_cast<uint32_t>((s * C::SLOT_PAIRS * kPairBytes) >> 4);
+            const uint32_t b = q_lo + static_cast<uint32_t>((2 * g * C::SLOT_PAIRS * C::Q_CHUNK) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 8 * C::SLOT_PAIRS; ++kk)
               mma_f16_ss(tS, a + static_cast<uint32_t>(((kk / 4) * kChunkBytes + (kk % 4) * 32) >> 4), k_hi,
                          b + static_cast<uint32_t>(((kk / 4) * C::Q_CHUNK + (kk % 4) * 32) >> 4), q_hi, idesc_qk,
-                         c > 0 || kk > 0 ? 1u : 0u);
+                         g > 0 || kk > 0 ? 1u : 0u);
           }
-          const int rs = nr % C::ROPES;
-          if (!ok || !(ok = wait(&rope_full[rs], (nr / C::ROPES) & 1))) break;
-          ++nr;
-          tc_fence_after();
+          const int rs = bn % C::ROPES;
+          if (!ok || !(ok = C::P_OVER_ROPE || wait(&rope_full[rs], (bn / C::ROPES) & 1))) break;
+          if (!C::P_OVER_ROPE) tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_f16_ss(tS, r_lo + static_cast<uint32_t>((rs * kChunkBytes + kk * 32) >> 4), r_hi,
@@ -359,21 +375,23 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
           if (!C::P_OVER_ROPE) mma_commit(&rope_empty[rs]);
           if (j == nb - 1) mma_commit(q_empty);
           // O^T += V^T P^T, 128 dims at a time
-          if (!(ok = (j > 0 || qn == 0 || wait(o_empty, (qn - 1) & 1)) && wait(p_full, pn & 1))) break;
-          ++pn;
+          if (!(ok = (j > 0 || qn == 0 || wait(o_empty, (qn - 1) & 1)) && wait(p_full, bn & 1))) break;
+          ++bn;
           tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < kPairs; ++c) {
-            const int s = (np + c) % C::PAIRS;
-            const uint32_t a = v_lo + static_cast<uint32_t>((s * kPairBytes) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kBlockK / 16; ++kk)
-              mma_f16_ss(tO + c * R, a + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi,
-                         p_lo + static_cast<uint32_t>((kk * 16 * C::P_ROW) >> 4), p_hi, idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
+          for (int g = 0; g < C::BLOCK_SLOTS; ++g) {
+            const int s = slot_of(g);
+#pragma unroll
+            for (int i = 0; i < C::SLOT_PAIRS; ++i) {
+              const uint32_t a = v_lo + static_cast<uint32_t>(((s * C::SLOT_PAIRS + i) * kPairBytes) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < kBlockK / 16; ++kk)
+                mma_f16_ss(tO + (g * C::SLOT_PAIRS + i) * R, a + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi,
+                           p_lo + static_cast<uint32_t>((kk * 16 * C::P_ROW) >> 4), p_hi, idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
+            }
             mma_commit(&pair_empty[s]);
           }
-          np += kPairs;
-          if (C::P_OVER_ROPE) mma_commit(&rope_empty[rs]);
+          nl += C::BLOCK_SLOTS;
           if (j == nb - 1) mma_commit(o_full);
         }
         if (!ok) break;
