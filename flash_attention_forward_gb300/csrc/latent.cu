@@ -54,7 +54,7 @@ struct LatentCfg {
   static constexpr int PAIRS = R == 64 ? 4 : 5, ROPES = R == 16 ? 2 : 1;  // room for so many
   // A slot of the ring, with a barrier for its arrival and one for its release, is a pair; with R = 64, where the single
   // issuing thread sets the pace and every wait costs it some 110 cycles and every commit 55, half a block, the
-  // second one with the rotary chunk (64 / 128 heads of 64 sequences: TIME us).
+  // second one with the rotary chunk (128 heads of 64 sequences: 244 -> 212 us).
   static constexpr int SLOT_PAIRS = R == 64 ? 2 : 1, SLOTS = PAIRS / SLOT_PAIRS, BLOCK_SLOTS = kPairs / SLOT_PAIRS;
   static constexpr int P_ROW = 2 * R, P_BYTES = kBlockK * P_ROW;
   static constexpr uint32_t P_SWIZZLE = R == 64 ? kSwizzle128B : R == 32 ? kSwizzle64B : kSwizzle32B;
@@ -65,7 +65,7 @@ struct LatentCfg {
   static constexpr int OFF_P = P_OVER_ROPE ? OFF_ROPE : OFF_ROPE + ROPES * kChunkBytes;
   static constexpr int OFF_BAR = OFF_ROPE + ROPES * kChunkBytes + (P_OVER_ROPE ? 0 : P_BYTES);
   static constexpr int PIECES = 8;  // announced pieces: more than the producer can run ahead of the softmax
-  static constexpr int N_BARS = 2 * (SLOTS + ROPES) + 7 + PIECES;
+  static constexpr int N_BARS = SLOTS + PAIRS + 2 * ROPES + 7 + PIECES;
   static constexpr int OFF_PIECE = OFF_BAR + 256;
   static constexpr int OFF_RED = OFF_PIECE + PIECES * 64;          // float [2][WGS][4][NC]: maxima, sums
   static constexpr int OFF_ROW = OFF_RED + 2 * WGS * 4 * NC * 4;  // int64 [R], float [2][R]: rows of O, factors, maxima
@@ -153,7 +153,7 @@ __device__ __forceinline__ void ffma2_pair(float& x0, float& x1, float a0, float
 // Barriers (phases continue from piece to piece):
 //   piece[i % PIECES]         : the producer announced piece i
 //   q_full / q_empty          : the query tile landed / its last Q K^T of the piece is done
-//   pair_full / pair_empty    : a ring slot holds its dims of 128 keys / their P V is done
+//   pair_full / pair_empty    : a ring slot holds its dims of 128 keys / the P V of a pair of it is done
 //   rope_full / rope_empty    : a rotary chunk landed / its K Q^T is done (R = 64: part of the second slot; P lies there, too)
 //   s_full, p_full            : the scores are there (and all P V before them done) / P is written, O rescaled
 //   o_full, o_empty           : the piece's last P V is done / O has been read
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   }
   uint8_t* sQ = smem + C::OFF_Q;
   uint64_t* pair_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [SLOTS]
-  uint64_t* pair_empty = pair_full + C::SLOTS;
-  uint64_t* rope_full = pair_empty + C::SLOTS;                            // [ROPES]
+  uint64_t* pair_empty = pair_full + C::SLOTS;                            // [PAIRS]
+  uint64_t* rope_full = pair_empty + C::PAIRS;                            // [ROPES]
   uint64_t* rope_empty = rope_full + C::ROPES;
   uint64_t* q_full = rope_empty + C::ROPES;
   uint64_t* q_empty = q_full + 1;
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   pdl_launch_dependents();  // the combine may be scheduled early; it waits for this grid
 
   if (tid == 64) {  // not in the warp that allocates
-    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&pair_full[s], 1), mbar_init(&pair_empty[s], 1);
+    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&pair_full[s], 1);
+    for (int s = 0; s < C::PAIRS; ++s) mbar_init(&pair_empty[s], 1);
     for (int s = 0; s < C::ROPES; ++s) mbar_init(&rope_full[s], 1), mbar_init(&rope_empty[s], 1);
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
@@ -292,7 +293,11 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
           const int s = nl % ring, r = nl / ring;
           const bool last = g == C::BLOCK_SLOTS - 1;
           if (C::P_OVER_ROPE && rope && !last) continue;
-          if (r > 0 && !mbar_wait_warp(&empty[s], (r - 1) & 1, abort_flag, p.status)) {
+          // where a slot is two pairs, each is loaded as it gets free; P, in the rotary chunk's place, with the last one
+          auto free_slot = [&](int i) {
+            return r == 0 || mbar_wait_warp(&empty[own_ring ? s : s * C::SLOT_PAIRS + i], (r - 1) & 1, abort_flag, p.status);
+          };
+          if (!free_slot(rope && !own_ring ? C::SLOT_PAIRS - 1 : 0)) {
             ok = false;
             break;
           }
@@ -306,9 +311,12 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
             if (lane < nsub) tma_load_3d(base + (own_ring ? s * kChunkBytes : 0), &tm_c, &full[s], kLatentDim, row, page);
           } else {
 #pragma unroll
-            for (int i = 0; i < C::SLOT_PAIRS; ++i)
+            for (int i = 0; i < C::SLOT_PAIRS; ++i) {
+              if (i > 0 && !(ok = free_slot(i))) break;
               if (lane < nsub)
                 tma_load_3d(base + (s * C::SLOT_PAIRS + i) * kPairBytes, &tm_c, &full[s], (g * C::SLOT_PAIRS + i) * 128 + part * 64, row, page);
+            }
+            if (!ok) break;
           }
         }
         // With one block in the ring the next one's boxes go to the L2 meanwhile (64 / 128 heads of 64 sequences: 151 -> 144,
@@ -388,8 +396,8 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
               for (int kk = 0; kk < kBlockK / 16; ++kk)
                 mma_f16_ss(tO + (g * C::SLOT_PAIRS + i) * R, a + static_cast<uint32_t>((kk * 16 * 128) >> 4), v_hi,
                            p_lo + static_cast<uint32_t>((kk * 16 * C::P_ROW) >> 4), p_hi, idesc_pv, j > 0 || kk > 0 ? 1u : 0u);
+              mma_commit(&pair_empty[s * C::SLOT_PAIRS + i]);
             }
-            mma_commit(&pair_empty[s]);
           }
           nl += C::BLOCK_SLOTS;
           if (j == nb - 1) mma_commit(o_full);

@@ -367,7 +367,7 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   const bool bf16 = dtype == SDPA_BF16;
   const CUtensorMapDataType dt = bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   auto rows = [&](CUtensorMap* map, const void* x, int H, int dim, int64_t s, int64_t h, int box_rows) {
-    return encode_bshd(map, x, dt, 2, 1, total_k, H, dim, (int64_t)total_k * s, s, h, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_bshd(map, x, dt, 2, 1, total_k, H, dim, s, s, h, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
   const int v_rows = max_seqlen_q <= p.tok_tile ? kBlockK : kBlockK / 2;  // the long chunks' kernel loads V by halves
   if (!encode_q(&tq, q, bf16, total_q, Hq, D, st[0], st[1], group) || !rows(&tk, k_nope, Hkv, nope, st[2], st[3], kBlockK) ||
