@@ -335,3 +335,50 @@ def test_absorbed_without_room_for_partials_and_repeatable():
         absorbed(args, new, lens, workspace=small)
         c = absorbed(args, new, lens)
         assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
+
+
+def test_absorbed_pages_past_32_bits():
+    # the sequences' pages lie behind 2^32 bytes of their pool
+    page = 64
+    n_pages = (1 << 32) // (576 * 2 * page) + 40
+    pool = torch.empty((n_pages, page, 576), dtype=torch.bfloat16, device=DEV)
+    pool[:40] = float("nan")
+    g = torch.Generator().manual_seed(2)
+    rows = torch.randn((36 * page, 576), generator=g).to(torch.bfloat16).to(DEV)
+    ids = torch.randperm(36, generator=g)
+    pool[n_pages - 36:] = rows.view(36, page, 576)[ids]
+    table = torch.empty(36, dtype=torch.int32)
+    table[ids] = torch.arange(n_pages - 36, n_pages, dtype=torch.int32)   # logical page i lies where ids is i
+    q = torch.randn((3, 16, 576), generator=g).to(torch.bfloat16).to(DEV)
+    new, lens = [1, 2], [20 * page - 5, 16 * page]
+    table2 = torch.full((2, 20), -1, dtype=torch.int32)
+    table2[0], table2[1, :16] = table[:20], table[20:]
+    table2, kv, cu = table2.to(DEV), torch.tensor(lens, dtype=torch.int32, device=DEV), offsets(new).to(DEV)
+    o, lse = fa.sdpa_fwd_latent_paged(q, pool, table2, kv, cu, 2, scale=0.05, causal=True)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    check_absorbed(q, pool, table2, new, lens, o, lse, 0.05, True)
+
+
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+def test_captured_calls_replay(form):
+    if form == "absorbed":
+        args = cache([3, 1, 40], [500, 9, 3000], 16, 64, "bf16")
+        call = lambda: fa.sdpa_fwd_latent_paged(*args, 40, scale=0.05, causal=True)
+    else:
+        q, k, r, v = packed([300, 5], [700, 5], 16, 16, "bf16")
+        cu_q, cu_k = offsets([300, 5]).to(DEV), offsets([700, 5]).to(DEV)
+        call = lambda: fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, 300, causal=True)
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):   # each with a workspace of its own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, call()))
+    for g, out in graphs + graphs:
+        for t in out:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
