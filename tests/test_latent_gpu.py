@@ -382,3 +382,28 @@ def test_captured_calls_replay(form):
         torch.cuda.synchronize()
         assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
     assert fa.sdpa_check_device_status() == fa.SDPA_OK
+
+
+@pytest.mark.parametrize("form,Hq", [("absorbed", 16), ("absorbed", 128), ("expanded", 2), ("expanded", 16)])
+def test_stalled_load_times_out_and_context_survives(form, Hq):
+    # the test hook withholds the first slots of one launch: every wait gives up, and the next call is right
+    if form == "absorbed":
+        new, lens = [1, 1], [900, 400]
+        args = cache(new, lens, Hq, 64, "bf16")
+        call = lambda: fa.sdpa_fwd_latent_paged(*args, 1, scale=0.05, causal=True)
+    else:
+        new, lens = ([300, 60], [500, 500]) if Hq == 2 else ([100, 60], [500, 500])
+        q, k, r, v = packed(new, lens, Hq, Hq, "bf16")
+        cu_q, cu_k = offsets(new).to(DEV), offsets(lens).to(DEV)
+        call = lambda: fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, max(new), scale=0.05, causal=True)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    assert fa.library().sdpa_debug_stall_next_call() == fa.SDPA_OK
+    call()
+    assert fa.sdpa_check_device_status() == fa.SDPA_ERR_TIMEOUT
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    o, lse = call()
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    if form == "absorbed":
+        check_absorbed(args[0], args[1], args[2], new, lens, o, lse, 0.05, True)
+    else:
+        check_expanded(q, k, r, v, new, lens, o, lse, 0.05, True)
