@@ -156,18 +156,19 @@ struct LatentWriteParams {
 constexpr int kWriteThreads = 256;
 constexpr int kWriteTokens = 16;  // a block's latent vectors: four 16-byte vectors a thread
 constexpr int kTurnTokens = 32;   // a block's rotary parts: four pairs a thread
+static_assert(kTurnTokens == 2 * kWriteTokens, "two blocks of vectors to one of rotary parts");
 
-// The first blocks copy latent vectors, the others turn the rotary parts beside them (in one block the copies of some
-// warps waited for their angles: 66,000 rows 28.9 -> 28.1 us; what is read once leaving the L2 first, 26.5).
+// Of three blocks two copy latent vectors, the third turns the rotary parts beside them (in one block the copies of some
+// warps waited for their angles: 66,000 rows 28.9 -> 28.1 us; what is read once leaving the L2 first, 26.2 us).
 template <bool BF16, bool INTERLEAVED>
 __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const LatentWriteParams p) {
   auto slot_row = [&](int64_t slot) {
     return p.pool + (slot >> p.log2_page) * p.p_page + (slot & ((int64_t(1) << p.log2_page) - 1)) * p.p_row;
   };
-  const int copies = (p.total + kWriteTokens - 1) / kWriteTokens;
-  if (static_cast<int>(blockIdx.x) < copies) {
+  const int group = blockIdx.x / 3, role = blockIdx.x - 3 * group;
+  if (role < 2) {
     constexpr int VECS = kLatentDim / 8, REPS = kWriteTokens * VECS / kWriteThreads;
-    const int t0 = blockIdx.x * kWriteTokens + threadIdx.x / VECS, v = threadIdx.x % VECS;
+    const int t0 = (2 * group + role) * kWriteTokens + threadIdx.x / VECS, v = threadIdx.x % VECS;
     uint4 x[REPS];
     int64_t slot[REPS];
 #pragma unroll
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kWriteThreads) latent_write_kernel(const Laten
       if (slot[i] >= 0 && slot[i] < p.n_slots) reinterpret_cast<uint4*>(slot_row(slot[i]))[v] = x[i];
     return;
   }
-  const int tok = (blockIdx.x - copies) * kTurnTokens + threadIdx.x / 8, u = threadIdx.x % 8;
+  const int tok = group * kTurnTokens + threadIdx.x / 8, u = threadIdx.x % 8;
   if (tok >= p.total) return;
   // pairs 4 u .. 4 u + 3: dims 8 u .. + 7 (interleaved), or 4 u .. + 3 and 32 + 4 u .. + 3
   const int64_t slot = __ldg(p.slots + tok);
@@ -300,7 +301,7 @@ int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64
   const bool bf16 = dtype == SDPA_BF16;
   auto kern = interleaved ? (bf16 ? latent_write_kernel<true, true> : latent_write_kernel<false, true>)
                           : (bf16 ? latent_write_kernel<true, false> : latent_write_kernel<false, false>);
-  const unsigned n = static_cast<unsigned>(total), grid = (n + kWriteTokens - 1) / kWriteTokens + (n + kTurnTokens - 1) / kTurnTokens;
+  const unsigned grid = 3 * ((static_cast<unsigned>(total) + kTurnTokens - 1) / kTurnTokens);
   kern<<<grid, kWriteThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? SDPA_OK : SDPA_ERR_CUDA;
 }
