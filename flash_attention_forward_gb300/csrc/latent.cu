@@ -27,7 +27,7 @@
 #include <cstring>
 
 #include "sdpa.h"
-#include "paged.cuh"
+#include "latent_plan.cuh"
 
 namespace sdpa {
 
@@ -38,8 +38,6 @@ constexpr int kPairBytes = 2 * kChunkBytes;
 constexpr int kPairs = kLatentDim / 128;       // of a key block
 constexpr int kLatentCols = 16;                // columns of a softmax warpgroup
 constexpr int kLatentMaxRows = 64;
-constexpr int kLatentMinPiece = 1;             // blocks; see paged.h
-constexpr int kLatentMinWork = 1;
 constexpr float kNoMax = 1e38f;                // minus the running maximum before the first visible key: finite, so that
                                                // a hidden key's -inf stays -inf
 
@@ -83,45 +81,6 @@ struct LatentCfg {
 struct LatentParams {
   int groups, group_heads;  // head groups of a tile's tokens, and the heads of one
   FastDiv div_heads;        // by group_heads
-};
-
-struct LatentPiece {
-  int b, tok0, jb0;
-  int n_blocks;             // 0: no more pieces
-  int slot;                 // partial slot, or -1: the whole unit, which stores O itself
-  int q_off, n, len, sk;
-  int pad[7];
-};
-static_assert(sizeof(LatentPiece) == 64, "the producer announces a piece in 64 bytes");
-
-// The pieces of a CTA's stretch, in order.
-struct LatentWalk {
-  int team, tile, off, first;
-  int4 end;
-
-  __device__ __forceinline__ LatentWalk(int team, int4 from, int4 to) : team(team), tile(from.x), off(from.z), first(1), end(to) {}
-  __device__ __forceinline__ LatentPiece next(const PagedParams& p) {
-    LatentPiece w{};
-    if (p.inline_plan)
-      while (tile < end.x && plan_ld(p.cu_q + tile) == plan_ld(p.cu_q + tile + 1)) ++tile;
-    if (!(tile < end.x || (tile == end.x && off < end.z))) return w;
-    const int2 at = p.inline_plan ? make_int2(tile, 0) : walk_ld(p.plan.tiles + tile);
-    w.b = at.x;
-    w.q_off = plan_ld(p.cu_q + w.b);
-    w.n = plan_ld(p.cu_q + w.b + 1) - w.q_off;
-    w.len = paged_len(p, w.b);
-    w.sk = min(max(w.len, 0), p.max_kv);
-    w.tok0 = at.y * p.tok_tile;
-    w.jb0 = off;
-    const int all = paged_tile_blocks(w.n, w.len, w.sk, p.tok_tile, p.causal, at.y);
-    const int stop = tile == end.x ? end.z : all;
-    w.n_blocks = stop - off;
-    w.slot = (off > 0 || stop < all) ? 2 * team + 1 - first : -1;
-    first = 0;
-    off = 0;
-    ++tile;
-    return w;
-  }
 };
 
 // Whether any of the `count` threads at barrier `id` says so; a barrier among them.
@@ -212,7 +171,7 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
   int4 cuts[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (p.inline_plan) {
     int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // free until eight pieces are announced
-    paged_inline_plan<C::THREADS>(p, sQ, mine, team, blockIdx.x == 0);  // barriers of the whole block
+    latent_inline_plan<C::THREADS>(p, sQ, mine, team, blockIdx.x == 0);  // barriers of the whole block
     cuts[0] = mine[0], cuts[1] = mine[1];
     __syncthreads();  // read before it is a piece's place
   } else {
@@ -837,7 +796,7 @@ int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_t
   p.slot_rows = t.tok_tile * Hq;
   p.cut = partials > 0 && workspace_bytes >= plan + partials;
   p.max_tiles = (int)tiles;
-  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= t.tok_tile;
+  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= kInlineTiles * t.tok_tile;
   p.plan = paged_plan_at(workspace, tiles);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
   p.part_ml = p.part_o + 2ull * (kPagedMaxCtas / t.groups) * p.slot_rows * kLatentDim;

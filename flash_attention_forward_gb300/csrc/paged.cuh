@@ -255,14 +255,13 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
 }
 
 // The plan where every sequence has one query tile, by each CTA for itself: a scan over the sequences'
-// lengths on the line, then this CTA's two cuts; one CTA stores all of them and the cut units for the merge.
+// lengths on the line, then this CTA's two cuts; CTA 0 stores all of them and the cut units for the merge.
 // Spares the launch of a planning kernel and the wait for it (in a graph, 16-bit and e4m3 pages: drafts of 16 sequences
 // 104.5 -> 101.7 us and 89.1 -> 87.9, 64 sequences of one key block 22.7 -> 21.0 and 28.0 -> 26.3, 200 of 512-1024 rows
 // 123 -> 122 and 174 -> 173).
 // scratch: 8 KB of shared memory that nobody uses yet.  All threads; returns the cuts in `mine`.
-// cta: the stretch that this block takes; store: it stores the plan.
 template <int THREADS>
-__device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine, int cta, bool store) {
+__device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t* scratch, int4* mine) {
   static_assert(THREADS >= kInlinePlanSeqs && THREADS > kPagedMaxCtas, "one thread per sequence and per cut");
   long long* pos = reinterpret_cast<long long*>(scratch);               // [kInlinePlanSeqs + 1]
   long long* warp_sum = pos + kInlinePlanSeqs + 1;                       // [THREADS / 32]
@@ -296,6 +295,7 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   __syncthreads();
   const long long total = pos[p.B];
   const int n_ctas = bad ? 0 : static_cast<int>(min(static_cast<long long>(p.sms), max(static_cast<long long>(units), total / p.min_work)));
+  const int cta = blockIdx.x;
   auto cut_at = [&](int c) { return bad ? make_int4(0, 0, 0, 0) : paged_inline_cut(p, pos, c, n_ctas); };
   if (cta < n_ctas) {
     if (tid == 0) mine[0] = cut_at(cta);
@@ -303,7 +303,7 @@ __device__ __forceinline__ void paged_inline_plan(const PagedParams& p, uint8_t*
   } else if (tid == 0) {
     mine[0] = mine[1] = make_int4(0, 0, 0, 0);
   }
-  if (store) {  // for the merge
+  if (cta == 0) {  // for the merge
     if (tid <= n_ctas) p.plan.cuts[tid] = cuts[tid] = cut_at(tid);
     __syncthreads();
     if (tid < n_ctas && cuts[tid].z != 0) {
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
   int4 cuts[2] = {make_int4(0, 0, 0, 0), make_int4(0, 0, 0, 0)};
   if (ONE && p.inline_plan) {
     int4* mine = reinterpret_cast<int4*>(&pieces[C::PIECES - 1]);  // not announced before the producer has read it
-    paged_inline_plan<C::THREADS>(p, sQ, mine, blockIdx.x, blockIdx.x == 0);
+    paged_inline_plan<C::THREADS>(p, sQ, mine);
     if (warp == 0) cuts[0] = mine[0], cuts[1] = mine[1];
   } else {
     pdl_wait();  // the plan comes from the kernel launched before

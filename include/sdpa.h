@@ -586,7 +586,7 @@ size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_
  * P is rounded to dtype for the product with the values, row sums take the fp32 probabilities.  Rows of a page at or past
  * kv_len never contribute and may hold anything; the visible rows must be finite.  Hq <= 128; latent_dim = 512, rotary_dim = 64;
  * page_size a power of two >= 16; pointers 16-byte aligned.  The kernels in `stream`: the plan (which the attention makes
- * itself for up to 256 sequences of one query tile), the attention, and the merge of divided tiles where the workspace
+ * itself for up to 256 sequences of few tokens), the attention, and the merge of divided tiles where the workspace
  * allows any.
  */
 int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_table, const int32_t* kv_len,
