@@ -1027,7 +1027,7 @@ def sdpa_fwd_latent_paged(q, pool, page_table, kv_len, cu_seqlens_q, max_seqlen_
     (customarily 1 / sqrt(nope + 64)).  Causal masking is bottom-right.  Returns (o [total_q,Hq,512], lse [Hq,total_q] fp32
     or None)."""
     n_pages, page_size, width = _check_latent_pool(pool)
-    if q.dim() != 3 or q.dtype != pool.dtype or q.shape[2] != width:
+    if q.dim() != 3 or q.dtype != pool.dtype or q.shape[2] != width or width <= 64:
         raise ValueError("q must be a packed [total_q, Hq, latent_dim + rotary_dim] tensor of the pool's type and width")
     total_q, Hq = q.shape[:2]
     _int32_vector("kv_len", kv_len)

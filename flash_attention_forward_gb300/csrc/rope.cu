@@ -245,6 +245,8 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
     if (!stride_ok(st[i], 8)) return SDPA_ERR_UNSUPPORTED;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3u) return SDPA_ERR_INVALID;
+  // an output's rows are places of their own
+  if ((total > 1 && (st[4] == 0 || (Hk > 0 && st[6] == 0))) || (Hq > 1 && st[5] == 0) || (Hk > 1 && st[7] == 0)) return SDPA_ERR_INVALID;
   // in place: the rows have to lie alike
   if ((q == q_out && (st[0] != st[4] || st[1] != st[5])) || (Hk > 0 && k == k_out && (st[2] != st[6] || st[3] != st[7])))
     return SDPA_ERR_INVALID;

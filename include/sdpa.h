@@ -521,7 +521,8 @@ int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t*
  *           i + rotary_dim / 2; else dims 2 i and 2 i + 1
  *   factor: finite; multiplies the turned dims (the attention factor of stretched contexts, else 1)
  *   strides: NULL for the contiguous layouts, else 8 element strides {q_s, q_h,  k_s, k_h,  q_out_s, q_out_h,  k_out_s,
- *           k_out_h}, multiples of 8; pointers 16-byte aligned.  D a multiple of 8.
+ *           k_out_h}, multiples of 8; an input's may be 0 (broadcast), an output's only where there is one token or one
+ *           head.  Pointers 16-byte aligned; D a multiple of 8.
  * One kernel.
  */
 int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,
@@ -656,9 +657,9 @@ int sdpa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
 /*
  * sdpa_check_device_status -- synchronizes `stream`, then reports and clears the device
  * status word the kernels raise when a bounded wait inside them gives up (a pipeline
- * stage that never arrived): SDPA_ERR_TIMEOUT in that case, SDPA_ERR_INVALID when a varlen
- * or paged call found bad sequence offsets or a cache call a row without a slot, SDPA_ERR_CUDA if the synchronization itself failed, else
- * SDPA_OK.  The status word is per device and per
+ * stage that never arrived): SDPA_ERR_TIMEOUT in that case, SDPA_ERR_INVALID when a varlen, paged
+ * or latent call found bad sequence offsets, a cache call a row without a slot or sdpa_cache_resize a change that
+ * cannot be made, SDPA_ERR_CUDA if the synchronization itself failed, else SDPA_OK.  The status word is per device and per
  * process, shared by all streams.
  */
 int sdpa_check_device_status(void* stream);

@@ -59,7 +59,9 @@ def test_rope_codes(lib):
                  dict(ko=ctypes.c_void_p(0x10008)), dict(strides=strides(516, 128, 256, 128, 512, 128, 256, 128)),
                  dict(strides=strides(512, 128, 256, 128, 512, -128, 256, 128)), dict(total=1 << 30)):
         assert call(**over) == UNSUPPORTED, over
-    # in place with other strides
+    # an output whose rows coincide; in place with other strides
+    assert call(qo=ctypes.c_void_p(0x20000), strides=strides(512, 128, 256, 128, 512, 0, 256, 128)) == INVALID
+    assert call(ko=ctypes.c_void_p(0x20000), strides=strides(512, 128, 256, 128, 512, 128, 0, 128)) == INVALID
     assert call(strides=strides(512, 128, 256, 128, 1024, 128, 256, 128)) == INVALID
     assert call(strides=strides(512, 128, 256, 128, 512, 128, 256, 136)) == INVALID
 
@@ -140,7 +142,7 @@ def test_binding_refuses_shapes_types_and_host_tensors():
         with pytest.raises(ValueError):
             fa.sdpa_latent_write(*args)
     q = h(5, 4, 576)
-    for args in ((h(5, 576), pool, i(2, 3), i(2), i(3)), (q.half(), pool, i(2, 3), i(2), i(3)), (h(5, 4, 512), pool, i(2, 3), i(2), i(3)),
+    for args in ((h(5, 4, 64), h(3, 16, 64), i(2, 3), i(2), i(3)), (h(5, 576), pool, i(2, 3), i(2), i(3)), (q.half(), pool, i(2, 3), i(2), i(3)), (h(5, 4, 512), pool, i(2, 3), i(2), i(3)),
                  (q, pool, i(3, 3), i(2), i(3)), (q, pool, i(2, 3), i(2), i(2)), (q, pool, i(2, 3), i(2), i(3))):
         with pytest.raises(ValueError):
             fa.sdpa_fwd_latent_paged(*args, 5, scale=0.1)

@@ -127,6 +127,15 @@ def test_in_place_and_views_of_a_part_of_the_head(interleaved):
     assert (pad == 5.0).all()
 
 
+def test_broadcast_inputs_and_shared_positions():
+    # one rotary key read as that of four heads; the input of all tokens one row
+    q, k, pos = case(9, 4, 1, 64, torch.float16, seed=5)
+    inv_freq = fa.sdpa_rope_frequencies(64)[0].to(DEV)
+    got_q, got_k = fa.sdpa_rope(q[:1].expand(9, -1, -1), k.expand(-1, 4, -1), pos, inv_freq)
+    close(got_q, *turned(q[:1].expand(9, -1, -1), pos, inv_freq, False), torch.float16)
+    close(got_k, *turned(k.expand(-1, 4, -1), pos, inv_freq, False), torch.float16)
+
+
 def test_gradient():
     # y = R x is linear: its gradient R^T g is the call with -positions; against the formula and against differences
     x, g, pos = case(50, 4, 4, 64, torch.float16, seed=4)
