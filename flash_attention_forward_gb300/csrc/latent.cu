@@ -777,7 +777,9 @@ int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_t
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < 6; ++i)
     if (!stride_ok(st[i], 8)) return SDPA_ERR_UNSUPPORTED;
-  if (st[6] < max_pages) return SDPA_ERR_INVALID;
+  if (st[6] < max_pages || rows_coincide(total_q, st[4]) || rows_coincide(Hq, st[5])) return SDPA_ERR_INVALID;
+  if (rows_coincide(total_q, st[0]) || rows_coincide(Hq, st[1]) || rows_coincide(n_pages, st[2]) || rows_coincide(page_size, st[3]))
+    return SDPA_ERR_UNSUPPORTED;  // no tensor map of such a layout
   if (!aligned16(q) || !aligned16(pool) || !aligned16(o)) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(page_table) | reinterpret_cast<uintptr_t>(kv_len) |
        reinterpret_cast<uintptr_t>(cu_seqlens_q) | reinterpret_cast<uintptr_t>(lse)) & 3u)

@@ -334,6 +334,10 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < SDPA_FWD_LATENT_NSTRIDES; ++i)
     if (!stride_ok(st[i], 8)) return SDPA_ERR_UNSUPPORTED;
+  if (rows_coincide(total_q, st[7]) || rows_coincide(Hq, st[8])) return SDPA_ERR_INVALID;
+  if (rows_coincide(total_q, st[0]) || rows_coincide(Hq, st[1]) || rows_coincide(total_k, st[2]) || rows_coincide(Hkv, st[3]) ||
+      rows_coincide(total_k, st[4]) || rows_coincide(total_k, st[5]) || rows_coincide(Hkv, st[6]))
+    return SDPA_ERR_UNSUPPORTED;  // no tensor map of such a layout
   if (!aligned16(q) || !aligned16(k_nope) || !aligned16(k_rope) || !aligned16(v) || !aligned16(o)) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k) | reinterpret_cast<uintptr_t>(lse)) & 3u)
     return SDPA_ERR_INVALID;

@@ -246,7 +246,8 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3u) return SDPA_ERR_INVALID;
   // an output's rows are places of their own
-  if ((total > 1 && (st[4] == 0 || (Hk > 0 && st[6] == 0))) || (Hq > 1 && st[5] == 0) || (Hk > 1 && st[7] == 0)) return SDPA_ERR_INVALID;
+  if (rows_coincide(total, st[4]) || rows_coincide(Hq, st[5]) || (Hk > 0 && rows_coincide(total, st[6])) || rows_coincide(Hk, st[7]))
+    return SDPA_ERR_INVALID;
   // in place: the rows have to lie alike
   if ((q == q_out && (st[0] != st[4] || st[1] != st[5])) || (Hk > 0 && k == k_out && (st[2] != st[6] || st[3] != st[7])))
     return SDPA_ERR_INVALID;
@@ -292,6 +293,7 @@ int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < SDPA_LATENT_WRITE_NSTRIDES; ++i)
     if (!stride_ok(st[i], 8)) return SDPA_ERR_UNSUPPORTED;
+  if (rows_coincide(n_pages, st[2]) || rows_coincide(page_size, st[3])) return SDPA_ERR_INVALID;
   if (!aligned16(c) || !aligned16(k_rope) || !aligned16(pool)) return SDPA_ERR_UNSUPPORTED;
   if ((reinterpret_cast<uintptr_t>(slots) & 7u) ||
       ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) & 3u))

@@ -489,7 +489,7 @@ size_t sdpa_cache_resize_workspace_size(int B, int total, int max_pages);
  *           sdpa_cache_write_fp8, sdpa_fwd_paged* and sdpa_fwd_latent_paged (with kv_len_out)
  *   positions [total] DEVICE int32, slots [total] DEVICE int64, written: position of each new token in its sequence,
  *           and its cache row page * page_size + position % page_size, for sdpa_rope and sdpa_latent_write.
- *           total >= the sum of the new tokens; entries behind it are position 0, slot -1 (no row)
+ *           total >= the sum of the new tokens, and 1 at least; entries behind the sum are position 0, slot -1 (no row)
  *   workspace: sdpa_cache_resize_workspace_size(B, total, max_pages) bytes, 16-byte aligned (NULL where that is 0);
  *           calls that overlap on the GPU need separate ones
  *
@@ -548,7 +548,7 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
  *   positions [total] DEVICE int32, inv_freq [rotary_dim / 2], interleaved, factor: as in sdpa_rope; both pointers NULL: the
  *           rotary part is stored as it is
  *   strides: NULL for the contiguous layouts, else 4 element strides {c_s, k_rope_s, pool page, row}, multiples
- *           of 8; c, k_rope and pool 16-byte aligned.  page_size: a power of two >= 16.
+ *           of 8, the first two may be 0; c, k_rope and pool 16-byte aligned.  page_size: a power of two >= 16.
  * One kernel.
  */
 int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64_t* slots, const int32_t* positions,
@@ -580,7 +580,7 @@ size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_
  *   pool [n_pages, page_size, latent_dim + rotary_dim]  dtype: a latent cache
  *   lse, page_table, kv_len, cu_seqlens_q, max_seqlen_q, bad offsets: as in sdpa_fwd_paged
  *   strides: NULL for the contiguous layouts, else 7 element strides {q_s, q_h,  pool page, row,  o_s, o_h,  page_table row},
- *           the first six multiples of 8
+ *           the first six multiples of 8, not 0 where there are two rows or more
  *   workspace: see sdpa_fwd_latent_paged_workspace_size; 16-byte aligned, contents on entry irrelevant.  Calls that
  *           overlap on the GPU need separate workspaces.
  *
@@ -621,7 +621,7 @@ size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int m
  *           n_b and <= total_q.  Offsets that break this make the call store nothing and raise a status that
  *           sdpa_check_device_status() reports as SDPA_ERR_INVALID.
  *   strides: NULL for the contiguous layouts, else 9 element strides {q_s, q_h,  k_nope_s, k_nope_h,  k_rope_s,  v_s, v_h,
- *           o_s, o_h}, multiples of 8 (k_nope and v may be views of one expanded tensor)
+ *           o_s, o_h}, multiples of 8, not 0 where there are two rows or more (k_nope and v may be views of one expanded tensor)
  *   workspace: see sdpa_fwd_latent_workspace_size; 16-byte aligned.  Calls that overlap on the GPU need separate ones.
  *
  * nope = 128, rotary_dim = 64, Dv = 128; Hq / Hkv <= 128; pointers 16-byte aligned.  Keys and values some sequence owns must be

@@ -151,3 +151,22 @@ def test_binding_refuses_shapes_types_and_host_tensors():
                  (q, kn, h(7, 32), v, i(2), i(2)), (q, kn, r, v.half(), i(2), i(2)), (q, kn, r, v, i(2), i(3)), (q, kn, r, v, i(2), i(2))):
         with pytest.raises(ValueError):
             fa.sdpa_fwd_latent(*args, 5)
+
+
+def test_inputs_and_outputs_whose_rows_coincide(lib):
+    """A broadcast view handed to an entry that cannot take it is refused before anything runs."""
+    absorbed = caller(lib.sdpa_fwd_latent_paged, q=FAKE, pool=FAKE, table=FAKE, kv=FAKE, cu=FAKE, o=FAKE, lse=None, B=2, Hq=16, total=10,
+                      maxq=6, page=64, max_pages=8, n_pages=20, latent=512, rot=64, strides=None, scale=F(0.1), causal=1, ws=FAKE,
+                      wsb=SZ(1 << 30), dt=fa.SDPA_BF16, stream=None)
+    expanded = caller(lib.sdpa_fwd_latent, q=FAKE, k=FAKE, r=FAKE, v=FAKE, cq=FAKE, ck=FAKE, o=FAKE, lse=None, B=2, Hq=16, Hkv=16, tq=10,
+                      tk=20, maxq=6, nope=128, rot=64, Dv=128, strides=None, scale=F(0.1), causal=1, ws=FAKE, wsb=SZ(1 << 30),
+                      dt=fa.SDPA_F16, stream=None)
+    write = caller(lib.sdpa_latent_write, c=FAKE, r=FAKE, pool=FAKE, slots=FAKE, pos=FAKE, inv=FAKE, total=10, page=64, n_pages=4,
+                   latent=512, rot=64, inter=0, factor=F(1.0), strides=None, dt=fa.SDPA_BF16, stream=None)
+    for call, full, outputs in ((absorbed, (16 * 576, 576, 64 * 576, 576, 16 * 512, 512, 8), (4, 5)),
+                                (expanded, (16 * 192, 192, 16 * 128, 128, 64, 16 * 128, 128, 16 * 128, 128), (7, 8))):
+        for at in range(len(full) - (call is absorbed)):
+            flat = [0 if i == at else x for i, x in enumerate(full)]
+            assert call(strides=strides(*flat)) == (INVALID if at in outputs else UNSUPPORTED), (at, flat)
+    for at in (2, 3):
+        assert write(strides=strides(*(0 if i == at else x for i, x in enumerate((512, 64, 64 * 576, 576))))) == INVALID

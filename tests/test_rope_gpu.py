@@ -209,6 +209,16 @@ def test_latent_write_reports_slots_behind_the_pool():
     assert (pool[0, 3] == 1).all() and pool.float().sum() == 576 and fa.sdpa_check_device_status() == fa.SDPA_OK
 
 
+def test_latent_write_of_one_row_to_many_slots():
+    g = torch.Generator().manual_seed(2)
+    c, r = torch.randn((1, 512), generator=g).half().to(DEV), torch.randn((1, 64), generator=g).half().to(DEV)
+    pool = torch.zeros((3, 16, 576), dtype=torch.float16, device=DEV)
+    slots = torch.arange(5, 45, device=DEV)
+    fa.sdpa_latent_write(c.expand(40, -1), r.expand(40, -1), pool, slots)
+    rows = pool.view(-1, 576)
+    assert (rows[5:45] == torch.cat([c, r], 1)).all() and not rows[:5].any() and not rows[45:].any()
+
+
 def test_latent_write_past_32_bits():
     n_pages = (1 << 32) // (576 * 2 * 256) + 20   # the last pages lie behind 2^32 bytes
     pool = torch.zeros((n_pages, 256, 576), dtype=torch.bfloat16, device=DEV)
