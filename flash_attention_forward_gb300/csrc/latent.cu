@@ -26,7 +26,8 @@
 //
 // What bounds it.  16 heads: memory.  A block takes 3.4 us an SM, 6.5 TB/s, 97% of the copy rate; 64 sequences of 1024-16384
 // rows take 123 us in all (5.2 TB/s), 11 being the start and the first loads, 10 the last pieces and the merge.  64 columns:
-// the issuing thread.  An MMA of 128 rows takes 49 cycles whatever the columns up to 64 (64 for 128), so a block's 68 are
+// the chain of the two products and the softmax between them, as there is room for a single block of keys beside the queries.  An
+// MMA of 128 rows takes the tensor core 49 cycles whatever the columns up to 64 (64 for 128), so a block's 68 are
 // 3400 of its 6500 cycles; 1700 pass between the last score's MMA and the first of P V (16 softmax warps: 210 to wake, 260 to
 // load, 570 of arithmetic, 170 for the vote, 130 for the fence, 400 until the issuer sees the last arrival), the rest are waits
 // and commits.  128 heads over the same sequences: 210 us, 740 TFLOP/s, 3.1 TB/s.

@@ -130,6 +130,25 @@ def test_expanded_other_sequences_rows_and_the_rest_of_the_output():
         assert torch.equal(o[rows], want[0][rows]) and torch.equal(lse[:, rows], want[1][:, rows])
 
 
+def test_expanded_past_32_bits():
+    # the sequences' rows lie behind 2^32 bytes, and 2^31 values, of every tensor with heads
+    H, new, lens = 128, [40, 1, 300], [40, 700, 301]
+    total = (1 << 31) // (H * 128) + 1100
+    q, k, r, v = packed(new, lens, H, H, "bf16", seed=3)
+    wide_q = torch.empty((total, H, 192), dtype=q.dtype, device=DEV)
+    wide_kv = torch.empty((total, H, 256), dtype=q.dtype, device=DEV)
+    wide_r = torch.empty((total, 64), dtype=q.dtype, device=DEV)
+    q0, k0 = total - sum(new), total - sum(lens)
+    wide_q[q0:], wide_kv[k0:, :, :128], wide_kv[k0:, :, 128:], wide_r[k0:] = q, k, v, r
+    out = torch.full((total, H, 128), 9.0, dtype=q.dtype, device=DEV)
+    cu_q, cu_k = offsets(new) + q0, offsets(lens) + k0
+    o, lse = fa.sdpa_fwd_latent(wide_q, wide_kv[..., :128], wide_r, wide_kv[..., 128:], cu_q.to(DEV), cu_k.to(DEV), 300,
+                                scale=0.07, causal=True, out=out)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    check_expanded(q, k, r, v, new, lens, o[q0:], lse[:, q0:], 0.07, True)
+    assert (out[:q0] == 9).all()
+
+
 def test_expanded_equals_the_packed_prefill_with_repeated_keys():
     # equal lengths: bottom-right and top-left masking are one; the same problem with the shared part repeated
     lens = [300, 17, 1000]
