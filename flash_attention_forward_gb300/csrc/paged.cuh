@@ -170,7 +170,7 @@ struct PagedWalk {
     return w;
   }
   // Item i of the list: a whole unit.
-  __device__ __forceinline__ static PagedPiece item(const PagedParams& p, int i, int n_items) {
+  __host__ __device__ __forceinline__ static PagedPiece item(const PagedParams& p, int i, int n_items) {
     const int tiles = n_items / p.Hkv, per = tiles * p.list_heads;
     const int g = i / per, heads = min(p.list_heads, p.Hkv - g * p.list_heads);
     const int r = i - g * per, rank = r / heads;
@@ -1393,9 +1393,8 @@ cudaError_t launch_paged_one(const CUtensorMap& tq, const CUtensorMap& tk, const
 template <bool BF16, bool QUANT, int D, int DV>
 cudaError_t launch_paged_instance(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                   const PagedParams& p, cudaStream_t st) {
-  // three-block operands leave no room for two readers' rings beside the raw codes
-  if constexpr (!(QUANT && D == 192))
-    if (p.max_seqlen_q <= p.tok_tile) return launch_paged_one<BF16, QUANT, D, DV, true, false>(tq, tk, tv, tv, p, st);
+  if constexpr (!(QUANT && D == 192))  // as paged_choose has it
+    if (p.one) return launch_paged_one<BF16, QUANT, D, DV, true, false>(tq, tk, tv, tv, p, st);
   return launch_paged_one<BF16, QUANT, D, DV, false, false>(tq, tk, tv, tv, p, st);
 }
 

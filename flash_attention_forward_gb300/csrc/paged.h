@@ -80,7 +80,8 @@ struct PagedParams {
   float* part_ml;          // ... and (max, sum) [slot][slot_rows][2]
   uint32_t* status;
   int B, Hq, Hkv, total_q, max_seqlen_q, group, causal;
-  int list_heads;          // packed keys: KV heads that the list takes at a time
+  int one;                 // the kernel for sequences of one query tile (see paged_choose)
+  int list_heads;          // packed keys: KV heads that the list takes at a time; 0: work is never a list
   int tok_tile;            // tokens per 128-row query tile: 128 / group
   int page_size, log2_page, max_pages, n_pages;
   int max_kv;              // max_pages * page_size, or total_k
@@ -93,6 +94,21 @@ struct PagedParams {
   float scale2;            // scale * log2(e)
   FastDiv div_group;
 };
+
+// Which kernel a call gets and which plans go with it.  The kernel for one query tile a sequence walks a line with cuts and
+// knows no list; it plans for itself where the sequences are few.  The other one takes a list where its keys are packed.
+// Everything that depends on the choice (launch, boxes, planning kernel) asks what this has written.  head_bytes: keys and
+// values of a head where they are packed, else 0.
+inline void paged_choose(PagedParams& p, bool quant, int D, int64_t head_bytes) {
+  // three-block operands leave no room for two readers' rings beside the raw codes
+  p.one = !(quant && D == 192) && p.max_seqlen_q <= p.tok_tile;
+  p.inline_plan = p.one && p.B <= kInlinePlanSeqs;
+  p.list_heads = 0;
+  if (head_bytes > 0 && !p.one) {
+    const int64_t heads = kListBytes / head_bytes;
+    p.list_heads = static_cast<int>(heads < 1 ? 1 : heads < p.Hkv ? heads : p.Hkv);
+  }
+}
 
 // Key blocks that query tile `tile` (tok_tile tokens) of a sequence sees: 0 past its last token, else
 // at least 1 (a tile without visible keys runs one masked block and stores O = 0, LSE = -inf).
@@ -118,6 +134,10 @@ __host__ __device__ __forceinline__ int plan_ld(const int32_t* p) {
 #else
   return *p;
 #endif
+}
+// Whether the planning kernel leaves a list.
+__host__ __device__ __forceinline__ bool paged_is_list(const PagedParams& p, long long n_tiles) {
+  return p.list_heads > 0 && n_tiles * p.Hkv >= static_cast<long long>(kListUnits) * p.sms;
 }
 // Keys of sequence b.
 __host__ __device__ __forceinline__ int paged_len(const PagedParams& p, int b) {

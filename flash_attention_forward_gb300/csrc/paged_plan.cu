@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PagedPar
   __syncthreads();
   const long long* pos = small ? s_pos : p.plan.tile_pos;
   const int2* tiles = small ? s_tile : p.plan.tiles;
-  if (p.list_heads > 0 && n_tiles * p.Hkv >= static_cast<long long>(kListUnits) * p.sms) {
+  if (paged_is_list(p, n_tiles)) {
     // a list: the tiles longest first (as they lie where shared memory does not hold them)
     if (small) {
       auto length = [&](int i) { return (i + 1 < n_tiles ? s_pos[i + 1] : total) - s_pos[i]; };
@@ -278,7 +278,7 @@ int fwd_paged(bool quant, const void* q, const void* k_pool, const void* v_pool,
   p.slot_rows = slot_rows(group, max_seqlen_q);
   p.cut = partials > 0 && workspace_bytes >= plan + partials;
   p.max_tiles = (int)tiles;
-  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= p.tok_tile && !(quant && D == 192);
+  paged_choose(p, quant, D, 0);
   p.plan = paged_plan_at(workspace, tiles);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
   p.part_ml = p.part_o + 2ull * kPagedMaxCtas * p.slot_rows * Dv;
@@ -349,7 +349,6 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   PagedParams p{};
   p.o = o, p.lse = lse, p.o_s = st[7], p.o_h = st[8];
   p.cu_q = cu_q, p.cu_k = cu_k;
-  p.list_heads = (int)std::max<int64_t>(1, std::min<int64_t>(Hkv, kListBytes / ((int64_t)total_k * (nope + Dv) * 2)));
   p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.total_q = total_q, p.max_seqlen_q = max_seqlen_q, p.group = group;
   p.causal = causal ? 1 : 0;
   p.tok_tile = kBlockQ / group;
@@ -359,7 +358,7 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   p.slot_rows = slot_rows(group, max_seqlen_q);
   p.cut = partials > 0 && workspace_bytes >= plan + partials;
   p.max_tiles = (int)tiles;
-  p.inline_plan = B <= kInlinePlanSeqs && max_seqlen_q <= p.tok_tile;
+  paged_choose(p, false, D, (int64_t)total_k * (nope + Dv) * 2);
   p.plan = paged_plan_at(workspace, tiles);
   p.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
   p.part_ml = p.part_o + 2ull * kPagedMaxCtas * p.slot_rows * Dv;
@@ -373,7 +372,7 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   auto rows = [&](CUtensorMap* map, const void* x, int H, int dim, int64_t s, int64_t h, int box_rows) {
     return encode_bshd(map, x, dt, 2, 1, total_k, H, dim, s, s, h, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
   };
-  const int v_rows = max_seqlen_q <= p.tok_tile ? kBlockK : kBlockK / 2;  // the long chunks' kernel loads V by halves
+  const int v_rows = p.one ? kBlockK : kBlockK / 2;  // the long chunks' kernel loads V by halves
   if (!encode_q(&tq, q, bf16, total_q, Hq, D, st[0], st[1], group) || !rows(&tk, k_nope, Hkv, nope, st[2], st[3], kBlockK) ||
       !rows(&tv, v, Hkv, Dv, st[5], st[6], v_rows) || !rows(&tr, k_rope, 1, rot, st[4], rot, kBlockK))
     return SDPA_ERR_CUDA;
