@@ -497,15 +497,24 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
           float nm[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) nm[c] = neg_max[c];
+          const float nm_l = neg_max[lane % NC];
           if (barrier_any(bar_id, 128, !ok)) {
             ok = false;
             break;
           }
+          auto block_max = [&](int c) {
+            return fmaxf(fmaxf(red_max[c], red_max[NC + c]), fmaxf(red_max[2 * NC + c], red_max[3 * NC + c]));
+          };
+          // A column with a score of +infinity takes that as its maximum (its P is NaN or 0 from here on, and it asks for no
+          // further vote), but moves no other: an infinite query does not touch the rounding of the rows beside it.  So whether
+          // a finite score passed its column's maximum is asked again, a column a lane.
+          const float mb_l = block_max(lane % NC);
+          const bool far = __any_sync(0xffffffffu, mb_l * p.scale2 < INFINITY && fmaf(mb_l, p.scale2, nm_l) > kPagedRescaleLog2);
           float alpha[NC];
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
-            const float mb = fmaxf(fmaxf(red_max[c], red_max[NC + c]), fmaxf(red_max[2 * NC + c], red_max[3 * NC + c]));
-            const float neg = fminf(nm[c], -(mb * p.scale2));
+            const float least = fminf(nm[c], -(block_max(c) * p.scale2));
+            const float neg = far || least == -INFINITY ? least : nm[c];
             alpha[c] = neg == nm[c] ? 1.f : ex2(neg - nm[c]);
             if (row == c) neg_max[c] = neg;
             l[c] *= alpha[c];
@@ -552,24 +561,27 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       if (row < NC) {
         // this thread's column: where its row of O goes (among the partials or to O; < 0: nowhere), its factor
         const int t = static_cast<int>(fast_div(static_cast<uint32_t>(col0 + row), lp.div_heads));
-        const int h = hg * lp.group_heads + col0 + row - t * lp.group_heads;
+        const int h = col0 + row - t * lp.group_heads;  // of the group
         const float neg = neg_max[row];
-        const float sum = (red_sum[row] + red_sum[NC + row]) + (red_sum[2 * NC + row] + red_sum[3 * NC + row]);
+        float sum = (red_sum[row] + red_sum[NC + row]) + (red_sum[2 * NC + row] + red_sum[3 * NC + row]);
+        // a score of +infinity: where only its product with the scale was, the sum is 0
+        if (neg == -INFINITY) sum = __uint_as_float(0x7FC00000u);
         int64_t at = -1;
-        if (neg != -INFINITY) {
+        if (t < tokens && h < heads) {
+          const int head = hg * lp.group_heads + h;
           if (partial) {
-            const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.Hq + h;
+            const int64_t prow = static_cast<int64_t>(slot) * p.slot_rows + t * p.Hq + head;
             at = prow * kLatentDim;
             *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(-neg, sum);
           } else {
             const int q_row = q_off + tok0 + t;
-            at = q_row * p.o_s + h * p.o_h;
+            at = q_row * p.o_s + head * p.o_h;
             if (p.lse != nullptr)
-              p.lse[static_cast<int64_t>(h) * p.total_q + q_row] = sum > 0.f ? (lg2(sum) - neg) * kPagedLn2 : -INFINITY;
+              p.lse[static_cast<int64_t>(head) * p.total_q + q_row] = sum == 0.f ? -INFINITY : (lg2(sum) - neg) * kPagedLn2;
           }
         }
         row_at[row] = at;
-        row_inv[row] = partial ? 1.f : sum > 0.f ? 1.f / sum : 0.f;
+        row_inv[row] = partial ? 1.f : sum == 0.f ? 0.f : 1.f / sum;  // NaN stays NaN
       }
       ok = mbar_wait_warp(o_full, on & 1, abort_flag, p.status);
       ++on;
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(64 * kLatentMergeRows) latent_combine_kernel(c
       for (int c = 0; c < 8; ++c) acc[c] += wi * v[c];
     }
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // NaN stays NaN
   const int head = row - row_tok * p.group;
   uint16_t* o = static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_off + tok) * p.o_s + static_cast<int64_t>(head) * p.o_h + col;
 #pragma unroll
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(64 * kLatentMergeRows) latent_combine_kernel(c
              : make_uint2(pack_f16x2(a[0] * inv, a[1] * inv), pack_f16x2(a[2] * inv, a[3] * inv));
   }
   if (p.lse != nullptr && col == 0)
-    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L > 0.f ? (M + lg2(L)) * kPagedLn2 : -INFINITY;
+    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L == 0.f ? -INFINITY : (M + lg2(L)) * kPagedLn2;
 }
 
 cudaError_t launch_latent_combine(bool bf16, const PagedParams& p, cudaStream_t st) {
