@@ -1302,7 +1302,9 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
       if (n_other > 0) ++on[1 - t];
       tc_fence_after();
       const bool partial = w.slot >= 0;
-      const float inv = partial ? 1.f : (l > 0.f ? 1.f / l : 0.f);
+      // a score of +infinity: where only its product with the scale was, the sum is 0
+      if (m_used == INFINITY) l = __uint_as_float(0x7FC00000u);
+      const float inv = partial ? 1.f : (l == 0.f ? 0.f : 1.f / l);  // NaN stays NaN
       w0 *= inv, w1 *= inv;
       const int64_t prow = static_cast<int64_t>(w.slot) * p.slot_rows + qt * kBlockQ + row;
       const int head = w.kvh * p.group + row_head;
@@ -1352,7 +1354,7 @@ __global__ void __launch_bounds__(PagedCfg<QUANT, D, DV, ONE>::THREADS, 1)
         if (partial)
           *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m_used, l);
         else if (p.lse != nullptr)
-          p.lse[static_cast<int64_t>(head) * p.total_q + q_row] = l > 0.f ? (m_used + lg2(l)) * kPagedLn2 : -INFINITY;
+          p.lse[static_cast<int64_t>(head) * p.total_q + q_row] = l == 0.f ? -INFINITY : (m_used + lg2(l)) * kPagedLn2;
       }
     }
   }

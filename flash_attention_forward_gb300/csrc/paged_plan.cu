@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = acc[c] * w0 + w1 * v[c];
   }
-  const float inv = L > 0.f ? 1.f / L : 0.f;
+  const float inv = L == 0.f ? 0.f : 1.f / L;  // NaN stays NaN
   uint32_t pk[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kMergeRows * DV / 8) paged_combine_kernel(cons
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + static_cast<int64_t>(q_off + tok) * p.o_s +
                             static_cast<int64_t>(head) * p.o_h + col) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
   if (p.lse != nullptr && col == 0)
-    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L > 0.f ? (M + lg2(L)) * 0.6931471805599453f : -INFINITY;
+    p.lse[static_cast<int64_t>(head) * p.total_q + q_off + tok] = L == 0.f ? -INFINITY : (M + lg2(L)) * 0.6931471805599453f;
 }
 
 // Work tiles that calls of these sizes can have.

@@ -438,7 +438,9 @@ size_t sdpa_fwd_paged_workspace_size(int B, int Hq, int Hkv, int total_q, int ma
  *           Calls that overlap on the GPU need separate workspaces.
  *
  * Rows of a page at or past kv_len never contribute and may hold anything; the visible rows must be
- * finite.  (D, Dv) in {(64, 64), (128, 128), (192, 128)}; Hq / Hkv <= 128; page_size a power of
+ * finite.  Queries over 16-bit pages need not be: a (token, head) with a NaN or +infinity among its scores, in fp32
+ * and times scale * log2(e), has NaN in O and LSE; a score of -infinity is a hidden key's.
+ * (D, Dv) in {(64, 64), (128, 128), (192, 128)}; Hq / Hkv <= 128; page_size a power of
  * two >= 16; pointers 16-byte aligned; total_q >= 1.  The kernels in `stream`: the plan (which the attention makes
  * itself for up to 256 sequences of max_seqlen_q <= 128 / (Hq / Hkv) tokens; not over quantised pages with D = 192),
  * the attention, and the merge of divided tiles where the workspace allows any.
@@ -627,7 +629,7 @@ size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int m
  *   workspace: see sdpa_fwd_latent_workspace_size; 16-byte aligned.  Calls that overlap on the GPU need separate ones.
  *
  * nope = 128, rotary_dim = 64, Dv = 128; Hq / Hkv <= 128; pointers 16-byte aligned.  Keys and values some sequence owns must be
- * finite.  The kernels are those of sdpa_fwd_paged.
+ * finite; queries as in sdpa_fwd_latent_paged.  The kernels are those of sdpa_fwd_paged.
  */
 int sdpa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_seqlens_q,
                     const int32_t* cu_seqlens_k, void* o, float* lse, int B, int Hq, int Hkv, int total_q, int total_k,

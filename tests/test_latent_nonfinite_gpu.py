@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import flash_attention_forward_gb300 as fa
-from test_latent_gpu import DEV, cache, check_absorbed
+from test_latent_gpu import DEV, cache, check_absorbed, check_expanded, offsets, packed
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +79,66 @@ def test_absorbed(kind, Hq, new, lens, rows):
 @pytest.mark.parametrize("kind", ["inf", "nan", "hidden"])   # fp16 holds no value whose scores overflow
 def test_absorbed_f16(kind):
     absorbed_case([1, 3], [700, 60], 16, kind, [(0, 2), (3, 15)], "f16")
+
+
+def expanded_case(new, lens, Hq, Hkv, kind, rows, dtype):
+    scale = 1.0 if kind == "scaled" else 0.05
+    q, k, r, v = packed(new, lens, Hq, Hkv, dtype, seed=Hq + len(new))
+    k[..., 7:9] = 1.0
+    q = clean(q, scale)
+    cu_q, cu_k = offsets(new).to(DEV), offsets(lens).to(DEV)
+
+    def call(q):
+        size = fa.sdpa_fwd_latent_workspace_size(len(new), Hq, Hkv, q.shape[0], max(new), k.shape[0])
+        out = torch.full((q.shape[0], Hq, 128), 5.0, dtype=q.dtype, device=DEV)
+        lse = torch.full((Hq, q.shape[0]), 5.0, device=DEV)
+        fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, max(new), scale=scale, causal=True, out=out, lse=lse,
+                           workspace=torch.zeros(size, dtype=torch.uint8, device=DEV))
+        assert fa.sdpa_check_device_status() == fa.SDPA_OK
+        return out, lse
+
+    want = call(q)
+    check_expanded(q, k, r, v, new, lens, *want, scale, True)
+    o, lse = call(poison(q, rows, kind))
+    check_rows(rows, kind, (o, lse), want, False)
+    # the others are rescaled together with the rows of their warp, so they are right within the tolerance
+    for t, h in rows:
+        o[t, h], lse[h, t] = want[0][t, h], want[1][h, t]
+    check_expanded(q, k, r, v, new, lens, o, lse, scale, True)
+
+
+# one tile a sequence (both accumulators, whole and cut), two tiles (whole and cut), a list
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("Hq,Hkv,new,lens,rows", [(4, 4, [3, 1, 60], [100, 1, 600], [(0, 0), (3, 3), (40, 1)]), (8, 1, [4, 1], [9000, 5000], [(0, 0), (4, 7)]),
+                                                  (2, 2, [300, 5], [300, 700], [(0, 0), (200, 1), (299, 0), (304, 1)]), (6, 2, [500], [6000], [(0, 0), (499, 5)]),
+                                                  (80, 80, [600, 1, 130, 300, 257, 900], [700, 1, 130, 900, 300, 900], [(0, 0), (600, 79), (1100, 40)])])
+def test_expanded(kind, Hq, Hkv, new, lens, rows):
+    expanded_case(new, lens, Hq, Hkv, kind, rows, "bf16")
+
+
+@pytest.mark.parametrize("kind", ["inf", "nan", "hidden"])
+def test_expanded_f16(kind):
+    expanded_case([1, 3], [700, 60], 4, 4, kind, [(0, 2), (3, 3)], "f16")
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+@pytest.mark.parametrize("new,lens,Hq,Hkv", [([1, 3], [700, 60], 8, 2), ([200, 5], [300, 9000], 4, 4), ([2], [20000], 4, 1)])
+def test_chunks_over_pages(kind, new, lens, Hq, Hkv):
+    # the same kernels over pages: one page a sequence
+    scale, page = 1.0 if kind == "scaled" else 0.05, 1 << max(lens).bit_length()
+    g = torch.Generator().manual_seed(Hq)
+    q = clean(torch.randn((sum(new), Hq, 128), generator=g).bfloat16().to(DEV), scale)
+    k, v = (torch.randn((len(new), page, Hkv, 128), generator=g).bfloat16().to(DEV) for _ in range(2))
+    k[..., 7:9] = 1.0
+    table = torch.arange(len(new), dtype=torch.int32, device=DEV)[:, None]
+    kv, cu = torch.tensor(lens, dtype=torch.int32, device=DEV), offsets(new).to(DEV)
+    rows = [(0, 0), (sum(new) - 1, Hq - 1)]
+    want = fa.sdpa_fwd_paged(q, k, v, table, kv, cu, max(new), scale=scale, causal=True)
+    assert torch.isfinite(want[0]).all() and torch.isfinite(want[1]).all()
+    got = fa.sdpa_fwd_paged(poison(q, rows, kind), k, v, table, kv, cu, max(new), scale=scale, causal=True)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
+    check_rows(rows, kind, got, want, False)
+    keep = torch.ones(want[1].shape, dtype=torch.bool, device=DEV)
+    for t, h in rows:
+        keep[h, t] = False
+    assert torch.isfinite(got[0].transpose(0, 1)[keep]).all() and torch.isfinite(got[1][keep]).all()
