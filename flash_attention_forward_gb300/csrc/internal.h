@@ -298,6 +298,8 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // Strides usable by a tensor map / 16-byte vector access: positive multiples of `mult` (a
 // stride of a size-1 dimension only needs the multiple).
 inline bool stride_ok(int64_t s, int64_t mult) { return s >= 0 && s % mult == 0 && s < (int64_t(1) << 36); }
+// Tokens, sequences or heads of a call, so that a kernel's 32-bit counts of them may pass their end by a block.
+constexpr int kMaxCount = 1 << 30;
 // n rows of stride s that all lie in one place.
 inline bool rows_coincide(int n, int64_t s) { return n > 1 && s == 0; }
 // Page sizes and counts of a paged cache: 0 or the public status code.

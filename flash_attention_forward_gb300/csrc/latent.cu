@@ -766,7 +766,7 @@ extern "C" {
 
 size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_seqlen_q, int max_kv) {
   if (B < 1 || Hq < 1 || Hq > 2 * kLatentMaxRows || total_q < 1 || max_seqlen_q < 1 || max_seqlen_q > total_q || max_kv < 1 ||
-      max_kv > (1 << 30))
+      max_kv > (1 << 30) || B > kMaxCount || total_q > kMaxCount)
     return 0;
   const LatentTile t = latent_tile(Hq, max_seqlen_q);
   return paged_plan_bytes(B, latent_tiles(B, total_q, max_seqlen_q, t.tok_tile)) + latent_partial_bytes(t, Hq, max_kv);
@@ -784,7 +784,8 @@ int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_t
   const int rc = page_check(page_size, max_pages, n_pages);
   if (rc != SDPA_OK) return rc;
   if (dtype != SDPA_F16 && dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
-  if (latent_dim != kLatentDim || rotary_dim != kLatentRot || Hq > 2 * kLatentMaxRows) return SDPA_ERR_UNSUPPORTED;
+  if (latent_dim != kLatentDim || rotary_dim != kLatentRot || Hq > 2 * kLatentMaxRows || B > kMaxCount || total_q > kMaxCount)
+    return SDPA_ERR_UNSUPPORTED;
   int64_t st[SDPA_FWD_LATENT_PAGED_NSTRIDES] = {(int64_t)Hq * kLatentRow, kLatentRow, (int64_t)page_size * kLatentRow,
                                                 kLatentRow, (int64_t)Hq * kLatentDim, kLatentDim, max_pages};
   if (strides) std::memcpy(st, strides, sizeof(st));

@@ -329,7 +329,7 @@ int fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void
   if (dtype != SDPA_F16 && dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
   if (nope != 128 || rot != 64 || Dv != 128) return SDPA_ERR_UNSUPPORTED;
   const int group = Hq / Hkv, D = nope + rot;
-  if (group > kBlockQ || total_k > (1 << 30)) return SDPA_ERR_UNSUPPORTED;
+  if (group > kBlockQ || total_k > (1 << 30) || B > kMaxCount || total_q > kMaxCount) return SDPA_ERR_UNSUPPORTED;
   int64_t st[SDPA_FWD_LATENT_NSTRIDES] = {(int64_t)Hq * D, D, (int64_t)Hkv * nope, nope, rot, (int64_t)Hkv * Dv, Dv, (int64_t)Hq * Dv, Dv};
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < SDPA_FWD_LATENT_NSTRIDES; ++i)
@@ -445,7 +445,7 @@ int sdpa_fwd_paged_fp8(const void* q, const void* k_pool, const void* v_pool, co
 }
 
 size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int max_seqlen_q, int total_k) {
-  return sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, total_k, 128);
+  return B > kMaxCount || total_q > kMaxCount ? 0 : sdpa_fwd_paged_workspace_size(B, Hq, Hkv, total_q, max_seqlen_q, total_k, 128);
 }
 
 int sdpa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_seqlens_q,

@@ -199,7 +199,8 @@ using namespace sdpa;
 extern "C" {
 
 size_t sdpa_cache_resize_workspace_size(int B, int total, int max_pages) {
-  return B < 1 || total < 1 || max_pages < 1 || one_block(B, total, max_pages) ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int4);
+  if (B < 1 || total < 1 || max_pages < 1 || B > kMaxCount || total > kMaxCount) return 0;
+  return one_block(B, total, max_pages) ? 0 : (static_cast<size_t>(B) + 1) * sizeof(int4);
 }
 
 int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t* change, int32_t* free_pages,
@@ -212,6 +213,7 @@ int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t*
   if (B < 1 || total < 1) return SDPA_ERR_INVALID;
   const int rc = page_check(page_size, max_pages, n_pages);
   if (rc != SDPA_OK) return rc;
+  if (B > kMaxCount || total > kMaxCount) return SDPA_ERR_UNSUPPORTED;
   if (table_stride < max_pages) return SDPA_ERR_INVALID;
   const void* words[] = {page_table, kv_len, change, free_pages, n_free, kv_len_out, n_free_out, cu_seqlens, positions};
   for (const void* w : words)

@@ -238,7 +238,7 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
   if (!q || !q_out || !positions || !inv_freq || (Hk > 0 && (!k || !k_out))) return SDPA_ERR_INVALID;
   if (total < 1 || Hq < 1 || Hk < 0 || D < 1 || rotary_dim < 1 || rotary_dim > D || !std::isfinite(factor)) return SDPA_ERR_INVALID;
   if (dtype != SDPA_F16 && dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
-  if (D % 8 != 0 || rotary_dim % (interleaved ? 8 : 16) != 0) return SDPA_ERR_UNSUPPORTED;
+  if (D % 8 != 0 || rotary_dim % (interleaved ? 8 : 16) != 0 || static_cast<long long>(Hq) + Hk > kMaxCount) return SDPA_ERR_UNSUPPORTED;
   int64_t st[SDPA_ROPE_NSTRIDES] = {(int64_t)Hq * D, D, (int64_t)Hk * D, D, (int64_t)Hq * D, D, (int64_t)Hk * D, D};
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < SDPA_ROPE_NSTRIDES; ++i)
@@ -288,7 +288,7 @@ int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64
   const int rc = page_check(page_size, 1, n_pages);
   if (rc != SDPA_OK) return rc;
   if (dtype != SDPA_F16 && dtype != SDPA_BF16) return SDPA_ERR_UNSUPPORTED;
-  if (latent_dim != kLatentDim || rotary_dim != kLatentRot) return SDPA_ERR_UNSUPPORTED;
+  if (latent_dim != kLatentDim || rotary_dim != kLatentRot || total > kMaxCount) return SDPA_ERR_UNSUPPORTED;
   int64_t st[SDPA_LATENT_WRITE_NSTRIDES] = {kLatentDim, kLatentRot, (int64_t)page_size * kLatentRow, kLatentRow};
   if (strides) std::memcpy(st, strides, sizeof(st));
   for (int i = 0; i < SDPA_LATENT_WRITE_NSTRIDES; ++i)

@@ -498,7 +498,8 @@ size_t sdpa_cache_resize_workspace_size(int B, int total, int max_pages);
  * A page belongs to one sequence.  If the free pages do not suffice, a length would be negative or past
  * max_pages * page_size, the new tokens are more than total, or the stack would leave [0, n_pages], the whole call
  * changes nothing: kv_len_out = kv_len, n_free_out = n_free, cu_seqlens = 0, slots = -1, and
- * sdpa_check_device_status() reports SDPA_ERR_INVALID.  page_size: a power of two >= 16.  One or two kernels.
+ * sdpa_check_device_status() reports SDPA_ERR_INVALID.  page_size: a power of two >= 16; B and total <= 2^30.  One or
+ * two kernels.
  */
 int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t* change, int32_t* free_pages,
                       const int32_t* n_free, int32_t* kv_len_out, int32_t* n_free_out, int32_t* cu_seqlens,
@@ -524,7 +525,8 @@ int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t*
  *   factor: finite; multiplies the turned dims (the attention factor of stretched contexts, else 1)
  *   strides: NULL for the contiguous layouts, else 8 element strides {q_s, q_h,  k_s, k_h,  q_out_s, q_out_h,  k_out_s,
  *           k_out_h}, multiples of 8; an input's may be 0 (broadcast), an output's only where there is one token or one
- *           head.  Pointers 16-byte aligned; D a multiple of 8.
+ *           head.  Pointers 16-byte aligned; D a multiple of 8.  Hq + Hk <= 2^30; total * (rotary_dim / 16, interleaved 8, and
+ *           (D - rotary_dim) / 8 where those dims are copied) < 2^31.
  * One kernel.
  */
 int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions, const float* inv_freq,
@@ -550,7 +552,7 @@ int sdpa_rope(const void* q, const void* k, void* q_out, void* k_out, const int3
  *   positions [total] DEVICE int32, inv_freq [rotary_dim / 2], interleaved, factor: as in sdpa_rope; both pointers NULL: the
  *           rotary part is stored as it is
  *   strides: NULL for the contiguous layouts, else 4 element strides {c_s, k_rope_s, pool page, row}, multiples
- *           of 8, the first two may be 0; c, k_rope and pool 16-byte aligned.  page_size: a power of two >= 16.
+ *           of 8, the first two may be 0; c, k_rope and pool 16-byte aligned.  page_size: a power of two >= 16; total <= 2^30.
  * One kernel.
  */
 int sdpa_latent_write(const void* c, const void* k_rope, void* pool, const int64_t* slots, const int32_t* positions,
@@ -590,8 +592,8 @@ size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_
  * kv_len never contribute and may hold anything; the visible rows must be finite.  Queries need not be: a (token, head) with a
  * NaN or +infinity among its scores, in fp32 and times scale * log2(e), has NaN in O and LSE; a score of -infinity is a hidden
  * key's.  Hq <= 128; latent_dim = 512, rotary_dim = 64;
- * page_size a power of two >= 16; pointers 16-byte aligned.  The kernels in `stream`: the plan (which the attention makes
- * itself for up to 256 sequences of few tokens), the attention, and the merge of divided tiles where the workspace
+ * page_size a power of two >= 16; B and total_q <= 2^30; pointers 16-byte aligned.  The kernels in `stream`: the plan (which
+ * the attention makes itself for up to 256 sequences of few tokens), the attention, and the merge of divided tiles where the workspace
  * allows any.
  */
 int sdpa_fwd_latent_paged(const void* q, const void* pool, const int32_t* page_table, const int32_t* kv_len,
@@ -628,7 +630,7 @@ size_t sdpa_fwd_latent_workspace_size(int B, int Hq, int Hkv, int total_q, int m
  *           o_s, o_h}, multiples of 8, not 0 where there are two rows or more (k_nope and v may be views of one expanded tensor)
  *   workspace: see sdpa_fwd_latent_workspace_size; 16-byte aligned.  Calls that overlap on the GPU need separate ones.
  *
- * nope = 128, rotary_dim = 64, Dv = 128; Hq / Hkv <= 128; pointers 16-byte aligned.  Keys and values some sequence owns must be
+ * nope = 128, rotary_dim = 64, Dv = 128; Hq / Hkv <= 128; B, total_q and total_k <= 2^30; pointers 16-byte aligned.  Keys and values some sequence owns must be
  * finite; queries as in sdpa_fwd_latent_paged.  The kernels are those of sdpa_fwd_paged.
  */
 int sdpa_fwd_latent(const void* q, const void* k_nope, const void* k_rope, const void* v, const int32_t* cu_seqlens_q,
