@@ -235,9 +235,10 @@ __global__ void __launch_bounds__(LatentCfg<R>::THREADS, 1)
       if (w.n_blocks == 0) break;
       const int32_t* table = p.page_table + w.b * p.pt_b;
       const int used = (w.sk + p.page_size - 1) >> p.log2_page;  // pages that hold visible rows
-      auto page_of = [&](int j) {  // of this lane's box in block j; outside the pool: zeros
+      auto page_of = [&](int j) {  // of this lane's box in block j; outside the pool: the zeros behind it, for prefetches as well
         const int page = ((w.jb0 + j) * kBlockK + lane * rows) >> p.log2_page;
-        return j < w.n_blocks && lane < nsub && page < used ? __ldg(table + page) : p.n_pages;
+        const int at = j < w.n_blocks && lane < nsub && page < used ? __ldg(table + page) : p.n_pages;
+        return static_cast<unsigned>(at) < static_cast<unsigned>(p.n_pages) ? at : p.n_pages;
       };
       auto row_of = [&](int j) { return ((w.jb0 + j) * kBlockK + lane * rows) & (p.page_size - 1); };
       int next = page_of(0);
