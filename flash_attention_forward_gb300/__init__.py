@@ -852,9 +852,10 @@ def sdpa_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: st
     "linear"    all divided by factor: positions are interpolated;
     "base"      the base raised to base * factor^(rotary_dim / (rotary_dim - 2)), so that the first pair keeps its
                 frequency and the last one is divided by factor;
-    "by_parts"  pairs that turn fast_turns times or more within original_length positions keep their frequency, those
-                that turn slow_turns times or fewer are divided by factor, those between are blended linearly in the
-                index of the pair; the turned dims are multiplied by 0.1 ln(factor) + 1."""
+    "by_parts"  (the method published as YaRN) pairs that turn fast_turns times or more within original_length positions
+                keep their frequency, those that turn slow_turns times or fewer are divided by factor, those between
+                are blended linearly in the index of the pair, from the last whole index before the blend to the first
+                behind it (within 0 and rotary_dim - 1); the turned dims are multiplied by 0.1 ln(factor) + 1."""
     if rotary_dim < 2 or rotary_dim % 2 or not base > 1.0 or not factor >= 1.0:
         raise ValueError("rotary_dim must be even and positive, base above 1, factor at least 1")
     half = torch.arange(rotary_dim // 2, dtype=torch.float64)
@@ -875,8 +876,10 @@ def sdpa_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: st
         def pair(turns):  # index of the pair that turns so often
             return rotary_dim * math.log(original_length / (2 * math.pi * turns)) / (2 * math.log(base))
 
+        # Models that were stretched so have learnt these frequencies, their bounds included: the upper one, twice the
+        # pairs, is only met where even the last pair turns often (10^8 positions and more for a base of 10000)
         lo, hi = max(math.floor(pair(fast_turns)), 0), min(math.ceil(pair(slow_turns)), rotary_dim - 1)
-        stretch = ((half - lo) / max(hi - lo, 0.001)).clamp(0, 1)
+        stretch = ((half - lo) / max(hi - lo, 0.001)).clamp(0, 1)  # ends that meet: a step behind that pair
         inv_freq = inv_freq * (1 - stretch + stretch / factor)
         attention = 0.1 * math.log(factor) + 1.0
     return inv_freq.float(), attention
