@@ -513,8 +513,8 @@ int sdpa_cache_resize(int32_t* page_table, const int32_t* kv_len, const int32_t*
  * sdpa_rope -- rotary positions on queries and keys: pair i of the first rotary_dim dims of every head is turned by
  * the angle positions[t] * inv_freq[i],
  *     (a, b) -> factor * (a cos - b sin, b cos + a sin),
- * in fp32, rounded once; dims rotary_dim .. D - 1 are copied.  The angle is reduced to a fraction of a turn before it is
- * rounded to fp32, which loses 2^-64 of the angle and 2^-64 turns a position.
+ * in fp32, rounded once; dims rotary_dim .. D - 1 are copied.  The angle is reduced to a fraction of a turn, which loses
+ * 2^-64 of the angle and 2^-64 turns a position; the fraction is cut to 2^-32 turns (1.5e-9 of |a| + |b|) and rounded to fp32.
  *
  *   q, q_out [total, Hq, D], k, k_out [total, Hk, D]  dtype (SDPA_F16 or SDPA_BF16); Hk = 0: no k (NULL).  q_out = q and
  *           k_out = k (with the same strides) turn in place; otherwise outputs must not overlap inputs
