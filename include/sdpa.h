@@ -591,7 +591,8 @@ size_t sdpa_fwd_latent_paged_workspace_size(int B, int Hq, int total_q, int max_
  * P is rounded to dtype for the product with the values, row sums take the fp32 probabilities.  Rows of a page at or past
  * kv_len never contribute and may hold anything; the visible rows must be finite.  Queries need not be: a (token, head) with a
  * NaN or +infinity among its scores, in fp32 and times scale * log2(e), has NaN in O and LSE; a score of -infinity is a hidden
- * key's.  Hq <= 128; latent_dim = 512, rotary_dim = 64;
+ * key's.  A score s, times scale * log2(e), enters the exponent with an error of up to 2^-21 s: it is meant to stay well below
+ * 2^21.  Hq <= 128; latent_dim = 512, rotary_dim = 64;
  * page_size a power of two >= 16; B and total_q <= 2^30; pointers 16-byte aligned.  The kernels in `stream`: the plan (which
  * the attention makes itself for up to 256 sequences of few tokens), the attention, and the merge of divided tiles where the workspace
  * allows any.

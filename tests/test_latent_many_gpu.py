@@ -57,3 +57,32 @@ def test_captured_call_of_many_short_sequences():
         torch.cuda.synchronize()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert fa.sdpa_check_device_status() == fa.SDPA_OK
+
+
+def test_two_lists_at_once_and_in_two_graphs():
+    # the list's counter lies in each call's own workspace
+    new, lens = [600, 1, 130, 300, 0, 257, 900, 40], [700, 1, 130, 900, 9, 100, 900, 300]
+    q, k, r, v = packed(new, lens, 80, 80, "bf16", seed=9)
+    cu_q, cu_k = offsets(new).to(DEV), offsets(lens).to(DEV)
+    call = lambda s=None: fa.sdpa_fwd_latent(q, k, r, v, cu_q, cu_k, max(new), scale=0.07, causal=True, stream=s)
+    want = [t.clone() for t in call()]
+    check_expanded(q, k, r, v, new, lens, *want, 0.07, True)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = [call(s) for s in (s1, s2) * 4]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            graphs.append((g, call()))
+    for _ in range(3):
+        for s, (g, out) in zip((s1, s2), graphs):
+            with torch.cuda.stream(s):
+                for t in out:
+                    t.zero_()
+                g.replay()
+    torch.cuda.synchronize()
+    for o, lse in got + [out for _, out in graphs]:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
