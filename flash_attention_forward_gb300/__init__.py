@@ -833,12 +833,14 @@ def sdpa_cache_resize(page_table, kv_len, change, free_pages, n_free, page_size:
         ws, ws_bytes = workspace.data_ptr(), workspace.nbytes
     dev = _current_device(names, given)
     _unit_vectors(names[1:], given[1:])
+    table_stride = max_pages  # of a single contiguous row torch may give any
     if not page_table.is_contiguous():
         _on_device(page_table=page_table)
+        table_stride = page_table.stride(0)
     rc = lib.sdpa_cache_resize(
         page_table.data_ptr(), kv_len.data_ptr(), change.data_ptr(), free_pages.data_ptr(), n_free.data_ptr(),
         kv_len_out.data_ptr(), n_free_out.data_ptr(), cu_seqlens.data_ptr(), positions.data_ptr(), slots.data_ptr(), B, total,
-        int(page_size), max_pages, free_pages.shape[0], page_table.stride(0), ws, ws_bytes, _raw_stream(stream, dev))
+        int(page_size), max_pages, free_pages.shape[0], table_stride, ws, ws_bytes, _raw_stream(stream, dev))
     if rc:
         raise SdpaError("sdpa_cache_resize", rc)
     return kv_len_out, n_free_out, cu_seqlens, positions, slots

@@ -61,3 +61,15 @@ def test_replayed_steps(B):
         check(m, table, kv_len, free, n_free, got[2:], want)
         assert fa.sdpa_check_device_status() == (fa.SDPA_OK if outcomes[-1] else fa.SDPA_ERR_INVALID), (step, outcomes)
     assert any(outcomes) and not all(outcomes)
+
+
+def test_single_row_of_any_stride():
+    # a table of one sequence made by a transpose: contiguous, with a row stride of 1
+    m = Pages(1, 16, 6, 9, 2)
+    _, kv_len, free, n_free = tensors(m)
+    table = torch.full((6, 1), -1, dtype=torch.int32, device="cuda").t()
+    assert table.is_contiguous() and table.stride(0) < 6
+    want = m.resize([50], 50)
+    got = fa.sdpa_cache_resize(table, kv_len, ints([50]), free, n_free, 16, 50, kv_len_out=kv_len, n_free_out=n_free)
+    check(m, table, kv_len, free, n_free, got[2:], want)
+    assert fa.sdpa_check_device_status() == fa.SDPA_OK
